@@ -296,6 +296,207 @@ orbit_status orbit_int4_linear(const void *Xrot, orbit_dtype xrot_dtype, int64_t
                                int64_t N, const void *bias, orbit_dtype bias_dtype,
                                void *out, orbit_dtype out_dtype, hipStream_t stream);
 
+/* ---- What stands between the quantized projections of a block ----------
+ *
+ * The operators a transformer block needs beside its linear layers when it
+ * is served: the norms before and after a branch with its gate and residual
+ * scale, low-rank adapters of many requests beside a shared projection, and
+ * a paged key-value cache (16-bit, or rotate-then-quantize int8) with the
+ * attention of one new token that reads it.  Rows and heads are given by
+ * strides in ELEMENTS; the innermost dimension is contiguous.  Argument
+ * structs are host memory, read only during the call.  Arguments named
+ * "optional" may be NULL.  Sums, norms and softmax statistics are float32.
+ * Unlike the entry points above these accept any alignment their element
+ * type has, unless an argument's comment asks for more. */
+
+#define ORBIT_MAX_ROWS (1LL << 22) /* rows or tokens of one call, exclusive */
+
+typedef enum { ORBIT_NORM_NONE = 0, ORBIT_NORM_RMS = 1, ORBIT_NORM_LAYER = 2 } orbit_norm;
+
+/* Norms around a residual sum, one pass over the rows:
+ *   b^ = post(branch) * post_weight          (branch itself: post NONE)
+ *   r  = residual_scale * x + gate[g] * b^    (x itself: no branch)
+ *   y  = norm(r) * weight * (1 + scale[g]) + shift[g]
+ * with rms(v) = v / sqrt(mean v^2 + eps), layer(v) = (v - mean v) /
+ * sqrt(mean (v - mean v)^2 + eps) over the row, g = group_ids[row], or
+ * floor(row / ceil(rows / groups)) where group_ids is NULL.  norm(r) is
+ * taken of r before it is rounded to x's type.  An id outside 0 ..
+ * groups - 1 leaves its row without modulation (gate 1, scale and shift 0).
+ * x: [rows, dim] F32, BF16 or F16.  branch: [rows, dim] (optional), of x's
+ * type, or any type where x is F32.  r_out: [rows, dim] of x's type,
+ * required with a branch, unused without one.  y_out: [rows, dim], unused
+ * (may be NULL) where norm is NONE; its type is x's, or any where x is F32.
+ * weight, post_weight: [dim]; gate, scale, shift: [groups, dim] by row
+ * strides (chunks of one projection's output are such rows); all optional,
+ * all of p_dtype (F32, BF16 or F16).  r_out may be x itself and y_out may be
+ * x or branch itself (same pointer, stride and type); otherwise outputs
+ * alias nothing.  1 <= dim <= ORBIT_MAX_D; 0 <= rows <
+ * ORBIT_MAX_ROWS.
+ * Errors: ORBIT_E_ARG (null or misaligned pointers, nothing to compute, eps
+ * negative or not finite, bad enum), ORBIT_E_SHAPE, ORBIT_E_DTYPE,
+ * ORBIT_E_HIP. */
+typedef struct {
+  const void *x, *branch;
+  void *r_out, *y_out;
+  const void *weight, *post_weight, *gate, *scale, *shift;
+  const int32_t *group_ids;
+  int64_t x_stride, branch_stride, r_stride, y_stride;
+  int64_t gate_stride, scale_stride, shift_stride;
+  int64_t rows, dim, groups;
+  int32_t x_dtype, branch_dtype, y_dtype, p_dtype; /* orbit_dtype */
+  int32_t norm, post;                              /* orbit_norm */
+  float residual_scale, eps;
+} orbit_block_norm_args;
+
+orbit_status orbit_block_norm(const orbit_block_norm_args *args, hipStream_t stream);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   out[m] = y[m] + scale[a] * B[a] (A[a] x[m]),  a = ids[m],
+ * the sums over the adapter's first ranks[a] rows; out[m] = y[m] where a is
+ * outside 0 .. adapters - 1 (-1 by convention) or ranks[a] is 0.  y is what
+ * the shared projection gave (any layer of this library).  Because
+ * W x = (W Pi^T)(Pi x), an adapter whose A was rotated once (A Pi^T:
+ * orbit_rotate on A's rows) reads the same rotated activations x' as the
+ * weight-only layers.
+ * x: [M, K] BF16 or F16, rows 16-byte aligned; A: [adapters, rank, K] and
+ * B: [adapters, N, rank] contiguous, 16-byte aligned, of x's type; values
+ * past an adapter's own rank are never used.  ids: int32 [M].  ranks: int32
+ * [adapters], optional (all `rank`; values are clamped to 0 .. rank).
+ * scale: float [adapters], optional (all 1).  y, out: [M, N] F32, BF16 or
+ * F16, out may be y itself (same pointer and stride).
+ * K a multiple of 8, 8 <= K <= 65536; rank a multiple of 8, 8 <= rank <= 128;
+ * 0 <= M < ORBIT_MAX_ROWS, 0 <= N <= 2^22.
+ * workspace: device, 16-byte aligned, orbit_adapter_workspace(M, K, rank)
+ * bytes, overwritten; it holds A x, in float32, as partial sums over K.
+ * Errors: ORBIT_E_ARG, ORBIT_E_SHAPE, ORBIT_E_DTYPE, ORBIT_E_HIP. */
+typedef struct {
+  const void *x, *A, *B, *y;
+  void *out;
+  const int32_t *ids, *ranks;
+  const float *scale;
+  void *workspace;
+  int64_t workspace_bytes;
+  int64_t x_stride, y_stride, out_stride;
+  int64_t M, K, N, adapters, rank;
+  int32_t x_dtype, y_dtype; /* orbit_dtype */
+} orbit_adapter_args;
+
+orbit_status orbit_adapter_add(const orbit_adapter_args *args, hipStream_t stream);
+
+/* Bytes of orbit_adapter_add's workspace; -1 for invalid sizes.  Host only. */
+int64_t orbit_adapter_workspace(int64_t M, int64_t K, int64_t rank);
+
+/* A paged key-value cache.  k, v: device [pages, kv_heads, page_size,
+ * head_dim], contiguous, 16-byte aligned, of type `format`: ORBIT_KV_BF16 /
+ * ORBIT_KV_F16 hold the values; ORBIT_KV_INT8 holds codes, symmetric in
+ * [-127, 127] with one fp16 scale per (token, head), scale =
+ * fp16(max|x| / 127), code = round_half_even(x / scale) (0 where scale is
+ * 0): the group format of orbit_int8_pack_weights with group = head_dim.
+ * k_scale, v_scale: device uint16 (fp16 bits) [pages, kv_heads, page_size],
+ * INT8 only, 16-byte aligned.  page_size a power of two, 1 .. 1024 (INT8: 4
+ * .. 1024); head_dim a multiple of 8 (INT8: 16), 8 .. 256; 1 <= kv_heads <=
+ * 1024; pages * page_size < 2^31.  Token `slot` of the cache is position
+ * slot % page_size of page slot / page_size. */
+typedef enum { ORBIT_KV_BF16 = 1, ORBIT_KV_F16 = 2, ORBIT_KV_INT8 = 3 } orbit_kv_format;
+
+typedef struct {
+  void *k, *v;
+  void *k_scale, *v_scale;
+  int64_t pages;
+  int32_t page_size, kv_heads, head_dim, format; /* orbit_kv_format */
+} orbit_kv_cache;
+
+/* Appends one key and one value per token and head to the cache, the
+ * position rotation (and for a rotated cache the Hadamard rotation) applied
+ * on the way; queries given along are rotated alike.
+ *   position rotation of the first rot_dim coordinates, pairs (a, b) =
+ *   (x[i], x[i + rot_dim/2]), or (x[2i], x[2i + 1]) where interleaved:
+ *   a' = a cos - b sin, b' = a sin + b cos, with cos = cos_sin[p][i], sin =
+ *   cos_sin[p][rot_dim/2 + i], p = positions[token]  (no table: no rotation);
+ *   then, where hadamard is set, H_head_dim / sqrt(head_dim) (Sylvester
+ *   order) on keys and queries: orthogonal, so q' . k' = q . k, while a
+ *   key's outlier channels are spread before they are coded (OrbitQuant
+ *   page, Method: rotate, then quantize; here between the position rotation
+ *   and the cache, where no weight can absorb it).  Values are stored as
+ *   given (a rotation of theirs can be absorbed into the projections).
+ * k, v: [tokens, kv_heads, head_dim] by token and head strides, q (optional,
+ * with q_out): [tokens, q_heads, head_dim]; all of in_dtype, F32, BF16 or
+ * F16.  q_out: like q, contiguous, of in_dtype, not q itself.  slots: int64
+ * [tokens]; a slot outside the cache (-1 by convention) stores nothing.  Slots
+ * that are stored to must differ: what is kept of two tokens with the same
+ * slot is unspecified.  positions: int64 [tokens];
+ * a token whose position is outside the table stores nothing and its queries
+ * are NaN.  cos_sin: float [table_len, rot_dim].  rot_dim even, 0 ..
+ * head_dim; hadamard needs a head_dim of 8, 16, 32, 64, 128 or 256.
+ * 0 <= tokens < ORBIT_MAX_ROWS.
+ * Errors: ORBIT_E_ARG, ORBIT_E_SHAPE, ORBIT_E_DTYPE, ORBIT_E_HIP. */
+typedef struct {
+  orbit_kv_cache cache;
+  const void *k, *v, *q;
+  void *q_out;
+  const int64_t *slots, *positions;
+  const float *cos_sin;
+  int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  int64_t q_token_stride, q_head_stride;
+  int64_t tokens, q_heads, table_len;
+  int32_t rot_dim, in_dtype, interleaved, hadamard;
+} orbit_kv_append_args;
+
+orbit_status orbit_kv_append(const orbit_kv_append_args *args, hipStream_t stream);
+
+/* Reads tokens of the cache back to dense rows, the inverse of the append:
+ * k_out[t], v_out[t] = the values (int8: code * scale, rounded once) of
+ * token slots[t], zeros where that slot is outside the cache.  k_out, v_out:
+ * [tokens, kv_heads, head_dim] contiguous, F32, BF16 or F16, 16-byte
+ * aligned; tokens as in orbit_kv_append, tokens * kv_heads * head_dim <
+ * 2^35.  A prompt's attention reads its prefix this way.
+ * Errors: ORBIT_E_ARG, ORBIT_E_SHAPE, ORBIT_E_DTYPE, ORBIT_E_HIP. */
+orbit_status orbit_kv_read(const orbit_kv_cache *cache, const int64_t *slots, int64_t tokens,
+                           void *k_out, void *v_out, orbit_dtype out_dtype, hipStream_t stream);
+
+/* Attention of one new token per request over the paged cache:
+ *   out[b, h] = sum_t softmax_t(sm_scale * q[b, h] . k[t]) v[t]
+ * over max(0, len - window) <= t < len (window 0: from the first token),
+ * len = lengths[b], with the keys and values of head h / (q_heads /
+ * kv_heads).  Token t of request b lies in page block_table[b][t /
+ * page_size].  A row with nothing to see (len <= 0) gives out = 0, lse =
+ * -inf; lengths past table_width * page_size are cut there, and a table
+ * entry outside the cache hides its page's tokens.  What lies in the cache
+ * outside the seen tokens is never used.
+ * q: [batch, q_heads, head_dim] by strides, rows 16-byte aligned, BF16 or
+ * F16; its type is the cache's, either one for an int8 cache.  out: [batch,
+ * q_heads, head_dim] contiguous, of q's type, 16-byte aligned.  lse: float
+ * [batch, q_heads], optional: the log of the softmax's denominator, by which
+ * parts of a longer context can be joined.  block_table: int32 [batch,
+ * table_width] by row stride.  q_heads a multiple of kv_heads; batch <=
+ * 65535; sm_scale finite; 0 <= window <= 2^30, table_width * page_size <=
+ * 2^30.
+ * workspace: device, 16-byte aligned, orbit_paged_attention_workspace bytes
+ * (may be 0), overwritten: partial outputs of the pieces that a long context
+ * is split into.
+ * Errors: ORBIT_E_ARG, ORBIT_E_SHAPE, ORBIT_E_DTYPE, ORBIT_E_HIP. */
+typedef struct {
+  orbit_kv_cache cache;
+  const void *q;
+  void *out;
+  float *lse;
+  const int32_t *block_table, *lengths;
+  void *workspace;
+  int64_t workspace_bytes;
+  int64_t q_batch_stride, q_head_stride, table_stride;
+  int64_t batch, q_heads, table_width, window;
+  float sm_scale;
+  int32_t q_dtype;
+} orbit_paged_attention_args;
+
+orbit_status orbit_paged_attention(const orbit_paged_attention_args *args, hipStream_t stream);
+
+/* Bytes of orbit_paged_attention's workspace for these sizes on the current
+ * device; -1 for invalid sizes or if the device cannot be asked. */
+int64_t orbit_paged_attention_workspace(int64_t batch, int64_t q_heads, int64_t kv_heads,
+                                        int64_t head_dim, int64_t page_size,
+                                        int64_t table_width, int64_t window);
+
 #ifdef __cplusplus
 }
 #endif

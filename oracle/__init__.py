@@ -57,6 +57,8 @@ from .orbit import (quantize_codes, boundary_band, pack_indices, unpack_indices,
                     gelu_erf)
 from .int8 import int8_pack, int8_dequant, int8_linear
 from .int4 import int4_pack, int4_dequant, int4_linear, pack_nibbles, unpack_nibbles
+from .block import (row_norm, block_norm, adapter_add, turn, hadamard_heads, kv_codes,
+                    paged_attention)
 
 __all__ = [
     "bf16_bits_to_f64", "f64_to_bf16_bits", "f16_bits_to_f64", "f64_to_f16_bits",
@@ -67,5 +69,6 @@ __all__ = [
     "pack_indices", "unpack_indices", "pack_weights", "quant_act",
     "qlinear_codes", "qlinear_unquantized", "gelu_erf", "int8_pack",
     "int8_dequant", "int8_linear", "int4_pack", "int4_dequant", "int4_linear",
-    "pack_nibbles", "unpack_nibbles",
+    "pack_nibbles", "unpack_nibbles", "row_norm", "block_norm", "adapter_add", "turn",
+    "hadamard_heads", "kv_codes", "paged_attention",
 ]

@@ -14,11 +14,18 @@ applied online to activations (x' = Pi x, split into ||x'|| and a coded unit
 direction); the product of the two coded factors approximates W x with no
 inverse rotation.  Also: the int8 per-group rotated weight-only path of the
 int8 article (section 4) and its 4-bit sibling (int4 codes, two per byte).
+
+Between those layers: norms around a branch with its gate and residual scale
+(block_norm), low-rank adapters of many requests beside a shared projection
+(adapter_add), and a paged key-value cache, 16-bit or rotate-then-quantize
+int8 (kv_append, kv_read), with the attention of one new token that reads it
+(paged_attention).
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -27,6 +34,7 @@ __all__ = [
     "OrbitError", "Codebook", "Rotation", "fit_codebook", "pack_weights",
     "quant_act", "qlinear", "rotate", "int8_pack_weights", "int8_linear",
     "int4_pack_weights", "int4_linear",
+    "block_norm", "adapter_add", "kv_append", "kv_read", "paged_attention",
     "packed_row_bytes", "LIB_PATH",
 ]
 
@@ -81,6 +89,13 @@ def _load():
                                P, ctypes.c_int, P], ctypes.c_int),
         "orbit_int4_linear": ([P, ctypes.c_int, I64, I64, P, P, I32, I64, P, ctypes.c_int,
                                P, ctypes.c_int, P], ctypes.c_int),
+        "orbit_block_norm": ([P, P], ctypes.c_int),
+        "orbit_adapter_add": ([P, P], ctypes.c_int),
+        "orbit_adapter_workspace": ([I64, I64, I64], I64),
+        "orbit_kv_append": ([P, P], ctypes.c_int),
+        "orbit_kv_read": ([P, P, I64, P, P, ctypes.c_int, P], ctypes.c_int),
+        "orbit_paged_attention": ([P, P], ctypes.c_int),
+        "orbit_paged_attention_workspace": ([I64] * 7, I64),
     }
     for name, (args, res) in sig.items():
         try:
@@ -304,3 +319,343 @@ def int4_linear(xrot: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, group:
                                  N, _ptr(bias), bias_dt, _ptr(out), _DT[out.dtype],
                                  _stream(xrot.device)), "orbit_int4_linear")
     return out
+
+
+# ---- what stands between the quantized projections of a block ---------------
+#
+# Tensors of these functions may be strided rows or heads: only the innermost
+# dimension has to be contiguous.  Argument structs of include/orbit.h are
+# packed field by field ("@": the C compiler's own layout).
+
+_NORMS = {None: 0, "rms": 1, "layer": 2}
+_KV_FORMATS = {torch.bfloat16: 1, torch.float16: 2, torch.int8: 3}
+_NORM_ARGS = struct.Struct("@10P10q6i2f")
+_ADAPTER_ARGS = struct.Struct("@9P9q2i")
+_CACHE = struct.Struct("@4Pq4i")
+_APPEND_ARGS = struct.Struct("@4Pq4i7P9q4i")
+_ATTENTION_ARGS = struct.Struct("@4Pq4i6P8qfi")
+
+
+def _view(t, name, dims, device, dtype=None):
+    """Checks a GPU tensor of `dims` dimensions whose innermost is contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise OrbitError(f"{name} must be a torch tensor on a GPU")
+    if t.dim() != dims:
+        raise OrbitError(f"{name} must have {dims} dimension{'s' if dims > 1 else ''}")
+    if t.device != device:
+        raise OrbitError(f"{name} must be on {device}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
+        raise OrbitError(f"{name}'s innermost dimension must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise OrbitError(f"{name} must be {dtype}")
+    return t
+
+
+def _dtype(t, name):
+    try:
+        return _DT[t.dtype]
+    except KeyError:
+        raise OrbitError(f"{name} must be float32, bfloat16 or float16") from None
+
+
+def _shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise OrbitError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _gpu(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise OrbitError(f"{name} must be a torch tensor on a GPU")
+    return t.device
+
+
+def _launch(fn, what, device, *args):
+    """Calls the library on the current stream of `device`, with that device current."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status:
+        _check(status, what)
+
+
+def block_norm(x, branch=None, *, weight=None, norm="rms", post=None, post_weight=None,
+               gate=None, scale=None, shift=None, groups=None, residual_scale=1.0, eps=1e-6,
+               out_dtype=None, r_out=None, out=None):
+    """The norms around a residual sum, in one pass over the rows:
+
+        b^ = post(branch) * post_weight                (post None: branch)
+        r  = residual_scale * x + gate[g] * b^         (no branch: x)
+        y  = norm(r) * weight * (1 + scale[g]) + shift[g]
+
+    norm and post: "rms", "layer" or None.  Returns (r, y) with a branch, y
+    without one, r where norm is None.  x, branch: [rows, dim] (branch of x's
+    dtype, any where x is float32); weight, post_weight: [dim]; gate, scale,
+    shift: [G, dim], rows of any stride (chunks of an AdaLN projection's
+    output); all five of one dtype.  Row m belongs to group groups[m] (int32
+    [rows]; an id outside 0 .. G - 1: no modulation), or, without groups, to
+    m // ceil(rows / G).  r has x's dtype, y out_dtype (x's; any where x is
+    float32).  r_out may be x; out may be x or branch.
+    """
+    dev = _gpu(x, "x")
+    _view(x, "x", 2, dev)
+    M, D = x.shape
+    xt = _dtype(x, "x")
+    if norm not in _NORMS or post not in _NORMS:
+        raise OrbitError(f"norm and post must be 'rms', 'layer' or None, got {norm!r}, {post!r}")
+    if branch is None and norm is None:
+        raise OrbitError("block_norm needs a branch, a norm, or both")
+    if branch is None and (post is not None or post_weight is not None or gate is not None or r_out is not None):
+        raise OrbitError("post, post_weight, gate and r_out need a branch")
+    if norm is None and (weight is not None or scale is not None or shift is not None or out is not None):
+        raise OrbitError("weight, scale, shift and out need a norm")
+    bt, bp, bs, r, rs = 0, 0, 0, None, 0
+    if branch is not None:
+        _view(branch, "branch", 2, dev)
+        _shape(branch, "branch", (M, D))
+        bt, bp, bs = _dtype(branch, "branch"), branch.data_ptr(), branch.stride(0)
+        r = torch.empty((M, D), dtype=x.dtype, device=dev) if r_out is None else _view(r_out, "r_out", 2, dev, x.dtype)
+        _shape(r, "r_out", (M, D))
+        rs = r.stride(0)
+    y, yt, ys = None, 0, 0
+    if norm is not None:
+        if out is None:
+            y = torch.empty((M, D), dtype=out_dtype or x.dtype, device=dev)
+        else:
+            y = _view(out, "out", 2, dev, out_dtype)
+            _shape(y, "out", (M, D))
+        yt, ys = _dtype(y, "out"), y.stride(0)
+    pt, ptrs, strides, G = None, [], [], None
+    for t, name, dims in ((weight, "weight", 1), (post_weight, "post_weight", 1), (gate, "gate", 2),
+                          (scale, "scale", 2), (shift, "shift", 2)):
+        if t is None:
+            ptrs.append(0)
+            strides.append(0)
+            continue
+        _view(t, name, dims, dev)
+        if pt is None:
+            pt = t.dtype
+        elif t.dtype != pt:
+            raise OrbitError("weight, post_weight, gate, scale and shift must share one dtype")
+        if dims == 2:
+            G = t.shape[0] if G is None else G
+            if G == 0:
+                raise OrbitError(f"{name} must have a row")
+            _shape(t, name, (G, D))
+        else:
+            _shape(t, name, (D,))
+        ptrs.append(t.data_ptr())
+        strides.append(t.stride(0))
+    if pt is not None and pt not in _DT:
+        raise OrbitError("weight, post_weight, gate, scale and shift must be float32, bfloat16 or float16")
+    gp = 0
+    if groups is not None:
+        _view(groups, "groups", 1, dev, torch.int32)
+        _shape(groups, "groups", (M,))
+        gp = groups.data_ptr()
+    if M == 0:  # an empty branch has no address to tell it from none
+        return y if r is None else r if y is None else (r, y)
+    _launch(lib.orbit_block_norm, "orbit_block_norm", dev, _NORM_ARGS.pack(
+        x.data_ptr(), bp, 0 if r is None else r.data_ptr(), 0 if y is None else y.data_ptr(), *ptrs, gp,
+        x.stride(0), bs, rs, ys, *strides[2:], M, D, G or 1, xt, bt, yt, _DT.get(pt, 0), _NORMS[norm],
+        _NORMS[post], residual_scale, eps))
+    return y if r is None else r if y is None else (r, y)
+
+
+def adapter_add(y, x, A, B, ids, *, scale=None, ranks=None, out=None):
+    """Low-rank adapters of many requests beside a shared projection:
+
+        out[m] = y[m] + scale[a] * B[a] (A[a] x[m]),  a = ids[m]
+
+    over the first ranks[a] rows of A[a]; out[m] = y[m] where a is outside
+    0 .. adapters - 1 (-1 by convention).  y: [M, N], the shared projection's
+    output; x: [M, K] bfloat16 or float16; A: [adapters, R, K] and B:
+    [adapters, N, R] of x's dtype, R a multiple of 8 up to 128; ids: int32
+    [M]; scale: float32 [adapters]; ranks: int32 [adapters].  Next to the
+    weight-only layers x is the rotated x' they read, with A rotated once:
+    rotate(rot, A.view(-1, K)).  out may be y.
+    """
+    dev = _gpu(x, "x")
+    _view(x, "x", 2, dev)
+    _view(y, "y", 2, dev)
+    M, K = x.shape
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise OrbitError("x must be bfloat16 or float16")
+    _view(A, "A", 3, dev, x.dtype)
+    _view(B, "B", 3, dev, x.dtype)
+    if not A.is_contiguous() or not B.is_contiguous():
+        raise OrbitError("A and B must be contiguous")
+    L, R, N = A.shape[0], A.shape[1], y.shape[1]
+    _shape(y, "y", (M, N))
+    _shape(A, "A", (L, R, K))
+    _shape(B, "B", (L, N, R))
+    _view(ids, "ids", 1, dev, torch.int32)
+    _shape(ids, "ids", (M,))
+    for t, name, dt in ((scale, "scale", torch.float32), (ranks, "ranks", torch.int32)):
+        if t is not None:
+            _view(t, name, 1, dev, dt)
+            _shape(t, name, (L,))
+    if out is None:
+        out = torch.empty((M, N), dtype=y.dtype, device=dev)
+    else:
+        _view(out, "out", 2, dev, y.dtype)
+        _shape(out, "out", (M, N))
+    ws = lib.orbit_adapter_workspace(M, K, R)
+    if ws < 0:
+        raise OrbitError(f"orbit_adapter_add: invalid shape (M {M}, K {K}, rank {R})")
+    work = torch.empty((ws,), dtype=torch.uint8, device=dev)
+    _launch(lib.orbit_adapter_add, "orbit_adapter_add", dev, _ADAPTER_ARGS.pack(
+        x.data_ptr(), A.data_ptr(), B.data_ptr(), y.data_ptr(), out.data_ptr(), ids.data_ptr(),
+        0 if ranks is None else ranks.data_ptr(), 0 if scale is None else scale.data_ptr(),
+        work.data_ptr(), ws, x.stride(0), y.stride(0), out.stride(0), M, K, N, L, R, _DT[x.dtype],
+        _dtype(y, "y")))
+    return out
+
+
+def _cache_fields(k_cache, v_cache, k_scale, v_scale, dev):
+    """The fields of orbit_kv_cache: caches [pages, heads, page size, head dim]."""
+    _view(k_cache, "k_cache", 4, dev)
+    _view(v_cache, "v_cache", 4, dev, k_cache.dtype)
+    _shape(v_cache, "v_cache", k_cache.shape)
+    if not k_cache.is_contiguous() or not v_cache.is_contiguous():
+        raise OrbitError("k_cache and v_cache must be contiguous")
+    fmt = _KV_FORMATS.get(k_cache.dtype)
+    if fmt is None:
+        raise OrbitError("k_cache and v_cache must be bfloat16, float16 or int8")
+    pages, heads, page, dim = k_cache.shape
+    sp = (0, 0)
+    if fmt == 3:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None:
+                raise OrbitError("an int8 cache needs k_scale and v_scale")
+            _view(t, name, 3, dev, torch.float16)
+            _shape(t, name, (pages, heads, page))
+            if not t.is_contiguous():
+                raise OrbitError(f"{name} must be contiguous")
+        sp = (k_scale.data_ptr(), v_scale.data_ptr())
+    elif k_scale is not None or v_scale is not None:
+        raise OrbitError("k_scale and v_scale belong to an int8 cache")
+    return (k_cache.data_ptr(), v_cache.data_ptr(), *sp, pages, page, heads, dim, fmt)
+
+
+def kv_append(k, v, k_cache, v_cache, slots, *, positions=None, cos_sin=None, interleaved=False,
+              q=None, q_out=None, k_scale=None, v_scale=None, hadamard=False):
+    """Appends a key and a value per token and head to the paged cache, the
+    position rotation (and, with hadamard, the orthonormal Hadamard rotation
+    of each head) applied to keys on the way, and to the queries if given.
+
+    k, v: [tokens, kv_heads, dim], q: [tokens, q_heads, dim], views of one
+    projection's output for instance.  k_cache, v_cache: [pages, kv_heads,
+    page_size, dim], bfloat16, float16, or int8 with k_scale, v_scale float16
+    [pages, kv_heads, page_size].  slots: int64 [tokens], page * page_size +
+    offset; a slot outside the cache (-1) stores nothing.  cos_sin: float32
+    [positions, rot_dim], cosines then sines; positions: int64 [tokens].
+    Returns the rotated queries (None without q).
+    """
+    dev = _gpu(k, "k")
+    _view(k, "k", 3, dev)
+    _view(v, "v", 3, dev, k.dtype)
+    cache = _cache_fields(k_cache, v_cache, k_scale, v_scale, dev)
+    T = k.shape[0]
+    heads, dim = cache[6], cache[7]
+    _shape(k, "k", (T, heads, dim))
+    _shape(v, "v", (T, heads, dim))
+    _view(slots, "slots", 1, dev, torch.int64)
+    _shape(slots, "slots", (T,))
+    cp, pp, P, rot = 0, 0, 0, 0
+    if cos_sin is not None:
+        _view(cos_sin, "cos_sin", 2, dev, torch.float32)
+        if not cos_sin.is_contiguous():
+            raise OrbitError("cos_sin must be contiguous")
+        if positions is None:
+            raise OrbitError("cos_sin needs positions")
+        _view(positions, "positions", 1, dev, torch.int64)
+        _shape(positions, "positions", (T,))
+        if not cos_sin.shape[0]:
+            raise OrbitError("cos_sin must have a row")
+        cp, pp, (P, rot) = cos_sin.data_ptr(), positions.data_ptr(), cos_sin.shape
+    qp, qo, qs, H = 0, 0, (0, 0), 0
+    if q is not None:
+        _view(q, "q", 3, dev, k.dtype)
+        H = q.shape[1]
+        _shape(q, "q", (T, H, dim))
+        if q_out is None:
+            q_out = torch.empty((T, H, dim), dtype=q.dtype, device=dev)
+        else:
+            _view(q_out, "q_out", 3, dev, q.dtype)
+            _shape(q_out, "q_out", (T, H, dim))
+            if not q_out.is_contiguous():
+                raise OrbitError("q_out must be contiguous")
+        qp, qo, qs = q.data_ptr(), q_out.data_ptr(), q.stride()
+    elif q_out is not None:
+        raise OrbitError("q_out needs q")
+    ks, vs = k.stride(), v.stride()
+    _launch(lib.orbit_kv_append, "orbit_kv_append", dev, _APPEND_ARGS.pack(
+        *cache, k.data_ptr(), v.data_ptr(), qp, qo, slots.data_ptr(), pp, cp, ks[0], ks[1], vs[0],
+        vs[1], qs[0], qs[1], T, H, P, rot, _dtype(k, "k"), bool(interleaved), bool(hadamard)))
+    return q_out
+
+
+def kv_read(k_cache, v_cache, slots, *, k_scale=None, v_scale=None, dtype=None):
+    """The keys and values of the tokens at `slots` (int64 [tokens]) as dense
+    rows [tokens, kv_heads, dim] of `dtype` (default: the cache's; float16 for
+    int8); zeros where a slot lies outside the cache."""
+    dev = _gpu(k_cache, "k_cache")
+    cache = _cache_fields(k_cache, v_cache, k_scale, v_scale, dev)
+    _view(slots, "slots", 1, dev, torch.int64)
+    if dtype is None:
+        dtype = torch.float16 if k_cache.dtype == torch.int8 else k_cache.dtype
+    if dtype not in _DT:
+        raise OrbitError("dtype must be float32, bfloat16 or float16")
+    k = torch.empty((slots.shape[0], cache[6], cache[7]), dtype=dtype, device=dev)
+    v = torch.empty_like(k)
+    _launch(lib.orbit_kv_read, "orbit_kv_read", dev, _CACHE.pack(*cache), slots.data_ptr(),
+            slots.shape[0], k.data_ptr(), v.data_ptr(), _DT[dtype])
+    return k, v
+
+
+def paged_attention(q, k_cache, v_cache, block_table, lengths, *, scale=None, window=0,
+                    k_scale=None, v_scale=None, out=None, return_lse=False):
+    """Attention of one new token per request over the paged cache.
+
+    q: [batch, q_heads, dim] bfloat16 or float16 (the cache's dtype, either
+    for int8); block_table: int32 [batch, width], the pages of each request;
+    lengths: int32 [batch], the tokens each sees (0: the output is 0, its lse
+    -inf).  Head h reads the keys of head h // (q_heads // kv_heads).  scale:
+    1 / sqrt(dim) by default.  window > 0: the last `window` tokens alone.
+    Returns out [batch, q_heads, dim], with return_lse also lse float32
+    [batch, q_heads].
+    """
+    dev = _gpu(q, "q")
+    _view(q, "q", 3, dev)
+    cache = _cache_fields(k_cache, v_cache, k_scale, v_scale, dev)
+    batch, H, dim = q.shape
+    if dim != cache[7]:
+        raise OrbitError(f"q's heads have dimension {dim}, the cache's {cache[7]}")
+    _view(block_table, "block_table", 2, dev, torch.int32)
+    _view(lengths, "lengths", 1, dev, torch.int32)
+    _shape(lengths, "lengths", (batch,))
+    if block_table.shape[0] != batch:
+        raise OrbitError("block_table must have a row per request")
+    if out is None:
+        out = torch.empty((batch, H, dim), dtype=q.dtype, device=dev)
+    else:
+        _view(out, "out", 3, dev, q.dtype)
+        _shape(out, "out", (batch, H, dim))
+        if not out.is_contiguous():
+            raise OrbitError("out must be contiguous")
+    lse = torch.empty((batch, H), dtype=torch.float32, device=dev) if return_lse else None
+    width = block_table.shape[1]
+    ws = lib.orbit_paged_attention_workspace(batch, H, cache[6], dim, cache[5], width, window)
+    if ws < 0:
+        raise OrbitError(f"orbit_paged_attention: invalid shape (batch {batch}, {H} query heads on "
+                         f"{cache[6]}, dim {dim}, window {window})")
+    work = torch.empty((ws,), dtype=torch.uint8, device=dev) if ws else None
+    _launch(lib.orbit_paged_attention, "orbit_paged_attention", dev, _ATTENTION_ARGS.pack(
+        *cache, q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        block_table.data_ptr(), lengths.data_ptr(), 0 if work is None else work.data_ptr(), ws,
+        q.stride(0), q.stride(1), block_table.stride(0), batch, H, width, window,
+        dim ** -0.5 if scale is None else scale, _dtype(q, "q")))
+    return (out, lse) if return_lse else out

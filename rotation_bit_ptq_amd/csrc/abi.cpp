@@ -7,15 +7,11 @@
 
 #include "orbit_internal.h"
 
+using orbit::hip_status;
+
 namespace {
 
 thread_local int g_last_hip_error = 0;
-
-orbit_status hip_status(hipError_t e) {
-  if (e == hipSuccess) return ORBIT_OK;
-  g_last_hip_error = (int)e;
-  return ORBIT_E_HIP;
-}
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
@@ -150,6 +146,12 @@ orbit_status group_linear(int kind, const void* Xrot, orbit_dtype xrot_dtype, in
 }  // namespace
 
 namespace orbit {
+
+orbit_status hip_status(hipError_t e) {
+  if (e == hipSuccess) return ORBIT_OK;
+  g_last_hip_error = (int)e;
+  return ORBIT_E_HIP;
+}
 
 hipError_t device_info(DeviceInfo* out) {
   static std::atomic<int> lds_cache[64];

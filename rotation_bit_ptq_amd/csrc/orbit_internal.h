@@ -16,6 +16,10 @@ struct DeviceInfo {
 };
 hipError_t device_info(DeviceInfo* out);
 
+// The status of a HIP call; a failure's code is kept for
+// orbit_last_hip_error.
+orbit_status hip_status(hipError_t e);
+
 // One launch site's cached setup: the dynamic-LDS limit raised once per
 // device, and the occupancy for the last LDS size asked about.
 struct LaunchCache {

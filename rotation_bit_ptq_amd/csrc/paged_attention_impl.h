@@ -1,0 +1,507 @@
+// Attention of one new token per request over the paged cache
+// (orbit_paged_attention):
+//   o = sum_t p_t v_t / sum_t p_t,  p_t = exp(sm_scale q . k_t - m),
+// the maximum m and the sums carried along the tokens (one pass over the
+// cache).
+//
+// Bound: memory; per byte of a 16-bit cache there are 2 (q_heads / kv_heads)
+// multiply-adds.
+//
+// Split.  A workgroup of four waves takes one key head of one request, up to
+// 16 of the query heads that share it, and `chunk` tokens; wave w takes the
+// tiles of 32 tokens w, w + 4, ... with sums of its own, so no barrier
+// stands between two tiles.  The waves' sums meet once in LDS.  Contexts of
+// more than one chunk leave partial sums in the workspace, which a second
+// kernel joins in a fixed order.
+//
+// Products on the matrix cores (16x16x32), also for a single query head: the
+// unused rows cost nothing that bounds the kernel.
+//   S^T = K Q^T: A = 16 tokens x 32 coordinates straight from memory (a
+//   lane's 16 contiguous bytes of a key are an operand), B = the queries,
+//   kept in registers.  A lane then holds head l % 16 and tokens 4 (l / 16)
+//   + i of each half tile.
+//   O^T = V^T P^T: those lanes' probabilities are the B operand as they
+//   stand if operand slot 8 g + j means token 4 g + j of the first half
+//   (j < 4) or 4 g + j - 4 of the second.  A = V^T needs four tokens of one
+//   coordinate side by side: values go through the wave's own LDS rows and
+//   come back by the transposing read (ds_read_b64_tr_b16).
+// Probabilities are multiplied as hi + lo pairs of 16-bit numbers (two
+// products), so no accuracy is lost to the operand type.
+//
+// INT8 cache: codes become fp16 integers exactly (a byte permute and one
+// packed subtraction).  A key's scale multiplies its score.  A value's scale
+// goes into its probability, with the running maximum taken of z_t +
+// log2(scale_t), so that the products stay in [0, 1] whatever the scales'
+// size.  Queries are scaled by a power of two per head to fit fp16.
+#pragma once
+
+#include "kv_cache.h"
+
+namespace orbit {
+namespace block {
+
+struct AttentionArgs {
+  Cache c;
+  const char* q;
+  char* out;
+  float* lse;
+  const int32_t *table, *lengths;
+  float* part;  // [batch, q_heads, chunks, head_dim] then [batch, q_heads, chunks, 2]
+  long long qbs, qhs, table_stride;
+  long long part_ml;  // floats before the second part
+  int q_heads, group, head_blocks;
+  int chunk, chunks;
+  int cap, window;
+  float scale_log2e;
+};
+
+// Tokens of a request: [lo, hi), and where its tiles begin (a multiple of 32).
+struct Span {
+  int lo, hi, first;
+};
+__device__ __forceinline__ Span span_of(int len, int cap, int window) {
+  Span s;
+  s.hi = len < 0 ? 0 : len < cap ? len : cap;
+  s.lo = window > 0 && s.hi > window ? s.hi - window : 0;
+  s.first = s.lo & ~31;
+  return s;
+}
+
+template <int F>
+struct Mma;
+template <>
+struct Mma<ORBIT_KV_BF16> {
+  typedef __bf16 T;
+  typedef bf16x8 V8;
+  static __device__ __forceinline__ f32x4 run(V8 a, V8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mma<ORBIT_KV_F16> {
+  typedef _Float16 T;
+  typedef f16x8 V8;
+  static __device__ __forceinline__ f32x4 run(V8 a, V8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mma<ORBIT_KV_INT8> : Mma<ORBIT_KV_F16> {};
+
+// Four signed bytes to four fp16 integers: 0x6400 + (byte + 128) is the fp16
+// number 1024 + byte + 128.
+__device__ __forceinline__ u32x2 codes_to_f16(uint32_t w) {
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  const uint32_t x = w ^ 0x80808080u;
+  const h2 off = {(_Float16)1152.0f, (_Float16)1152.0f};
+  const h2 a = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, x, 0x04010400u)) - off;
+  const h2 b = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, x, 0x04030402u)) - off;
+  u32x2 r;
+  r.x = __builtin_bit_cast(uint32_t, a);
+  r.y = __builtin_bit_cast(uint32_t, b);
+  return r;
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kTile = 32;
+constexpr int kWaves = 4;
+
+template <int DP>
+struct Stage {
+  // four rows apart a quarter of the banks apart, so that the transposing
+  // read's four row groups meet in no bank
+  static constexpr int kStride = DP + 4;  // 16-bit elements
+  static constexpr int kWaveElems = kTile * kStride;
+};
+
+// Q: the queries' format (BF16 or F16); F: the cache's; DP: head_dim rounded
+// up to 64, 128 or 256.
+template <int Q, int F, int DP>
+__global__ __launch_bounds__(256) void attend_kernel(AttentionArgs a) {
+  constexpr bool kCoded = F == ORBIT_KV_INT8;
+  typedef Mma<F> M;
+  typedef typename M::T T;
+  typedef typename M::V8 V8;
+  typedef typename Mma<Q>::T QT;
+  constexpr int kSteps = DP / 32;                   // products per tile half
+  constexpr int kLoads = kCoded ? DP / 64 : kSteps;  // 16-byte loads of one key per lane
+  constexpr int kRowLanes = kCoded ? DP / 16 : DP / 8;  // lanes on one value row
+  constexpr int kRowsAtOnce = 64 / kRowLanes;
+  constexpr int kVLoads = kTile / kRowsAtOnce;
+  constexpr int kBlocks = DP / 16;
+  constexpr int kElem = kCoded ? 1 : 2;
+
+  constexpr int kStageBytes = kWaves * Stage<DP>::kWaveElems * 2;
+  constexpr int kSumBytes = kWaves * 16 * DP * 4 + kWaves * 16 * 8;
+  __shared__ __align__(16) char lds[kStageBytes > kSumBytes ? kStageBytes : kSumBytes];
+
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int r16 = lane & 15, lg = lane >> 4;
+  const int head = blockIdx.x / a.head_blocks, hb = blockIdx.x - head * a.head_blocks;
+  const int b = blockIdx.y;
+  const int dim = a.c.head_dim;
+  const Span span = span_of(a.lengths[b], a.cap, a.window);
+  const int c0 = span.first + (int)blockIdx.z * a.chunk;
+  const int heads_here = min(16, a.group - hb * 16);
+  const int h0 = head * a.group + hb * 16;  // first query head
+  if (c0 >= span.hi) {
+    // the first chunk of a request with nothing to see writes its zeros
+    if (blockIdx.z == 0) {
+      for (int i = threadIdx.x; i < heads_here * dim; i += 256)
+        ((QT*)a.out)[((long long)b * a.q_heads + h0) * dim + i] = (QT)0.0f;
+      if (a.lse && (int)threadIdx.x < heads_here)
+        a.lse[(long long)b * a.q_heads + h0 + threadIdx.x] = -__builtin_inff();
+    }
+    return;
+  }
+  const int c1 = min(span.hi, c0 + a.chunk);
+  const int32_t* const table = a.table + b * a.table_stride;
+
+  // Queries as the B operand: lane's head r16, coordinates as the keys' loads
+  // bring them (INT8: 16 codes a load are two operands' slots).
+  V8 qf[kSteps];
+  float zscale = a.scale_log2e;
+  {
+    const QT* const qrow = (const QT*)a.q + b * a.qbs + (h0 + (r16 < heads_here ? r16 : 0)) * a.qhs;
+    float f[kSteps][8];
+    float m = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int d = kCoded ? (s >> 1) * 64 + lg * 16 + (s & 1) * 8 : s * 32 + lg * 8;
+      const bool in = r16 < heads_here && d < dim;
+      Vec8<QT> v;
+      if (in) v = *(const Vec8<QT>*)(qrow + d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[s][j] = in ? (float)v.e[j] : 0.0f;
+        if (kCoded) m = fmaxf(m, fabsf(f[s][j]));
+      }
+    }
+    if (kCoded) {
+      m = max_rows32(max_rows16(m));
+      // 2^-e brings the largest into [1/2, 1); an infinite one stays infinite
+      const int e = m > 0.0f && m < __builtin_inff() ? __builtin_amdgcn_frexp_expf(m) : 0;
+      const float down = ldexpf(1.0f, -e / 2), down2 = ldexpf(1.0f, -e - (-e / 2));
+      zscale = ldexpf(zscale, e);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[s][j] = f[s][j] * down * down2;
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) qf[s][j] = (T)f[s][j];
+  }
+
+  u32x4 kr[2][kLoads];
+  u32x4 vr[kVLoads];
+  u32x2 ksr[2], vsr[2];
+  uint32_t live = 0;  // bit t: token t of the tile is seen (and its page lies in the cache)
+
+  // page of token tile + (lane & 31), or ~0
+  auto look_up = [&](int tile) -> uint32_t {
+    const int t = tile + (lane & 31);
+    uint32_t page = 0xffffffffu;
+    if (t >= span.lo && t < c1) page = (uint32_t)table[t >> a.c.page_shift];
+    return page < a.c.pages ? page : 0xffffffffu;
+  };
+  auto row_at = [&](uint32_t page, int t) -> long long {
+    return cache_row(a.c, page, head, (uint32_t)t & a.c.page_mask);
+  };
+  auto load_keys = [&](int tile, uint32_t page) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int at = half * 16 + r16;
+      const uint32_t pg = (uint32_t)__shfl((int)page, at);
+      const char* const row = a.c.k + row_at(pg, tile + at) * (dim * kElem);
+#pragma unroll
+      for (int s = 0; s < kLoads; ++s) {
+        const int off = s * 64 + lg * 16;  // bytes
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (pg != 0xffffffffu && off < dim * kElem) v = *(const u32x4*)(row + off);
+        kr[half][s] = v;
+      }
+    }
+    if (kCoded) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        // four neighbouring tokens lie in one page (page_size >= 4); a page
+        // is known where any of the four is seen
+        const int at = half * 16 + lg * 4;
+        uint32_t pg = (uint32_t)__shfl((int)page, at);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+          const uint32_t o = (uint32_t)__shfl((int)page, at + i);
+          pg = pg != 0xffffffffu ? pg : o;
+        }
+        ksr[half] = vsr[half] = u32x2{0u, 0u};
+        if (pg != 0xffffffffu) {
+          const long long row = row_at(pg, tile + at);
+          ksr[half] = *(const u32x2*)(a.c.ks + row);
+          vsr[half] = *(const u32x2*)(a.c.vs + row);
+        }
+      }
+    }
+  };
+  auto load_values = [&](int tile, uint32_t page) {
+    const int off = (lane & (kRowLanes - 1)) * 16;  // bytes
+#pragma unroll
+    for (int i = 0; i < kVLoads; ++i) {
+      const int at = i * kRowsAtOnce + lane / kRowLanes;
+      const uint32_t pg = (uint32_t)__shfl((int)page, at);
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (pg != 0xffffffffu && off < dim * kElem) v = *(const u32x4*)(a.c.v + row_at(pg, tile + at) * (dim * kElem) + off);
+      vr[i] = v;
+    }
+  };
+
+  f32x4 o[kBlocks];
+#pragma unroll
+  for (int d = 0; d < kBlocks; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float m_run = -__builtin_inff(), l_run = 0.0f;  // l: this lane's tokens alone
+  T* const stage = (T*)lds + wave * Stage<DP>::kWaveElems;
+
+  int tile = c0 + wave * kTile;
+  if (tile < c1) {
+    uint32_t page = look_up(tile);
+    load_keys(tile, page);
+    load_values(tile, page);
+    live = (uint32_t)__ballot(page != 0xffffffffu);
+    constexpr int kStep = kWaves * kTile;
+    uint32_t next = tile + kStep < c1 ? look_up(tile + kStep) : 0xffffffffu;
+    for (; tile < c1; tile += kStep) {
+      const bool more = tile + kStep < c1;
+      // scores of the tile
+      f32x4 s[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if constexpr (kCoded) {
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            union {
+              u32x2 w[4];
+              V8 v[2];
+            } u;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) u.w[c] = codes_to_f16(kr[half][i][c]);
+            s[half] = M::run(u.v[0], qf[2 * i], s[half]);
+            s[half] = M::run(u.v[1], qf[2 * i + 1], s[half]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) s[half] = M::run(__builtin_bit_cast(V8, kr[half][i]), qf[i], s[half]);
+        }
+      }
+      float z[8], vs[8];
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[half * 4 + i] = s[half][i] * zscale;
+          if constexpr (kCoded) {
+            typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+            z[half * 4 + i] *= (float)__builtin_bit_cast(h4, ksr[half])[i];
+            vs[half * 4 + i] = (float)__builtin_bit_cast(h4, vsr[half])[i];
+          }
+        }
+      if (live != 0xffffffffu) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool seen = (live >> ((j >> 2) * 16 + lg * 4 + (j & 3))) & 1u;
+          z[j] = seen ? z[j] : -__builtin_inff();
+          if constexpr (kCoded) vs[j] = seen ? vs[j] : 0.0f;
+        }
+      }
+      const uint32_t page_now = next;
+      if (more) {
+        load_keys(tile + kStep, page_now);
+        next = tile + 2 * kStep < c1 ? look_up(tile + 2 * kStep) : 0xffffffffu;
+      }
+
+      // running maximum (of z + log2(scale) where values carry one) and sums
+      float mt = -__builtin_inff();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (kCoded) mt = fmaxf(mt, z[j] + __builtin_amdgcn_logf(fmaxf(vs[j], 5.9604645e-8f)));
+        else mt = fmaxf(mt, z[j]);
+      }
+      mt = max_rows32(max_rows16(mt));
+      const float m_new = fmaxf(m_run, mt);
+      const float m_use = m_new == -__builtin_inff() ? 0.0f : m_new;
+      const float alpha = __builtin_amdgcn_exp2f(m_run - m_use);
+      m_run = m_new;
+      l_run *= alpha;
+      V8 hi, lo;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float p = __builtin_amdgcn_exp2f(z[j] - m_use);
+        l_run += p;
+        if constexpr (kCoded) p *= vs[j];
+        hi[j] = (T)p;
+        lo[j] = (T)(p - (float)hi[j]);
+      }
+#pragma unroll
+      for (int d = 0; d < kBlocks; ++d) o[d] *= alpha;
+
+      // values to the wave's rows (LDS serves one wave's accesses in order)
+      {
+        const int e0 = (lane & (kRowLanes - 1)) * (kCoded ? 16 : 8);
+#pragma unroll
+        for (int i = 0; i < kVLoads; ++i) {
+          u32x2* const to = (u32x2*)(stage + (i * kRowsAtOnce + lane / kRowLanes) * Stage<DP>::kStride + e0);
+          if constexpr (kCoded) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) to[c] = codes_to_f16(vr[i][c]);
+          } else {
+            to[0] = u32x2{vr[i].x, vr[i].y};
+            to[1] = u32x2{vr[i].z, vr[i].w};
+          }
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (more) {
+        load_values(tile + kStep, page_now);
+        live = (uint32_t)__ballot(page_now != 0xffffffffu);
+      }
+      {
+        typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+        const T* const at = stage + (lg * 4 + (r16 >> 2)) * Stage<DP>::kStride + (r16 & 3) * 4;
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d) {
+          union {
+            s16x4 h[2];
+            V8 v;
+          } u;
+          u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + d * 16));
+          u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 16 * Stage<DP>::kStride + d * 16));
+          o[d] = M::run(u.v, hi, o[d]);
+          o[d] = M::run(u.v, lo, o[d]);
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  l_run = add_rows32(add_rows16(l_run));
+
+  // the four waves' sums meet
+  __syncthreads();
+  float* const so = (float*)lds;                     // [wave][head][DP]
+  float* const sm = (float*)(lds + kWaves * 16 * DP * 4);  // [wave][head], then the sums
+  if (lg == 0) {
+    sm[wave * 16 + r16] = m_run;
+    sm[kWaves * 16 + wave * 16 + r16] = l_run;
+  }
+#pragma unroll
+  for (int d = 0; d < kBlocks; ++d) *(f32x4*)(so + (wave * 16 + r16) * DP + d * 16 + lg * 4) = o[d];
+  __syncthreads();
+  const bool last = a.chunks == 1;
+  for (int i = threadIdx.x; i < heads_here * (DP / 8); i += 256) {
+    const int h = i / (DP / 8), d = (i - h * (DP / 8)) * 8;
+    if (d >= dim) continue;
+    float m = sm[h];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sm[w * 16 + h]);
+    const float m_use = m == -__builtin_inff() ? 0.0f : m;
+    float l = 0.0f, f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float e = __builtin_amdgcn_exp2f(sm[w * 16 + h] - m_use);
+      l = fmaf(e, sm[kWaves * 16 + w * 16 + h], l);
+      const f32x4 x = *(const f32x4*)(so + (w * 16 + h) * DP + d), y = *(const f32x4*)(so + (w * 16 + h) * DP + d + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[j] = fmaf(e, x[j], f[j]);
+        f[4 + j] = fmaf(e, y[j], f[4 + j]);
+      }
+    }
+    const long long bh = (long long)b * a.q_heads + h0 + h;
+    if (last) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      Vec8<QT> v;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v.e[j] = (QT)(l == 0.0f ? 0.0f : f[j] * inv);
+      *(Vec8<QT>*)((QT*)a.out + bh * dim + d) = v;
+      if (a.lse && d == 0) a.lse[bh] = (m + __builtin_amdgcn_logf(l)) * 0.69314718056f;
+    } else {
+      const long long at = bh * a.chunks + blockIdx.z;
+      f32x4* const to = (f32x4*)(a.part + at * dim + d);
+      to[0] = f32x4{f[0], f[1], f[2], f[3]};
+      to[1] = f32x4{f[4], f[5], f[6], f[7]};
+      if (d == 0) *(float2*)(a.part + a.part_ml + at * 2) = make_float2(m, l);
+    }
+  }
+}
+
+// Joins the chunks of one query head: a workgroup per (request, head), its
+// groups of dim / 4 lanes taking every n-th chunk.
+template <class QT>
+__global__ __launch_bounds__(256) void join_kernel(AttentionArgs a) {
+  __shared__ f32x4 so[256];
+  __shared__ float sl[256];
+  const int b = blockIdx.y, h = blockIdx.x;
+  const Span span = span_of(a.lengths[b], a.cap, a.window);
+  if (span.hi <= span.first) return;  // nothing to see: written already
+  const int n = (span.hi - span.first + a.chunk - 1) / a.chunk;
+  const long long bh = (long long)b * a.q_heads + h;
+  const int dim = a.c.head_dim, lanes = dim >> 2;
+  const int groups = 256 / lanes;
+  const int g = threadIdx.x / lanes, t = threadIdx.x - g * lanes;
+  const float2* const ml = (const float2*)(a.part + a.part_ml) + bh * a.chunks;
+  float m = -__builtin_inff();
+  for (int c = threadIdx.x & 63; c < n; c += 64) m = fmaxf(m, ml[c].x);
+  m = dpp_max<kXor1>(m);
+  m = dpp_max<kXor2>(m);
+  m = dpp_max<kHalfMirror>(m);
+  m = dpp_max<kRowMirror>(m);
+  m = max_rows32(max_rows16(m));
+  const float m_use = m == -__builtin_inff() ? 0.0f : m;
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  float l = 0.0f;
+  if (g < groups) {
+    const f32x4* const part = (const f32x4*)(a.part + bh * a.chunks * dim) + t;
+#pragma unroll 4
+    for (int c = g; c < n; c += groups) {
+      const float2 x = ml[c];
+      const float e = __builtin_amdgcn_exp2f(x.x - m_use);
+      const f32x4 v = part[(long long)c * lanes];
+      l = fmaf(e, x.y, l);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = fmaf(e, v[j], o[j]);
+    }
+  }
+  so[threadIdx.x] = o;
+  sl[threadIdx.x] = l;
+  __syncthreads();
+  if (g != 0) return;
+  const int used = groups < n ? groups : n;
+  for (int i = 1; i < used; ++i) {
+    o += so[i * lanes + t];
+    l += sl[i * lanes + t];
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  struct alignas(8) {
+    QT e[4];
+  } v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v.e[j] = (QT)(l == 0.0f ? 0.0f : o[j] * inv);
+  *(decltype(v)*)((QT*)a.out + bh * dim + t * 4) = v;
+  if (a.lse && t == 0) a.lse[bh] = (m + __builtin_amdgcn_logf(l)) * 0.69314718056f;
+}
+
+template <int Q, int F>
+hipError_t launch_attend(const AttentionArgs& a, dim3 grid, hipStream_t stream) {
+  const int dim = a.c.head_dim;
+  if (dim <= 64) attend_kernel<Q, F, 64><<<grid, dim3(256), 0, stream>>>(a);
+  else if (dim <= 128) attend_kernel<Q, F, 128><<<grid, dim3(256), 0, stream>>>(a);
+  else attend_kernel<Q, F, 256><<<grid, dim3(256), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_attend_coded(const AttentionArgs& a, int q_dtype, dim3 grid, hipStream_t stream);
+
+}  // namespace block
+}  // namespace orbit

@@ -491,8 +491,8 @@ typedef struct {
 
 orbit_status orbit_paged_attention(const orbit_paged_attention_args *args, hipStream_t stream);
 
-/* Bytes of orbit_paged_attention's workspace for these sizes on the current
- * device; -1 for invalid sizes or if the device cannot be asked. */
+/* Bytes of orbit_paged_attention's workspace for these sizes; -1 for invalid
+ * ones.  Host only. */
 int64_t orbit_paged_attention_workspace(int64_t batch, int64_t q_heads, int64_t kv_heads,
                                         int64_t head_dim, int64_t page_size,
                                         int64_t table_width, int64_t window);

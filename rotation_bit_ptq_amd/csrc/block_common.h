@@ -17,6 +17,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
+// Compute units that a launch should fill (the whole device; splits are
+// chosen from sizes alone, so that workspaces can be sized without asking it).
+constexpr int kUnits = 256;
+
 // Eight neighbouring elements, loaded and stored as 16-byte words.
 template <class T>
 struct alignas(16) Vec8 {
@@ -29,6 +33,25 @@ inline bool aligned_to(const void* p, int64_t bytes) { return ((uintptr_t)p & (u
 // Rows that eight-element vectors may read: 16-byte base, strides in whole
 // vectors.
 inline bool vector_rows(const void* p, int64_t stride) { return aligned_to(p, 16) && stride % 8 == 0; }
+
+// One 16x16x32 product.  Lane l holds row (A) or column (B) l % 16 at k = 8
+// (l / 16) + 0 .. 7, and of the result column l % 16, rows 4 (l / 16) + 0 .. 3.
+__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+template <class T>
+struct Vec8Of;
+template <>
+struct Vec8Of<__bf16> {
+  typedef bf16x8 V;
+};
+template <>
+struct Vec8Of<_Float16> {
+  typedef f16x8 V;
+};
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v) {

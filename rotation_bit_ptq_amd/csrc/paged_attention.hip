@@ -23,24 +23,19 @@ struct Split {
 
 // Tokens per workgroup: whole rounds of its four waves' tiles, so many that
 // the chunks of full contexts make about six workgroups per compute unit.
-hipError_t split_of(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t cap, int64_t window, Split* s) {
-  DeviceInfo di;
-  const hipError_t e = device_info(&di);
-  if (e != hipSuccess) return e;
+Split split_of(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t cap, int64_t window) {
   const int64_t round = kTile * kWaves;
   int64_t span = cap;
   if (window > 0 && window + 31 < span) span = window + 31;
   if (span < 1) span = 1;
   const int64_t heads = kv_heads * ((q_heads / kv_heads + 15) / 16);
-  const int64_t want = (int64_t)di.n_cu * 6;
+  const int64_t want = (int64_t)kUnits * 6;
   int64_t pieces = (want + batch * heads - 1) / (batch * heads > 0 ? batch * heads : 1);
   const int64_t most = (span + round - 1) / round;
   if (pieces > most) pieces = most;
   if (pieces < 1) pieces = 1;
   const int64_t chunk = ((span + pieces - 1) / pieces + round - 1) / round * round;
-  s->chunk = (int)chunk;
-  s->chunks = (int)((span + chunk - 1) / chunk);
-  return hipSuccess;
+  return Split{(int)chunk, (int)((span + chunk - 1) / chunk)};
 }
 
 int64_t bytes_of(const Split& s, int64_t batch, int64_t q_heads, int64_t head_dim) {
@@ -53,9 +48,7 @@ extern "C" int64_t orbit_paged_attention_workspace(int64_t batch, int64_t q_head
                                                    int64_t page_size, int64_t table_width, int64_t window) {
   if (!sizes_ok(batch, q_heads, kv_heads, head_dim, page_size, table_width, window)) return -1;
   if (batch == 0) return 0;
-  Split s;
-  if (split_of(batch, q_heads, kv_heads, table_width * page_size, window, &s) != hipSuccess) return -1;
-  return bytes_of(s, batch, q_heads, head_dim);
+  return bytes_of(split_of(batch, q_heads, kv_heads, table_width * page_size, window), batch, q_heads, head_dim);
 }
 
 extern "C" orbit_status orbit_paged_attention(const orbit_paged_attention_args* p, hipStream_t stream) {
@@ -75,9 +68,7 @@ extern "C" orbit_status orbit_paged_attention(const orbit_paged_attention_args* 
   if (!vector_rows(p->q, p->q_batch_stride) || p->q_head_stride % 8) return ORBIT_E_ARG;
   if (p->table_width > 0 && (!p->block_table || !aligned_to(p->block_table, 4))) return ORBIT_E_ARG;
   if (p->lse && !aligned_to(p->lse, 4)) return ORBIT_E_ARG;
-  Split s;
-  hipError_t e = split_of(p->batch, p->q_heads, c.kv_heads, p->table_width * c.page_size, p->window, &s);
-  if (e != hipSuccess) return hip_status(e);
+  const Split s = split_of(p->batch, p->q_heads, c.kv_heads, p->table_width * c.page_size, p->window);
   const int64_t need = bytes_of(s, p->batch, p->q_heads, c.head_dim);
   if (need > 0 && (!p->workspace || !aligned_to(p->workspace, 16) || p->workspace_bytes < need)) return ORBIT_E_ARG;
   AttentionArgs a = {};
@@ -101,6 +92,7 @@ extern "C" orbit_status orbit_paged_attention(const orbit_paged_attention_args* 
   a.window = (int)p->window;
   a.scale_log2e = p->sm_scale * 1.44269504089f;
   const dim3 grid((unsigned)(c.kv_heads * a.head_blocks), (unsigned)p->batch, (unsigned)s.chunks);
+  hipError_t e;
   switch (c.format) {
     case ORBIT_KV_BF16: e = launch_attend<ORBIT_KV_BF16, ORBIT_KV_BF16>(a, grid, stream); break;
     case ORBIT_KV_F16: e = launch_attend<ORBIT_KV_F16, ORBIT_KV_F16>(a, grid, stream); break;

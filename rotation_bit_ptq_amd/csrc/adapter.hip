@@ -21,12 +21,12 @@ struct AdapterArgs {
   uint32_t M, adapters;
   int K, N, R;
   int parts, k_part;  // K in parts of k_part, a workgroup each
-  int columns;        // blocks of 256 columns per workgroup
+  int columns, blocks;  // 256 columns a piece per workgroup; workgroups across N
 };
 
 constexpr int kWaves = 4;
-constexpr int kRowsAtMost = 64;   // tokens up to which rows go one by one
-constexpr int kPartsAtMost = 16;  // parts of K
+constexpr int kRequestsAtMost = 4;  // of a tile, past which its rows go one by one
+constexpr int kFewTokens = 64, kSomeTokens = 2048;  // see cut_of
 
 // The adapter's rank, 0 where there is none.
 __device__ __forceinline__ int rank_of(const AdapterArgs& a, int id) {
@@ -35,24 +35,110 @@ __device__ __forceinline__ int rank_of(const AdapterArgs& a, int id) {
   return r < 0 ? 0 : r < a.R ? r : a.R;
 }
 
-// v[m][r] = A[id][r] . x[m]: a wave per (row, rank).
-template <class T>
-__global__ __launch_bounds__(256) void shrink_rows_kernel(AdapterArgs a) {
-  const uint32_t m = blockIdx.x;
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int id = a.ids[m];
-  if (r >= rank_of(a, id)) return;
-  const T* const x = (const T*)a.x + m * a.xs;
-  const T* const w = (const T*)a.A + ((long long)id * a.R + r) * a.K;
-  float s = 0.0f;
-#pragma unroll 4
-  for (int k = lane * 8; k < a.K; k += 512) {
-    const Vec8<T> p = *(const Vec8<T>*)(x + k), q = *(const Vec8<T>*)(w + k);
+// Eight products and their sum.  bf16: v_dot2_f32_bf16 (exact products);
+// fp16: mixed-precision multiply-adds, which keep fp16's subnormal numbers.
+__device__ __forceinline__ float dot8(const u32x4& x, const u32x4& w, float s, __bf16) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  struct B4 {
+    b2 e[4];
+  };
+  const B4 p = __builtin_bit_cast(B4, x), q = __builtin_bit_cast(B4, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s = fmaf((float)p.e[j], (float)q.e[j], s);
+  for (int j = 0; j < 4; ++j) s = __builtin_amdgcn_fdot2_f32_bf16(p.e[j], q.e[j], s, false);
+  return s;
+}
+__device__ __forceinline__ float dot8(const u32x4& x, const u32x4& w, float s, _Float16) {
+  const f16x8 p = __builtin_bit_cast(f16x8, x), q = __builtin_bit_cast(f16x8, w);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s = fmaf((float)p[j], (float)q[j], s);
+  return s;
+}
+
+// Sums of four values over the wave at once: row i of 16 lanes ends up with
+// the sum of s[i] (each exchange merges two values' halves).
+__device__ __forceinline__ float sum_of_four(const float (&s)[4]) {
+  auto merge32 = [](float x, float y) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, x), __builtin_bit_cast(unsigned, y), false, false);
+    return __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
+  };
+  const float u = merge32(s[0], s[2]), w = merge32(s[1], s[3]);
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, u), __builtin_bit_cast(unsigned, w), false, false);
+  float v = __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
+  v = dpp_add<kXor1>(v);
+  v = dpp_add<kXor2>(v);
+  v = dpp_add<kHalfMirror>(v);
+  return dpp_add<kRowMirror>(v);
+}
+
+// v[m][r] = A[id][r] . x[m] over k0 <= k < k1 for RG rows and RW (1 or 4)
+// ranks from r0, by one wave without matrix cores: the lanes take
+// neighbouring vectors of K, so that every load is one contiguous KB.  A is
+// read once for the rows that share an adapter.
+template <class T, int RG, int RW>
+__device__ __forceinline__ void row_products(const AdapterArgs& a, uint32_t m0, int r0, int k0, int k1, float* v) {
+  const int lane = threadIdx.x & 63;
+  int id[RG];
+  const T* x[RG];
+#pragma unroll
+  for (int g = 0; g < RG; ++g) {
+    const uint32_t m = min(m0 + g, a.M - 1);
+    id[g] = m0 + g < a.M ? a.ids[m] : -1;
+    x[g] = (const T*)a.x + (long long)m * a.xs + lane * 8;
   }
-  s = wave_sum(s);
-  if (lane == 0) a.v[(long long)m * a.R + r] = s;
+#pragma unroll
+  for (int g = 0; g < RG; ++g) {
+    bool seen = false;  // with an earlier row
+#pragma unroll
+    for (int h = 0; h < g; ++h) seen = seen || id[h] == id[g];
+    const int rank = seen ? 0 : rank_of(a, id[g]);
+    if (r0 >= rank) continue;
+    const T* w[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+      w[i] = (const T*)a.A + ((long long)id[g] * a.R + min(r0 + i, rank - 1)) * a.K + lane * 8;
+    float s[RG][RW];
+#pragma unroll
+    for (int h = 0; h < RG; ++h)
+#pragma unroll
+      for (int i = 0; i < RW; ++i) s[h][i] = 0.0f;
+    int k = k0;
+    auto step = [&]() {
+      u32x4 xv[RG], wv[RW];
+#pragma unroll
+      for (int h = 0; h < RG; ++h) xv[h] = *(const u32x4*)(x[h] + k);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) wv[i] = *(const u32x4*)(w[i] + k);
+#pragma unroll
+      for (int h = 0; h < RG; ++h)
+#pragma unroll
+        for (int i = 0; i < RW; ++i) s[h][i] = dot8(xv[h], wv[i], s[h][i], T());
+    };
+    constexpr int kAtOnce = RG * RW == 1 ? 8 : 2;
+    for (; k + 512 * kAtOnce <= k1;) {
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u, k += 512) step();
+    }
+    for (; k + 512 <= k1; k += 512) step();
+    if (k + lane * 8 < k1) step();
+#pragma unroll
+    for (int h = g; h < RG; ++h) {
+      float* const to = v + (long long)(m0 + h) * a.R + r0;
+      const bool own = id[h] == id[g];
+      if constexpr (RW == 4) {
+        const float t = sum_of_four(s[h]);
+        if (own && (lane & 15) == 0 && r0 + (lane >> 4) < rank) to[lane >> 4] = t;
+      } else {
+        const float t = wave_sum(s[h][0]);
+        if (own && lane == 0) *to = t;
+      }
+    }
+  }
+}
+
+template <class T, int RG, int RW>
+__global__ __launch_bounds__(256) void shrink_rows_kernel(AdapterArgs a) {
+  const int r0 = ((int)blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * RW;
+  row_products<T, RG, RW>(a, blockIdx.x * RG, r0, 0, a.K, a.v);
 }
 
 // out[m][n] = y[m][n] + s B[id][n] . v[m]: a thread per column.
@@ -83,191 +169,345 @@ __global__ __launch_bounds__(256) void expand_rows_kernel(AdapterArgs a) {
   ((YT*)a.out)[m * a.os + n] = (YT)f;
 }
 
-// The distinct adapters of a tile of up to 64 rows, one after the other.
-// Lane l holds row l's adapter (-1: none, or past the tile).
-struct Requests {
-  unsigned long long rest;
+// One row's request: its adapter (-1: none, or one of rank 0), rank, scale.
+struct Request {
   int id, rank;
-  unsigned long long rows;  // the rows of `id`
+  float scale;
+};
 
-  __device__ __forceinline__ void begin(int mine) { rest = __ballot(mine >= 0); }
-  __device__ __forceinline__ bool next(const AdapterArgs& a, int mine) {
+// Lane l's: that of row m0 + l of a tile of TM <= 64 rows.
+template <int TM>
+__device__ __forceinline__ Request request_of(const AdapterArgs& a, uint32_t m0, int lane) {
+  Request q = {-1, 0, 1.0f};
+  if (lane < TM && m0 + lane < a.M) {
+    q.id = a.ids[m0 + lane];
+    q.rank = rank_of(a, q.id);
+    if (q.rank == 0) q.id = -1;
+    else if (a.scale) q.scale = a.scale[q.id];
+  }
+  return q;
+}
+
+// The distinct adapters of a tile, one after the other.  Everything about
+// them is in the lanes' registers: a load here would wait for the operands'
+// loads that are in flight.
+struct Requests {
+  unsigned long long rest, rows;  // rows still to come; rows of `id`
+  int id, rank;
+
+  __device__ __forceinline__ void begin(const Request& mine) { rest = __ballot(mine.id >= 0); }
+  // Whether there are more than `most` of them.
+  static __device__ __forceinline__ bool exceed(const Request& mine, int most) {
+    Requests q;
+    q.begin(mine);
+    int n = 0;
+    while (n <= most && q.next(mine)) ++n;
+    return n > most;
+  }
+  __device__ __forceinline__ bool next(const Request& mine) {
     if (rest == 0) return false;
-    id = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rest));
-    rows = __ballot(mine == id);
+    const int first = __builtin_ctzll(rest);
+    id = __builtin_amdgcn_readlane(mine.id, first);
+    rank = __builtin_amdgcn_readlane(mine.rank, first);
+    rows = __ballot(mine.id == id);
     rest &= ~rows;
-    rank = rank_of(a, id);
     return true;
   }
 };
 
-// This lane's row's adapter if it has one of rank > 0, else -1.
-template <int TM>
-__device__ __forceinline__ int my_request(const AdapterArgs& a, uint32_t m0, int lane) {
-  if (lane >= TM || m0 + lane >= a.M) return -1;
-  const int id = a.ids[m0 + lane];
-  return rank_of(a, id) > 0 ? id : -1;
-}
-
-// v = A x for tiles of 16 MB rows, ranks up to 16 RB, on the matrix cores:
-// rows of x are the A operand, rows of the adapter's A the B operand, both
-// straight from memory (16 contiguous bytes of a lane are an operand's
-// slots).  The four waves share the workgroup's part of K, so each loads
-// its piece of x once for all RB blocks of ranks; their sums meet in LDS.
-// blockIdx.y takes part blockIdx.y of K: the parts are summed, in a fixed
-// order, by the second kernel, so no atomics.  A tile of several requests
-// runs once over its part of K for each, on the row blocks that hold the
-// request alone; loads of P steps are in flight, also across requests.
-template <class T, int MB, int RB, int P>
-__global__ __launch_bounds__(256) void shrink_tiles_kernel(AdapterArgs a) {
+// v = A x for many tokens, on the matrix cores: tiles of 64 rows, a part of K
+// in chunks of 128.  blockIdx.y takes part blockIdx.y of K; the parts are
+// summed, in a fixed order, by the second kernel, so no atomics.
+// A chunk of x and of the request's A go through LDS: sixteen lanes read 256
+// contiguous bytes of a row (a matrix operand read from memory directly has
+// its neighbouring lanes in 16 different rows, which costs the address unit
+// four times the cycles), and the operands come back as 16-byte reads from
+// rows 16 bytes further than 256 apart, which spread over the banks.  The
+// next chunk's loads are in flight, in registers, while one is multiplied.
+// Wave w takes rows 16 w .. 16 w + 15 and all ranks, so sums stay in one
+// wave.  A tile of several requests runs over its part of K for each;
+// blockIdx.z takes every second of them, because where all workgroups are
+// resident at once a tile that runs twice (at the border of two prompts)
+// would double the kernel's time.
+template <class T, int RB>
+__global__ __launch_bounds__(256) void shrink_staged_kernel(AdapterArgs a) {
   typedef typename Vec8Of<T>::V V8;
-  constexpr int TM = 16 * MB, RP = 16 * RB;
-  __shared__ float red[kWaves][TM][RP];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r16 = lane & 15, lg = lane >> 4;
+  constexpr int TM = 64, KC = 128, kRow = KC + 8;
+  __shared__ __align__(16) T xs[TM][kRow], ws[16 * RB][kRow];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, r16 = lane & 15, lg = lane >> 4;
+  const int trow = threadIdx.x >> 4, tcol = (threadIdx.x & 15) * 8;  // this thread's place in 16 rows of a chunk
   const uint32_t m0 = blockIdx.x * TM;
-  const int mine = my_request<TM>(a, m0, lane);
-  const int k0 = (int)blockIdx.y * a.k_part + wave * (a.k_part / kWaves);
-  const int k1 = min(a.K, k0 + a.k_part / kWaves);
-  const int steps = k1 > k0 ? (k1 - k0 + 31) / 32 : 0;
-
-  const T* xrow[MB];
-#pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    const uint32_t m = m0 + mb * 16 + r16;
-    xrow[mb] = (const T*)a.x + (long long)(m < a.M ? m : a.M - 1) * a.xs + lg * 8;
+  if (blockIdx.z) {  // mostly there is one request: leave at once
+    const int id = a.ids[min(m0 + lane, a.M - 1)];
+    if (__ballot(id != __builtin_amdgcn_readfirstlane(id)) == 0) return;
   }
-  u32x4 xf[P][MB], wf[P][RB];
-  f32x4 acc[MB][RB];
-  auto clear = [&]() {
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb) acc[mb][rb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const Request mine = request_of<TM>(a, m0, lane);
+  const int first_k = (int)blockIdx.y * a.k_part, k1 = min(a.K, first_k + a.k_part);
+  if (Requests::exceed(mine, kRequestsAtMost)) {
+    // single tokens of many requests: row by row, half the rows to each z
+    for (int i = 0; i < 8; ++i)
+      for (int r = 0; r < a.R; r += 4)
+        row_products<T, 1, 4>(a, m0 + blockIdx.z * 32 + wave * 8 + i, r, first_k, k1, a.v + (long long)blockIdx.y * a.M * a.R);
+    return;
+  }
+  auto next = [&](Requests& q) {
+    bool more = q.next(mine);
+    for (unsigned z = 1; z < gridDim.z && more; ++z) more = q.next(mine);
+    return more;
   };
-  auto holds = [&](unsigned long long rows, int mb) { return MB == 1 || ((rows >> (mb * 16)) & 0xffffull) != 0; };
 
-  Requests ld, cp;  // the requests being loaded and multiplied
+  const T* xrow[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t m = m0 + i * 16 + trow;
+    xrow[i] = (const T*)a.x + (long long)(m < a.M ? m : a.M - 1) * a.xs;
+  }
+  Requests ld, cp;
   ld.begin(mine);
   cp.begin(mine);
-  int ls = 0, cs = 0;
-  bool more = steps > 0 && ld.next(a, mine);
-  if (more) cp.next(a, mine);
-  bool left = more;
-  auto load = [&](int p) {
-    if (!more) return;
-    const int k = k0 + ls * 32;
-    const bool in = k + lg * 8 < k1;
+  if (blockIdx.z) {
+    cp.next(mine);
+    ld.next(mine);
+  }
+  if (!cp.next(mine)) return;  // the same for the whole workgroup
+  ld.next(mine);
+  int lk = first_k, ck = first_k;
+  u32x4 xr[4], wr[RB];
+  const T* wrow[RB];
+  auto aim = [&]() {
+    const T* const w = (const T*)a.A + (long long)ld.id * a.R * a.K;
+#pragma unroll
+    for (int i = 0; i < RB; ++i) wrow[i] = w + (long long)min(i * 16 + trow, ld.rank - 1) * a.K;
+  };
+  auto load = [&]() {  // past the end: what was read before
+    const int at = lk + tcol < k1 ? lk + tcol : first_k;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) xr[i] = *(const u32x4*)(xrow[i] + at);
+#pragma unroll
+    for (int i = 0; i < RB; ++i) wr[i] = *(const u32x4*)(wrow[i] + at);
+    lk += KC;
+    if (lk >= k1 && next(ld)) {
+      lk = first_k;
+      aim();
+    }
+  };
+  aim();
+  load();
+  f32x4 acc[RB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  while (true) {
+    const bool in = ck + tcol < k1;
     const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-      xf[p][mb] = zero;
-      if (holds(ld.rows, mb) && in) xf[p][mb] = *(const u32x4*)(xrow[mb] + k);
+    for (int i = 0; i < 4; ++i) *(u32x4*)&xs[i * 16 + trow][tcol] = in ? xr[i] : zero;
+#pragma unroll
+    for (int i = 0; i < RB; ++i) *(u32x4*)&ws[i * 16 + trow][tcol] = in ? wr[i] : zero;
+    __syncthreads();
+    load();
+#pragma unroll
+    for (int k = 0; k < KC; k += 32) {
+      const V8 x = *(const V8*)&xs[wave * 16 + r16][k + lg * 8];
+#pragma unroll
+      for (int i = 0; i < RB; ++i) acc[i] = mma(x, *(const V8*)&ws[i * 16 + r16][k + lg * 8], acc[i]);
     }
-    const T* const w = (const T*)a.A + (long long)ld.id * a.R * a.K + k + lg * 8;
+    __syncthreads();
+    ck += KC;
+    if (ck >= k1) {
+      ck = first_k;
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      const int r = rb * 16 + r16;
-      wf[p][rb] = zero;
-      if (r < ld.rank && in) wf[p][rb] = *(const u32x4*)(w + (long long)r * a.K);
-    }
-    if (++ls == steps) {
-      ls = 0;
-      more = ld.next(a, mine);
-    }
-  };
-  auto multiply = [&](int p) {
-    if (!left) return;
+      for (int j = 0; j < 4; ++j) {
+        const int row = wave * 16 + lg * 4 + j;
+        if ((cp.rows >> row) & 1ull) {
+          float* const v = a.v + ((long long)blockIdx.y * a.M + m0 + row) * a.R + r16;
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-      if (holds(cp.rows, mb)) {
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
-          acc[mb][rb] = mma(__builtin_bit_cast(V8, xf[p][mb]), __builtin_bit_cast(V8, wf[p][rb]), acc[mb][rb]);
-      }
-    if (++cs == steps) {
-      cs = 0;
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = mb * 16 + lg * 4 + i;
-          if ((cp.rows >> row) & 1ull) {
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) red[wave][row][rb * 16 + r16] = acc[mb][rb][i];
-          }
+          for (int i = 0; i < RB; ++i)
+            if (i * 16 + r16 < a.R) v[i * 16] = acc[i][j];
         }
-      clear();
-      left = cp.next(a, mine);
-    }
-  };
-  clear();
+      }
 #pragma unroll
-  for (int p = 0; p < P; ++p) load(p);
-  while (left) {
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      multiply(p);
-      load(p);
+      for (int i = 0; i < RB; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (!next(cp)) break;
     }
   }
+}
+
+// Which tile of rows and which block of columns a workgroup of the second
+// kernel takes.  Workgroups go round the eight XCDs, each with an L2 of its
+// own: with eight blocks of columns or more, an XCD keeps to every eighth
+// block for all tiles, so that the adapters' blocks of B stay in its L2.
+struct Place {
+  uint32_t tile;
+  int block;
+};
+__device__ __forceinline__ Place place_of(const AdapterArgs& a, uint32_t tiles) {
+  const uint32_t i = blockIdx.x;
+  Place p;
+  if (a.blocks >= 8) {
+    p.tile = (i >> 3) % tiles;
+    p.block = (int)((i >> 3) / tiles * 8 + (i & 7));
+  } else {
+    p.tile = i % tiles;
+    p.block = (int)(i / tiles);
+  }
+  return p;
+}
+
+// Eight of a row's v from r0: the parts of K summed, the adapter's scale
+// applied, zeros past its rank.  Loaded whether used or not (rows without an
+// adapter hold anything), so that the loads need not wait for the request.
+__device__ __forceinline__ void load_v(const AdapterArgs& a, uint32_t m, int r0, int rank, float scale, float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+  const float* const v = a.v + (long long)min(m, a.M - 1) * a.R + (r0 < a.R ? r0 : 0);
+#pragma unroll 4
+  for (int s = 0; s < a.parts; ++s) {
+    const f32x4* const q = (const f32x4*)(v + (long long)s * a.M * a.R);
+    const f32x4 p0 = q[0], p1 = q[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] += p0[j];
+      f[4 + j] += p1[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = r0 + j < rank ? f[j] * scale : 0.0f;
+}
+
+// A vector of VW elements of y and out.
+template <class YT, int VW>
+struct alignas(VW * sizeof(YT)) Vector {
+  YT e[VW];
+};
+
+// The same for tiles of more than kRequestsAtMost requests (single tokens):
+// 16 rows of a tile of TM and 256 J columns, row by row without matrix cores.
+// A row's block of B is read in the order of memory, KB * 4 KB at a time; a
+// lane's eight ranks are summed over the lanes of a row of B.
+template <class T, class YT, int TM, int KB, int VW>
+__global__ __launch_bounds__(256) void expand_singles_kernel(AdapterArgs a) {
+  typedef typename Vec8Of<T>::V V8;
+  constexpr int RP = 32 * KB, kLanes = RP / 8, kAcross = 64 / kLanes;  // lanes on a row of B, rows at once
+  __shared__ __align__(16) float vf[16][RP + 4];
+  __shared__ __align__(16) float turns[kWaves][16][68];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const Place place = place_of(a, (a.M + 15) / 16);
+  if (place.block >= a.blocks) return;
+  const uint32_t m0 = place.tile * 16 / TM * TM;
+  const int sub = (int)(place.tile * 16 - m0);  // these rows of the tile
+  const Request mine = request_of<TM>(a, m0, lane);
+  if (!Requests::exceed(mine, kRequestsAtMost)) return;  // expand_tiles_kernel's
+  for (int i = threadIdx.x; i < 16 * kLanes; i += 256) {
+    const int row = i / kLanes, r0 = (i - row * kLanes) * 8;
+    float f[8];
+    load_v(a, m0 + sub + row, r0, __shfl(mine.rank, sub + row), __shfl(mine.scale, sub + row), f);
+    *(f32x4*)&vf[row][r0] = f32x4{f[0], f[1], f[2], f[3]};
+    *(f32x4*)&vf[row][r0 + 4] = f32x4{f[4], f[5], f[6], f[7]};
+  }
   __syncthreads();
-  // waves without a step of their own wrote nothing
-  const int part = a.k_part / kWaves;
-  const int used = min(kWaves, (min(a.K, (int)blockIdx.y * a.k_part + a.k_part) - (int)blockIdx.y * a.k_part + part - 1) / part);
-  for (int i = threadIdx.x; i < TM * RP; i += 256) {
-    const int row = i / RP, r = i - row * RP;
-    if (r >= a.R || m0 + row >= a.M) continue;
-    float s = red[0][row][r];
-    for (int w = 1; w < used; ++w) s += red[w][row][r];
-    a.v[((long long)blockIdx.y * a.M + m0 + row) * a.R + r] = s;  // of rows without an adapter: never read
+  float(*const turn)[68] = turns[wave];
+  const int brow = lane / kLanes, bcol = lane % kLanes, brank = bcol * 8;
+  const int prow = lane / (64 / VW), pcol = (lane % (64 / VW)) * VW;
+  for (int j = 0; j < a.columns; ++j) {
+    const int n0 = (place.block * a.columns + j) * 256 + wave * 64;
+    if (n0 >= a.N) return;
+    constexpr int kAtOnce = KB == 1 ? 4 : 2;  // rows whose loads are in flight together
+#pragma unroll 1
+    for (int i = 0; i < 16; i += kAtOnce) {
+      u32x4 w[kAtOnce][4 * KB];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int id = max(__builtin_amdgcn_readlane(mine.id, sub + i + u), 0);  // none: of rank 0, any will do
+        const int rank = __builtin_amdgcn_readlane(mine.rank, sub + i + u);
+        const T* const at = (const T*)a.B + (long long)id * a.N * a.R + (brank < rank ? brank : 0);
+#pragma unroll
+        for (int c = 0; c < 4 * KB; ++c) w[u][c] = *(const u32x4*)(at + (long long)min(n0 + c * kAcross + brow, a.N - 1) * a.R);
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int used = __builtin_amdgcn_readlane(mine.rank, sub + i + u) - brank;  // of this lane's eight ranks
+        const f32x4 v0 = *(const f32x4*)&vf[i + u][brank], v1 = *(const f32x4*)&vf[i + u][brank + 4];
+        float own = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4 * KB; ++c) {
+          const V8 b = __builtin_bit_cast(V8, w[u][c]);
+          float s = 0.0f;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) s = fmaf(q < used ? (float)b[q] : 0.0f, q < 4 ? v0[q & 3] : v1[q & 3], s);
+          s = dpp_add<kXor1>(s);
+          s = dpp_add<kXor2>(s);
+          if (KB >= 2) s = dpp_add<kHalfMirror>(s);
+          if (KB >= 4) s = dpp_add<kRowMirror>(s);
+          if (bcol == c) own = s;  // the sum is in all lanes of the row: lane c keeps the c-th
+        }
+        if (bcol < 4 * KB) turn[i + u][bcol * kAcross + brow] = own;
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 16 / VW; ++i) {
+      const uint32_t m = m0 + sub + i * VW + prow;
+      if (m >= a.M || n0 + pcol >= a.N) continue;
+      const Vector<YT, VW> y = *(const Vector<YT, VW>*)((const YT*)a.y + (long long)m * a.ys + n0 + pcol);
+      Vector<YT, VW> o;
+#pragma unroll
+      for (int c = 0; c < VW; ++c) o.e[c] = (YT)((float)y.e[c] + turn[i * VW + prow][pcol + c]);
+      *(Vector<YT, VW>*)((YT*)a.out + (long long)m * a.os + n0 + pcol) = o;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
 // out = y + s B v for tiles of 16 MB rows and 256 J columns, on the matrix
-// cores with the product transposed: rows of B are the A operand, straight
-// from memory, and their order is chosen so that a lane ends up with 16
-// neighbouring columns of one row, read and written in whole vectors.  v
-// enters as a pair of 16-bit numbers (hi + lo, two products; for fp16 scaled
-// by a power of two per row), so it keeps float32's range and 16 (bf16) or
-// 21 (fp16) bits.  A tile's y is read once and held in float32 while its
-// requests are added, each to its own rows.
+// cores with the product transposed (rows of B are the A operand), so that a
+// lane's four results are neighbouring columns.  v enters as a pair of
+// 16-bit numbers (hi + lo, two products; for fp16 scaled by a power of two
+// per row), so it keeps float32's range and 16 (bf16) or 21 (fp16) bits.
+// The products of a tile's requests are kept in float32, each in its own
+// rows, and leave through the wave's LDS rows, 16 at a time, in the order in
+// which y is read and out written: neighbouring lanes on neighbouring
+// vectors of VW columns (in the products' own order neighbouring lanes would
+// be in 16 different rows, which takes the address unit four times longer).
 template <class T, class YT, int MB, int KB, int VW, int P>
 __global__ __launch_bounds__(256) void expand_tiles_kernel(AdapterArgs a) {
   typedef typename Vec8Of<T>::V V8;
   constexpr int TM = 16 * MB, RP = 32 * KB;
+  typedef Vector<YT, VW> Part;
   constexpr int kRow = RP + 8;  // 16 bytes further per row: the operand reads spread over the banks
-  __shared__ __align__(16) T vhi[TM][kRow], vlo[TM][kRow];
+  constexpr int kPasses = 16 / VW;  // of VW rows each over 16 rows, 64 / VW lanes on a row
+  __shared__ __align__(16) T vpair[2][TM][kRow];
+  T(*const vhi)[kRow] = vpair[0];
+  T(*const vlo)[kRow] = vpair[1];
   __shared__ float up[TM];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r16 = lane & 15, lg = lane >> 4;
-  const uint32_t m0 = blockIdx.x * TM;
-  const int mine = my_request<TM>(a, m0, lane);
+  // B's block of a request and the products' way out share the wave's rows
+  constexpr bool kStaged = KB <= 2;
+  constexpr int kTurn = 16 * 68 * 4, kStage = kStaged ? 64 * kRow * 2 : 0;
+  __shared__ __align__(16) char wave_rows[kWaves][kTurn > kStage ? kTurn : kStage];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, r16 = lane & 15, lg = lane >> 4;
+  float(*const turn)[68] = (float(*)[68])wave_rows[wave];
+  T(*const stage)[kRow] = (T(*)[kRow])wave_rows[wave];
+  constexpr int kLanes = RP / 8, kAcross = 64 / kLanes;  // lanes on a row of B, rows at once
+  const int brow = lane / kLanes, brank = (lane % kLanes) * 8;
+  const int prow = lane / (64 / VW), pcol = (lane % (64 / VW)) * VW;
+  const Place place = place_of(a, (a.M + TM - 1) / TM);
+  if (place.block >= a.blocks) return;
+  const uint32_t m0 = place.tile * TM;
+  const Request mine = request_of<TM>(a, m0, lane);
 
   // v of the tile: the parts of K summed, the adapter's scale applied, split
+  if (Requests::exceed(mine, kRequestsAtMost)) return;  // expand_singles_kernel's
   constexpr int kPer = RP / 8;  // threads on a row, within a wave
   for (int i = threadIdx.x; i < TM * kPer; i += 256) {
     const int row = i / kPer, r0 = (i - row * kPer) * 8;
     const uint32_t m = m0 + row;
-    float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    const int id = m < a.M ? a.ids[m] : -1;
-    const int rank = rank_of(a, id);
-    if (r0 < rank) {
-      const float* const v = a.v + (long long)m * a.R + r0;
-#pragma unroll 4
-      for (int s = 0; s < a.parts; ++s) {
-        const f32x4* const q = (const f32x4*)(v + (long long)s * a.M * a.R);
-        const f32x4 p0 = q[0], p1 = q[1];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[j] += p0[j];
-          f[4 + j] += p1[j];
-        }
-      }
-      const float s = a.scale ? a.scale[id] : 1.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = r0 + j < rank ? f[j] * s : 0.0f;
-    }
+    float f[8];
+    load_v(a, m, r0, __shfl(mine.rank, row), __shfl(mine.scale, row), f);
     int e = 0;
-    if (sizeof(T) == 2 && !__is_same(T, __bf16)) {
+    if (!__is_same(T, __bf16)) {
       float m8 = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) m8 = fmaxf(m8, fabsf(f[j]));
@@ -289,62 +529,95 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(AdapterArgs a) {
   }
   __syncthreads();
 
+  auto order = [] {  // between writes and reads of the wave's rows by other lanes
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
   for (int j = 0; j < a.columns; ++j) {
-    const int n0 = ((int)blockIdx.y * a.columns + j) * 256 + wave * 64;
+    const int n0 = (place.block * a.columns + j) * 256 + wave * 64;
     if (n0 >= a.N) return;
-    const int nl = n0 + lg * 16;  // this lane's 16 columns
-    float f[MB][16];
+    // past the last row or column (N is a multiple of VW) the last one is
+    // read again, so that no load is conditional and none waits for another
+    auto load_y = [&](int mb, Part (&y)[kPasses]) {
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-      const uint32_t m = m0 + mb * 16 + r16;
-      const YT* const y = (const YT*)a.y + (long long)m * a.ys + nl;
-#pragma unroll
-      for (int c = 0; c < 16; c += VW) {
-        struct alignas(VW * sizeof(YT)) {
-          YT e[VW];
-        } v;
-        const bool in = m < a.M && nl + c < a.N;  // N a multiple of VW
-        if (in) v = *(const decltype(v)*)(y + c);
-#pragma unroll
-        for (int i = 0; i < VW; ++i) f[mb][c + i] = in ? (float)v.e[i] : 0.0f;
+      for (int i = 0; i < kPasses; ++i) {
+        const uint32_t m = min(m0 + mb * 16 + i * VW + prow, a.M - 1);
+        y[i] = *(const Part*)((const YT*)a.y + (long long)m * a.ys + min(n0 + pcol, a.N - VW));
       }
-    }
-    // B's rows: slot r16 of block nb is column 16 (r16 / 4) + 4 nb + r16 % 4
+    };
+    auto finish = [&](int mb, const Part (&y)[kPasses]) {  // the products of 16 rows lie in `turn`
+      order();
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const uint32_t m = m0 + mb * 16 + i * VW + prow;
+        float d[VW];
+        if constexpr (VW >= 4) {
+#pragma unroll
+          for (int c = 0; c < VW; c += 4) *(f32x4*)(d + c) = *(const f32x4*)&turn[i * VW + prow][pcol + c];
+        } else {
+          d[0] = turn[i * VW + prow][pcol];
+        }
+        Part o;
+#pragma unroll
+        for (int c = 0; c < VW; ++c) o.e[c] = (YT)((float)y[i].e[c] + d[c]);
+        if (m < a.M && n0 + pcol < a.N) *(Part*)((YT*)a.out + (long long)m * a.os + n0 + pcol) = o;
+      }
+      order();
+    };
+    Part yv[MB][kPasses];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) load_y(mb, yv[mb]);
     u32x4 bf[P][4][KB];
     Requests ld, cp;
     ld.begin(mine);
     cp.begin(mine);
-    bool more = ld.next(a, mine), left = cp.next(a, mine);
+    bool more = ld.next(mine), left = cp.next(mine);
     auto load = [&](int p) {
       if (!more) return;
+      // past the rank v is zero: any vector of the adapter's will do
+      const T* const w = (const T*)a.B + (long long)ld.id * a.N * a.R;
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        const int n = n0 + (r16 >> 2) * 16 + nb * 4 + (r16 & 3);
-        const T* const w = (const T*)a.B + ((long long)ld.id * a.N + n) * a.R;
+      for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
         for (int kk = 0; kk < KB; ++kk) {
-          const int r = kk * 32 + lg * 8;
-          u32x4 v = {0u, 0u, 0u, 0u};
-          if (n < a.N && r < ld.rank) v = *(const u32x4*)(w + r);
-          bf[p][nb][kk] = v;
+          const int n = kStaged ? n0 + (nb * KB + kk) * kAcross + brow : n0 + nb * 16 + r16;
+          const int r = kStaged ? brank : kk * 32 + lg * 8;
+          bf[p][nb][kk] = *(const u32x4*)(w + (long long)min(n, a.N - 1) * a.R + (r < ld.rank ? r : 0));
         }
-      }
-      if (ld.rank & 7) {  // the last vector holds values past the adapter's rank
+      more = ld.next(mine);
+    };
+    f32x4 f[MB][4];  // this lane's row r16 of a block, columns 16 nb + 4 lg + 0 .. 3
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb) f[mb][nb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto add = [&](int p) {
+      if (!left) return;
+      if (cp.rank & 7) {  // a vector holds values past the adapter's rank
 #pragma unroll
         for (int kk = 0; kk < KB; ++kk) {
-          const int left_over = ld.rank - (kk * 32 + lg * 8);  // values of this lane's vector in use
+          const int r = kStaged ? brank : kk * 32 + lg * 8;
+          const int used = cp.rank - (r < cp.rank ? r : 0);  // values of this lane's vector in use
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const uint32_t keep = left_over >= 2 * w + 2 ? 0xffffffffu : left_over == 2 * w + 1 ? 0xffffu : 0u;
+            const uint32_t keep = used >= 2 * w + 2 ? 0xffffffffu : used == 2 * w + 1 ? 0xffffu : 0u;
 #pragma unroll
             for (int nb = 0; nb < 4; ++nb) bf[p][nb][kk][w] &= keep;
           }
         }
       }
-      more = ld.next(a, mine);
-    };
-    auto add = [&](int p) {
-      if (!left) return;
+      if constexpr (kStaged) {
+        // through LDS from the order of memory to the operands'; LDS serves
+        // one wave's accesses in order
+        order();
+#pragma unroll
+        for (int i = 0; i < 4 * KB; ++i) *(u32x4*)&stage[i * kAcross + brow][brank] = bf[p][i / KB][i % KB];
+        order();
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+          for (int kk = 0; kk < KB; ++kk) bf[p][nb][kk] = *(const u32x4*)&stage[nb * 16 + r16][kk * 32 + lg * 8];
+      }
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
         const uint32_t rows = (uint32_t)(cp.rows >> (mb * 16)) & 0xffffu;
@@ -365,106 +638,106 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(AdapterArgs a) {
         const bool own = (rows >> r16) & 1u;
         const float s = up[mb * 16 + r16];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) f[mb][c] = own ? fmaf(acc[c >> 2][c & 3], s, f[mb][c]) : f[mb][c];
+        for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[mb][nb][i] = own ? acc[nb][i] * s : f[mb][nb][i];
       }
-      left = cp.next(a, mine);
+      left = cp.next(mine);
     };
+    while (left) {  // P requests at a time
 #pragma unroll
-    for (int p = 0; p < P; ++p) load(p);
-    while (left) {
+      for (int p = 0; p < P; ++p) load(p);
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        add(p);
-        load(p);
-      }
+      for (int p = 0; p < P; ++p) add(p);
     }
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
-      const uint32_t m = m0 + mb * 16 + r16;
-      YT* const out = (YT*)a.out + (long long)m * a.os + nl;
+      order();
 #pragma unroll
-      for (int c = 0; c < 16; c += VW) {
-        struct alignas(VW * sizeof(YT)) {
-          YT e[VW];
-        } v;
-#pragma unroll
-        for (int i = 0; i < VW; ++i) v.e[i] = (YT)f[mb][c + i];
-        if (m < a.M && nl + c < a.N) *(decltype(v)*)(out + c) = v;
-      }
+      for (int nb = 0; nb < 4; ++nb) *(f32x4*)&turn[r16][nb * 16 + lg * 4] = f[mb][nb];
+      finish(mb, yv[mb]);
     }
   }
 }
 
-// How a call is cut.  Few tokens: a wave per (token, rank) and a thread per
-// (token, column).  More: tiles of 64 rows, or of 16 where 64 would leave
-// compute units without work, and K in parts for the same reason.
+// How a call is cut.
+//   up to kFewTokens: a wave per (token, rank), a thread per (token, column);
+//   up to kSomeTokens: a wave per (4 tokens, 4 ranks), expand in tiles;
+//   more: both in tiles, K in parts that fill the compute units.
 struct Cut {
-  bool tiles;
-  int mb_shrink, mb_expand, parts, k_part, columns;
+  int mb;  // expand's tiles: 16 mb rows (0: rows one by one)
+  int parts, k_part, columns;
 };
 
-Cut cut_of(int64_t M, int64_t K, int64_t N, int64_t rank) {
-  Cut cut, *const c = &cut;
-  c->tiles = M > kRowsAtMost;
-  c->parts = 1;
-  c->k_part = (int)K;
-  c->columns = 1;
-  c->mb_shrink = c->mb_expand = 1;
-  if (!c->tiles) return cut;
-  const int big = rank > 64 ? 2 : 4;
-  c->mb_shrink = (M + 16 * big - 1) / (16 * big) >= kUnits / 4 ? big : 1;
-  const int64_t tiles = (M + 16 * c->mb_shrink - 1) / (16 * c->mb_shrink);
-  int64_t parts = (4 * kUnits + tiles - 1) / tiles;
-  const int64_t round = 32 * kWaves;  // a step of every wave
-  if (parts > (K + 2 * round - 1) / (2 * round)) parts = (K + 2 * round - 1) / (2 * round);
-  if (parts > kPartsAtMost) parts = kPartsAtMost;
-  if (parts < 1) parts = 1;
-  c->k_part = (int)(((K + parts - 1) / parts + round - 1) / round * round);
-  c->parts = (int)((K + c->k_part - 1) / c->k_part);
-  const int64_t across = (N + 255) / 256;
-  c->mb_expand = ((M + 63) / 64) * across >= 4 * kUnits ? 4 : 1;
-  const int64_t work = ((M + 16 * c->mb_expand - 1) / (16 * c->mb_expand)) * across;
-  c->columns = work >= 16 * kUnits ? 4 : work >= 8 * kUnits ? 2 : 1;
-  return cut;
+Cut cut_of(int64_t M, int64_t K, int64_t N) {
+  Cut c = {0, 1, (int)K, 1};
+  if (M > kSomeTokens) {
+    const int64_t tiles = (M + 63) / 64;
+    int64_t parts = (4 * kUnits + tiles - 1) / tiles;
+    if (parts > (K + 511) / 512) parts = (K + 511) / 512;
+    c.k_part = (int)(((K + parts - 1) / parts + 127) / 128 * 128);
+    c.parts = (int)((K + c.k_part - 1) / c.k_part);
+  }
+  if (M > kFewTokens) {
+    const int64_t across = (N + 255) / 256;
+    c.mb = ((M + 63) / 64) * across >= 4 * kUnits ? 4 : 1;
+    const int64_t work = ((M + 16 * c.mb - 1) / (16 * c.mb)) * across;
+    c.columns = work >= 16 * kUnits ? 4 : work >= 8 * kUnits ? 2 : 1;
+  }
+  return c;
 }
 
 template <class T>
-hipError_t launch_shrink(const AdapterArgs& a, int mb, hipStream_t stream) {
-  const dim3 grid((a.M + 16 * mb - 1) / (16 * mb), a.parts), block(256);
-  const int rb = (a.R + 15) / 16;
-  if (mb == 1) {
-    if (rb == 1) shrink_tiles_kernel<T, 1, 1, 8><<<grid, block, 0, stream>>>(a);
-    else if (rb == 2) shrink_tiles_kernel<T, 1, 2, 6><<<grid, block, 0, stream>>>(a);
-    else if (rb <= 4) shrink_tiles_kernel<T, 1, 4, 4><<<grid, block, 0, stream>>>(a);
-    else shrink_tiles_kernel<T, 1, 8, 2><<<grid, block, 0, stream>>>(a);
+hipError_t launch_shrink(const AdapterArgs& a, hipStream_t stream) {
+  const dim3 block(256);
+  if (a.M <= kFewTokens) {
+    shrink_rows_kernel<T, 1, 1><<<dim3(a.M, (a.R + 3) / 4), block, 0, stream>>>(a);
+  } else if (a.M <= kSomeTokens) {
+    shrink_rows_kernel<T, 4, 4><<<dim3((a.M + 3) / 4, (a.R + 15) / 16), block, 0, stream>>>(a);
   } else {
-    if (rb == 1) shrink_tiles_kernel<T, 4, 1, 4><<<grid, block, 0, stream>>>(a);
-    else if (rb == 2) shrink_tiles_kernel<T, 4, 2, 3><<<grid, block, 0, stream>>>(a);
-    else if (rb <= 4) shrink_tiles_kernel<T, 4, 4, 2><<<grid, block, 0, stream>>>(a);
-    else shrink_tiles_kernel<T, 2, 8, 2><<<grid, block, 0, stream>>>(a);
+    const dim3 grid((a.M + 63) / 64, a.parts, 2);
+    const int rb = (a.R + 15) / 16;
+    if (rb == 1) shrink_staged_kernel<T, 1><<<grid, block, 0, stream>>>(a);
+    else if (rb == 2) shrink_staged_kernel<T, 2><<<grid, block, 0, stream>>>(a);
+    else if (rb <= 4) shrink_staged_kernel<T, 4><<<grid, block, 0, stream>>>(a);
+    else shrink_staged_kernel<T, 8><<<grid, block, 0, stream>>>(a);
+  }
+  return hipGetLastError();
+}
+
+template <class T, class YT, int VW, int KB>
+hipError_t launch_expand_kb(AdapterArgs a, int mb, hipStream_t stream) {
+  const auto grid = [&](int rows) {
+    const uint64_t across = a.blocks >= 8 ? (a.blocks + 7) / 8 * 8 : a.blocks;
+    return (a.M + rows - 1) / rows * across;
+  };
+  if (grid(16) >= (1ull << 22)) return hipErrorInvalidConfiguration;  // 2^32 threads: no memory holds such an out
+  constexpr int kInFlight = KB == 1 ? 4 : KB == 2 ? 2 : 1;  // requests whose blocks of B are loaded together
+  if (mb == 1) expand_tiles_kernel<T, YT, 1, KB, VW, kInFlight><<<dim3(grid(16)), dim3(256), 0, stream>>>(a);
+  else expand_tiles_kernel<T, YT, 4, KB, VW, 1><<<dim3(grid(64)), dim3(256), 0, stream>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (mb == 1) {  // few tiles: as many workgroups as there are blocks of columns
+    a.columns = 1;
+    a.blocks = (a.N + 255) / 256;
+    expand_singles_kernel<T, YT, 16, KB, VW><<<dim3(grid(16)), dim3(256), 0, stream>>>(a);
+  } else {
+    expand_singles_kernel<T, YT, 64, KB, VW><<<dim3(grid(16)), dim3(256), 0, stream>>>(a);
   }
   return hipGetLastError();
 }
 
 template <class T, class YT, int VW>
 hipError_t launch_expand(const AdapterArgs& a, int mb, hipStream_t stream) {
-  const dim3 grid((a.M + 16 * mb - 1) / (16 * mb), (a.N + 256 * a.columns - 1) / (256 * a.columns)), block(256);
   const int kb = (a.R + 31) / 32;
-  if (mb == 1) {
-    if (kb == 1) expand_tiles_kernel<T, YT, 1, 1, VW, 4><<<grid, block, 0, stream>>>(a);
-    else if (kb == 2) expand_tiles_kernel<T, YT, 1, 2, VW, 2><<<grid, block, 0, stream>>>(a);
-    else expand_tiles_kernel<T, YT, 1, 4, VW, 1><<<grid, block, 0, stream>>>(a);
-  } else {
-    if (kb == 1) expand_tiles_kernel<T, YT, 4, 1, VW, 1><<<grid, block, 0, stream>>>(a);
-    else if (kb == 2) expand_tiles_kernel<T, YT, 4, 2, VW, 1><<<grid, block, 0, stream>>>(a);
-    else expand_tiles_kernel<T, YT, 4, 4, VW, 1><<<grid, block, 0, stream>>>(a);
-  }
-  return hipGetLastError();
+  if (kb == 1) return launch_expand_kb<T, YT, VW, 1>(a, mb, stream);
+  if (kb == 2) return launch_expand_kb<T, YT, VW, 2>(a, mb, stream);
+  return launch_expand_kb<T, YT, VW, 4>(a, mb, stream);
 }
 
 template <class T, class YT>
 hipError_t launch_y(AdapterArgs& a, const Cut& c, hipStream_t stream) {
-  if (!c.tiles) {
+  if (c.mb == 0) {
     expand_rows_kernel<T, YT><<<dim3(a.M, (a.N + 255) / 256), dim3(256), 0, stream>>>(a);
     return hipGetLastError();
   }
@@ -474,20 +747,14 @@ hipError_t launch_y(AdapterArgs& a, const Cut& c, hipStream_t stream) {
            aligned_to(a.out, w * (int)sizeof(YT) > 16 ? 16 : w * (int)sizeof(YT));
   };
   constexpr int kWide = 16 / sizeof(YT);  // elements of 16 bytes
-  if (whole(kWide)) return launch_expand<T, YT, kWide>(a, c.mb_expand, stream);
-  if (kWide > 4 && whole(4)) return launch_expand<T, YT, 4>(a, c.mb_expand, stream);
-  return launch_expand<T, YT, 1>(a, c.mb_expand, stream);
+  if (whole(kWide)) return launch_expand<T, YT, kWide>(a, c.mb, stream);
+  if (kWide > 4 && whole(4)) return launch_expand<T, YT, 4>(a, c.mb, stream);
+  return launch_expand<T, YT, 1>(a, c.mb, stream);
 }
 
 template <class T>
 hipError_t launch(AdapterArgs& a, const Cut& c, int y_dtype, hipStream_t stream) {
-  hipError_t e;
-  if (c.tiles) {
-    e = launch_shrink<T>(a, c.mb_shrink, stream);
-  } else {
-    shrink_rows_kernel<T><<<dim3(a.M, (a.R + 3) / 4), dim3(256), 0, stream>>>(a);
-    e = hipGetLastError();
-  }
+  const hipError_t e = launch_shrink<T>(a, stream);
   if (e != hipSuccess) return e;
   switch (y_dtype) {
     case ORBIT_BF16: return launch_y<T, __bf16>(a, c, stream);
@@ -504,7 +771,7 @@ bool sizes_ok(int64_t M, int64_t K, int64_t rank) {
 
 extern "C" int64_t orbit_adapter_workspace(int64_t M, int64_t K, int64_t rank) {
   if (!sizes_ok(M, K, rank)) return -1;
-  return M * rank * 4 * cut_of(M, K, 1, rank).parts;
+  return M * rank * 4 * cut_of(M, K, 1).parts;
 }
 
 extern "C" orbit_status orbit_adapter_add(const orbit_adapter_args* p, hipStream_t stream) {
@@ -542,9 +809,10 @@ extern "C" orbit_status orbit_adapter_add(const orbit_adapter_args* p, hipStream
   a.K = (int)p->K;
   a.N = (int)p->N;
   a.R = (int)p->rank;
-  const Cut c = cut_of(p->M, p->K, p->N, p->rank);
+  const Cut c = cut_of(p->M, p->K, p->N);
   a.parts = c.parts;
   a.k_part = c.k_part;
   a.columns = c.columns;
+  a.blocks = (a.N + 256 * c.columns - 1) / (256 * c.columns);
   return hip_status(p->x_dtype == ORBIT_BF16 ? launch<__bf16>(a, c, p->y_dtype, stream) : launch<_Float16>(a, c, p->y_dtype, stream));
 }

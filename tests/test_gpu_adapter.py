@@ -108,6 +108,24 @@ def test_every_order_of_requests(gpu_lib, order, M):
     _run(gpu_lib, M, M, 320, 264, 32, L, ids, xt="f16")
 
 
+@pytest.mark.parametrize("M", [2047, 2049, 2500, 4113])
+@pytest.mark.parametrize("R,K,xt", [(16, 200, "bf16"), (24, 1032, "f16"), (64, 520, "bf16"), (104, 136, "f16")])
+def test_many_tokens(gpu_lib, M, R, K, xt):
+    rng = np.random.default_rng(M + R)
+    L, N = 70, 72
+    ranks = [int(r) for r in rng.integers(0, R + 1, L)]
+    long_runs = sorted(int(i) for i in rng.integers(-1, 5, M - 200))
+    ids = long_runs + [int(i) for i in rng.integers(-1, L, 200)]  # prompts, then single tokens
+    _run(gpu_lib, M, M, K, N, R, L, ids, xt=xt, ranks=ranks)
+
+
+def test_many_tokens_into_wide_rows(gpu_lib):
+    rng = np.random.default_rng(1)
+    for N in (1001, 2052, 4096):  # tiles of 64 rows and of 16; single elements, fours, eights
+        for order in (sorted(int(i) for i in rng.integers(-1, 3, 2100)), [m % 33 for m in range(2100)]):
+            _run(gpu_lib, N, 2100, 64, N, 16, 33, order, ranks=[16 - i % 9 for i in range(33)])
+
+
 def test_no_scale_no_ranks_no_adapters(gpu_lib):
     _run(gpu_lib, 1, 20, 128, 64, 8, 2, [0, 1] * 10, scale=False)
     x = torch.ones(4, 128, device="cuda", dtype=torch.bfloat16)

@@ -495,7 +495,8 @@ orbit_status orbit_paged_attention(const orbit_paged_attention_args *args, hipSt
  * ones.  Host only. */
 int64_t orbit_paged_attention_workspace(int64_t batch, int64_t q_heads, int64_t kv_heads,
                                         int64_t head_dim, int64_t page_size,
-                                        int64_t table_width, int64_t window);
+                                        int64_t table_width, int64_t window,
+                                        int32_t format);
 
 #ifdef __cplusplus
 }

@@ -95,7 +95,7 @@ def _load():
         "orbit_kv_append": ([P, P], ctypes.c_int),
         "orbit_kv_read": ([P, P, I64, P, P, ctypes.c_int, P], ctypes.c_int),
         "orbit_paged_attention": ([P, P], ctypes.c_int),
-        "orbit_paged_attention_workspace": ([I64] * 7, I64),
+        "orbit_paged_attention_workspace": ([I64] * 7 + [I32], I64),
     }
     for name, (args, res) in sig.items():
         try:
@@ -658,7 +658,7 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, *, scale=None, wi
         if not out.is_contiguous():
             raise OrbitError("out must be contiguous")
     lse = q.new_empty((batch, H), dtype=torch.float32) if return_lse else None
-    ws = lib.orbit_paged_attention_workspace(batch, H, cache[6], dim, cache[5], width, window)
+    ws = lib.orbit_paged_attention_workspace(batch, H, cache[6], dim, cache[5], width, window, cache[8])
     if ws < 0:
         raise OrbitError(f"orbit_paged_attention: invalid shape (batch {batch}, {H} query heads on "
                          f"{cache[6]}, dim {dim}, window {window})")

@@ -107,6 +107,14 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int kTile = 32;
 constexpr int kWaves = 4;
 
+// Workgroups per compute unit (waves per SIMD) that the kernel's registers
+// allow; 0: the compiler's choice.  More spill: at 128 coordinates an int8
+// cache took 165 us at two, 141 at three, 142 at four (spilling).
+constexpr int residents(int format, int dp, bool paged16) {
+  if (format == ORBIT_KV_INT8) return dp == 64 ? 4 : dp == 128 ? 3 : 2;
+  return dp == 64 ? 4 : dp == 128 && paged16 ? 3 : 1;
+}
+
 template <int DP>
 struct Stage {
   // four rows apart a quarter of the banks apart, so that the transposing
@@ -115,10 +123,30 @@ struct Stage {
   static constexpr int kWaveElems = kTile * kStride;
 };
 
+// Two probabilities as a hi + lo pair of 16-bit numbers.  fp16: both parts
+// rounded toward zero (one instruction for two), 20 bits together.
+__device__ __forceinline__ void split2(float p0, float p1, bf16x8& hi, bf16x8& lo, int j) {
+  hi[j] = (__bf16)p0;
+  hi[j + 1] = (__bf16)p1;
+  lo[j] = (__bf16)(p0 - (float)hi[j]);
+  lo[j + 1] = (__bf16)(p1 - (float)hi[j + 1]);
+}
+__device__ __forceinline__ void split2(float p0, float p1, f16x8& hi, f16x8& lo, int j) {
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  const h2 h = __builtin_bit_cast(h2, __builtin_amdgcn_cvt_pkrtz(p0, p1));
+  const h2 l = __builtin_bit_cast(h2, __builtin_amdgcn_cvt_pkrtz(p0 - (float)h[0], p1 - (float)h[1]));
+  hi[j] = h[0];
+  hi[j + 1] = h[1];
+  lo[j] = l[0];
+  lo[j + 1] = l[1];
+}
+
 // Q: the queries' format (BF16 or F16); F: the cache's; DP: head_dim rounded
-// up to 64, 128 or 256.
-template <int Q, int F, int DP>
-__global__ __launch_bounds__(256) void attend_kernel(AttentionArgs a) {
+// up to 64, 128 or 256; PAGED16: pages of 16 tokens or more, so that half a
+// tile lies in one page and its address is the wave's (scalar registers)
+// plus a lane's constant; smaller pages take an address per row.
+template <int Q, int F, int DP, bool PAGED16>
+__global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(AttentionArgs a) {
   constexpr bool kCoded = F == ORBIT_KV_INT8;
   typedef Mma<F> M;
   typedef typename M::T T;
@@ -136,7 +164,7 @@ __global__ __launch_bounds__(256) void attend_kernel(AttentionArgs a) {
   constexpr int kSumBytes = kWaves * 16 * DP * 4 + kWaves * 16 * 8;
   __shared__ __align__(16) char lds[kStageBytes > kSumBytes ? kStageBytes : kSumBytes];
 
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r16 = lane & 15, lg = lane >> 4;
   const int head = blockIdx.x / a.head_blocks, hb = blockIdx.x - head * a.head_blocks;
   const int b = blockIdx.y;
@@ -195,65 +223,104 @@ __global__ __launch_bounds__(256) void attend_kernel(AttentionArgs a) {
       for (int j = 0; j < 8; ++j) qf[s][j] = (T)f[s][j];
   }
 
+  // Loads are unconditional, so that none waits for another: tokens that are
+  // not seen read page 0 (or the rest of their own page), coordinates past
+  // head_dim the row's last vector again; scores of the former are masked and
+  // their values cleared, the latter meet zeros of the queries or are results
+  // that are not stored.
   u32x4 kr[2][kLoads];
   u32x4 vr[kVLoads];
   u32x2 ksr[2], vsr[2];
-  uint32_t live = 0;  // bit t: token t of the tile is seen (and its page lies in the cache)
+  const int row_bytes = dim * kElem;
+  const uint32_t page_bytes = (uint32_t)row_bytes << a.c.page_shift;  // of one head
+  int koff[kLoads];
+#pragma unroll
+  for (int s = 0; s < kLoads; ++s) koff[s] = (PAGED16 ? r16 * row_bytes : 0) + min(s * 64 + lg * 16, row_bytes - 16);
+  const int vcol = min((lane & (kRowLanes - 1)) * 16, row_bytes - 16);
+  const int voff = (PAGED16 ? lane / kRowLanes * row_bytes : 0) + vcol;
 
-  // page of token tile + (lane & 31), or ~0
-  auto look_up = [&](int tile) -> uint32_t {
-    const int t = tile + (lane & 31);
-    uint32_t page = 0xffffffffu;
-    if (t >= span.lo && t < c1) page = (uint32_t)table[t >> a.c.page_shift];
-    return page < a.c.pages ? page : 0xffffffffu;
+  // The pages of a tile and which of its tokens are seen (bit t: token t).
+  struct Pages {
+    uint32_t page[PAGED16 ? 2 : 1];  // of each half; or of token (lane & 31)
+    uint32_t live;
   };
-  auto row_at = [&](uint32_t page, int t) -> long long {
-    return cache_row(a.c, page, head, (uint32_t)t & a.c.page_mask);
+  auto look_up = [&](int tile) {
+    Pages p;
+    p.live = 0;
+    p.page[0] = 0;
+    if constexpr (PAGED16) {
+      p.page[1] = 0;
+      if (tile < c1) {
+        uint32_t live = 0xffffffffu;
+        if (tile < span.lo) live <<= span.lo - tile;
+        if (tile + 32 > c1) live &= (1u << (c1 - tile)) - 1u;
+        p.page[0] = __builtin_amdgcn_readfirstlane((uint32_t)table[tile >> a.c.page_shift]);
+        p.page[1] = tile + 16 < c1 ? __builtin_amdgcn_readfirstlane((uint32_t)table[(tile + 16) >> a.c.page_shift]) : 0u;
+        if (p.page[0] >= a.c.pages) {
+          live &= 0xffff0000u;
+          p.page[0] = 0;
+        }
+        if (p.page[1] >= a.c.pages) {
+          live &= 0xffffu;
+          p.page[1] = 0;
+        }
+        p.live = live;
+      }
+    } else {
+      const int t = tile + (lane & 31);
+      uint32_t page = 0xffffffffu;
+      if (t >= span.lo && t < c1) page = (uint32_t)table[t >> a.c.page_shift];
+      p.live = (uint32_t)__ballot(page < a.c.pages);
+      p.page[0] = page < a.c.pages ? page : 0u;
+    }
+    return p;
   };
-  auto load_keys = [&](int tile, uint32_t page) {
+  // The first byte of a head's part of a page, of its scales.
+  auto head_of = [&](uint32_t page) { return ((uint64_t)page * a.c.kv_heads + head) * page_bytes; };
+  auto load_keys = [&](int tile, const Pages& p) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int at = half * 16 + r16;
-      const uint32_t pg = (uint32_t)__shfl((int)page, at);
-      const char* const row = a.c.k + row_at(pg, tile + at) * (dim * kElem);
+      if constexpr (PAGED16) {
+        const uint32_t off = (uint32_t)(tile + half * 16) & a.c.page_mask;
+        const char* const at = a.c.k + head_of(p.page[half]) + off * (uint32_t)row_bytes;
 #pragma unroll
-      for (int s = 0; s < kLoads; ++s) {
-        const int off = s * 64 + lg * 16;  // bytes
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (pg != 0xffffffffu && off < dim * kElem) v = *(const u32x4*)(row + off);
-        kr[half][s] = v;
-      }
-    }
-    if (kCoded) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        // four neighbouring tokens lie in one page (page_size >= 4); a page
-        // is known where any of the four is seen
-        const int at = half * 16 + lg * 4;
-        uint32_t pg = (uint32_t)__shfl((int)page, at);
-#pragma unroll
-        for (int i = 1; i < 4; ++i) {
-          const uint32_t o = (uint32_t)__shfl((int)page, at + i);
-          pg = pg != 0xffffffffu ? pg : o;
+        for (int s = 0; s < kLoads; ++s) kr[half][s] = *(const u32x4*)(at + koff[s]);
+        if constexpr (kCoded) {
+          const uint64_t row = (((uint64_t)p.page[half] * a.c.kv_heads + head) << a.c.page_shift) + off;
+          ksr[half] = *(const u32x2*)(a.c.ks + row + lg * 4);
+          vsr[half] = *(const u32x2*)(a.c.vs + row + lg * 4);
         }
-        ksr[half] = vsr[half] = u32x2{0u, 0u};
-        if (pg != 0xffffffffu) {
-          const long long row = row_at(pg, tile + at);
+      } else {
+        const int t = half * 16 + r16;
+        const uint32_t page = (uint32_t)__shfl((int)p.page[0], t);
+        const char* const at = a.c.k + head_of(page) + ((uint32_t)(tile + t) & a.c.page_mask) * (uint32_t)row_bytes;
+#pragma unroll
+        for (int s = 0; s < kLoads; ++s) kr[half][s] = *(const u32x4*)(at + koff[s]);
+        if constexpr (kCoded) {
+          // four neighbouring tokens lie in one page (page_size >= 4), whose
+          // number the first that is seen has
+          const int t4 = half * 16 + lg * 4;
+          const uint32_t four = (p.live >> t4) & 15u;
+          const uint32_t pg = (uint32_t)__shfl((int)p.page[0], t4 + (four ? __builtin_ctz(four) : 0));
+          const uint64_t row = (((uint64_t)pg * a.c.kv_heads + head) << a.c.page_shift) + ((uint32_t)(tile + t4) & a.c.page_mask);
           ksr[half] = *(const u32x2*)(a.c.ks + row);
           vsr[half] = *(const u32x2*)(a.c.vs + row);
         }
       }
     }
   };
-  auto load_values = [&](int tile, uint32_t page) {
-    const int off = (lane & (kRowLanes - 1)) * 16;  // bytes
+  auto load_values = [&](int tile, const Pages& p) {
 #pragma unroll
     for (int i = 0; i < kVLoads; ++i) {
-      const int at = i * kRowsAtOnce + lane / kRowLanes;
-      const uint32_t pg = (uint32_t)__shfl((int)page, at);
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if (pg != 0xffffffffu && off < dim * kElem) v = *(const u32x4*)(a.c.v + row_at(pg, tile + at) * (dim * kElem) + off);
-      vr[i] = v;
+      if constexpr (PAGED16) {
+        const int half = i * 2 / kVLoads;
+        const uint32_t off = ((uint32_t)(tile + half * 16) & a.c.page_mask) + (i - half * (kVLoads / 2)) * kRowsAtOnce;
+        vr[i] = *(const u32x4*)(a.c.v + head_of(p.page[half]) + off * (uint32_t)row_bytes + voff);
+      } else {
+        const int t = i * kRowsAtOnce + lane / kRowLanes;
+        const uint32_t page = (uint32_t)__shfl((int)p.page[0], t);
+        vr[i] = *(const u32x4*)(a.c.v + head_of(page) + ((uint32_t)(tile + t) & a.c.page_mask) * (uint32_t)row_bytes + voff);
+      }
     }
   };
 
@@ -265,14 +332,13 @@ __global__ __launch_bounds__(256) void attend_kernel(AttentionArgs a) {
 
   int tile = c0 + wave * kTile;
   if (tile < c1) {
-    uint32_t page = look_up(tile);
-    load_keys(tile, page);
-    load_values(tile, page);
-    live = (uint32_t)__ballot(page != 0xffffffffu);
     constexpr int kStep = kWaves * kTile;
-    uint32_t next = tile + kStep < c1 ? look_up(tile + kStep) : 0xffffffffu;
+    Pages now = look_up(tile);
+    load_keys(tile, now);
+    load_values(tile, now);
+    Pages next = look_up(tile + kStep);
     for (; tile < c1; tile += kStep) {
-      const bool more = tile + kStep < c1;
+      const uint32_t live = now.live;
       // scores of the tile
       f32x4 s[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
@@ -314,11 +380,10 @@ __global__ __launch_bounds__(256) void attend_kernel(AttentionArgs a) {
           if constexpr (kCoded) vs[j] = seen ? vs[j] : 0.0f;
         }
       }
-      const uint32_t page_now = next;
-      if (more) {
-        load_keys(tile + kStep, page_now);
-        next = tile + 2 * kStep < c1 ? look_up(tile + 2 * kStep) : 0xffffffffu;
-      }
+      // past the end page 0 is read, and never used
+      now = next;
+      load_keys(tile + kStep, now);
+      next = look_up(tile + 2 * kStep);
 
       // running maximum (of z + log2(scale) where values carry one) and sums
       float mt = -__builtin_inff();
@@ -328,24 +393,33 @@ __global__ __launch_bounds__(256) void attend_kernel(AttentionArgs a) {
         else mt = fmaxf(mt, z[j]);
       }
       mt = max_rows32(max_rows16(mt));
-      const float m_new = fmaxf(m_run, mt);
-      const float m_use = m_new == -__builtin_inff() ? 0.0f : m_new;
-      const float alpha = __builtin_amdgcn_exp2f(m_run - m_use);
-      m_run = m_new;
-      l_run *= alpha;
+      if (__any(mt > m_run)) {
+        const float m_new = fmaxf(m_run, mt);
+        const float alpha = __builtin_amdgcn_exp2f(m_run - (m_new == -__builtin_inff() ? 0.0f : m_new));
+        m_run = m_new;
+        l_run *= alpha;
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d) o[d] *= alpha;
+      }
+      const float m_use = m_run == -__builtin_inff() ? 0.0f : m_run;
       V8 hi, lo;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float p = __builtin_amdgcn_exp2f(z[j] - m_use);
-        l_run += p;
-        if constexpr (kCoded) p *= vs[j];
-        hi[j] = (T)p;
-        lo[j] = (T)(p - (float)hi[j]);
+      for (int j = 0; j < 8; j += 2) {
+        float p0 = __builtin_amdgcn_exp2f(z[j] - m_use), p1 = __builtin_amdgcn_exp2f(z[j + 1] - m_use);
+        l_run += p0 + p1;
+        if constexpr (kCoded) {
+          p0 *= vs[j];
+          p1 *= vs[j + 1];
+        }
+        split2(p0, p1, hi, lo, j);
       }
-#pragma unroll
-      for (int d = 0; d < kBlocks; ++d) o[d] *= alpha;
 
       // values to the wave's rows (LDS serves one wave's accesses in order)
+      if (live != 0xffffffffu) {
+#pragma unroll
+        for (int i = 0; i < kVLoads; ++i)
+          vr[i] = (live >> (i * kRowsAtOnce + lane / kRowLanes)) & 1u ? vr[i] : u32x4{0u, 0u, 0u, 0u};
+      }
       {
         const int e0 = (lane & (kRowLanes - 1)) * (kCoded ? 16 : 8);
 #pragma unroll
@@ -362,10 +436,7 @@ __global__ __launch_bounds__(256) void attend_kernel(AttentionArgs a) {
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      if (more) {
-        load_values(tile + kStep, page_now);
-        live = (uint32_t)__ballot(page_now != 0xffffffffu);
-      }
+      load_values(tile + kStep, now);
       {
         typedef __attribute__((address_space(3))) s16x4* lds_ptr;
         const T* const at = stage + (lg * 4 + (r16 >> 2)) * Stage<DP>::kStride + (r16 & 3) * 4;
@@ -495,9 +566,15 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a) {
 template <int Q, int F>
 hipError_t launch_attend(const AttentionArgs& a, dim3 grid, hipStream_t stream) {
   const int dim = a.c.head_dim;
-  if (dim <= 64) attend_kernel<Q, F, 64><<<grid, dim3(256), 0, stream>>>(a);
-  else if (dim <= 128) attend_kernel<Q, F, 128><<<grid, dim3(256), 0, stream>>>(a);
-  else attend_kernel<Q, F, 256><<<grid, dim3(256), 0, stream>>>(a);
+  if (a.c.page_shift >= 4) {
+    if (dim <= 64) attend_kernel<Q, F, 64, true><<<grid, dim3(256), 0, stream>>>(a);
+    else if (dim <= 128) attend_kernel<Q, F, 128, true><<<grid, dim3(256), 0, stream>>>(a);
+    else attend_kernel<Q, F, 256, true><<<grid, dim3(256), 0, stream>>>(a);
+  } else {
+    if (dim <= 64) attend_kernel<Q, F, 64, false><<<grid, dim3(256), 0, stream>>>(a);
+    else if (dim <= 128) attend_kernel<Q, F, 128, false><<<grid, dim3(256), 0, stream>>>(a);
+    else attend_kernel<Q, F, 256, false><<<grid, dim3(256), 0, stream>>>(a);
+  }
   return hipGetLastError();
 }
 

@@ -134,9 +134,9 @@ def test_null_structs():
 
 def test_attention_workspace_of_invalid_sizes():
     f = rbp.lib.orbit_paged_attention_workspace
-    assert f(0, 8, 2, 128, 16, 100, 0) == 0 and f(1, 8, 2, 128, 16, 4096, 0) > 0
-    for bad in ((-1, 8, 2, 128, 16, 1, 0), (1, 7, 2, 128, 16, 1, 0), (1, 8, 2, 100, 16, 1, 0), (1, 8, 2, 128, 0, 1, 0),
-                (1, 8, 2, 128, 16, -1, 0), (1, 8, 2, 128, 16, 1, -1)):
+    assert f(0, 8, 2, 128, 16, 100, 0, 1) == 0 and f(1, 8, 2, 128, 16, 4096, 0, 3) > 0
+    for bad in ((-1, 8, 2, 128, 16, 1, 0, 1), (1, 7, 2, 128, 16, 1, 0, 1), (1, 8, 2, 100, 16, 1, 0, 1), (1, 8, 2, 128, 0, 1, 0, 1),
+                (1, 8, 2, 128, 16, -1, 0, 1), (1, 8, 2, 128, 16, 1, -1, 1), (1, 8, 2, 128, 16, 1, 0, 0)):
         assert f(*bad) == -1
 
 

@@ -9,11 +9,9 @@
 // so a head is a group of D / 8 lanes (a power of two of them, the rest
 // idle) and a wave holds several heads; the Hadamard transform is three
 // register stages and log2(D / 8) exchanges between lanes of the group, the
-// row maximum one reduction over it.  A workgroup takes one token (or
-// several, if they have few heads): its cosines and sines are loaded once
-// and serve every head, each lane keeping the eight pairs it needs.  The
-// other half of a pair (x[i + rot/2]) is loaded a second time rather than
-// exchanged: the line is in L1, and any rot_dim works alike.
+// row maximum one reduction over it.  The other half of a pair (x[i + rot/2])
+// is loaded a second time rather than exchanged: the line is in L1, and any
+// rot_dim works alike.
 #include "kv_cache.h"
 
 using namespace orbit;
@@ -32,7 +30,7 @@ struct AppendArgs {
   uint32_t tokens;
   int q_heads, tasks, tokens_per_block;
   int rot, half, interleaved, hadamard;
-  int vec, vec_pair, vec_table;  // rows, half-split partners and table rows in 16-byte words
+  int vec;  // rows, partners and table rows in 16-byte words
 };
 
 template <class T>
@@ -101,158 +99,151 @@ __device__ __forceinline__ void put(char* base, long long row, int dim, int e0, 
   *(Vec8<CT>*)((CT*)base + row * dim + e0) = o;
 }
 
-template <class IT, class CT, int LPH>
+// A group of LPH lanes takes one head of one token: blockIdx.y the heads in
+// pieces of 256 / LPH, or a workgroup several tokens where they have fewer.
+// VEC: rows, partners and table rows in 16-byte words.  One head per group
+// and not several in turn: the fewer registers keep twice the waves in
+// flight, which is what hides the chain position -> cosines -> result
+// (16384 tokens of 32 + 8 + 8 heads: two heads in turn 119 us, three with all
+// all their loads ahead 214, one with the wave's registers below 64: see the
+// launch).
+template <class IT, class CT, int LPH, bool VEC>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
   constexpr int kGroups = 256 / LPH;
-  constexpr int kAtOnce = 2;  // heads in flight per group
   const int lane = threadIdx.x & (LPH - 1), grp = threadIdx.x / LPH;
   const int dim = a.c.head_dim, e0 = lane * 8;
-  int task = grp;
+  int t = (int)blockIdx.y * kGroups + grp;
   uint32_t token = blockIdx.x;
   if (a.tokens_per_block > 1) {
     const int sub = grp / a.tasks;
-    task = grp - sub * a.tasks;
+    t = grp - sub * a.tasks;
     if (sub >= a.tokens_per_block) return;
     token = blockIdx.x * (uint32_t)a.tokens_per_block + sub;
   }
-  if (token >= a.tokens || e0 >= dim) return;
-
+  if (token >= a.tokens || t >= a.tasks || e0 >= dim) return;
+  const int last_k = a.q_heads + a.c.kv_heads;
+  const bool turned = a.cos_sin && t < last_k;  // this head takes the position rotation
+  const bool rotated = turned && e0 < a.rot;    // and these coordinates
   const long long slot = a.slots[token];
-  const bool rotated = e0 < a.rot;
-  bool known = true;
-  float cs[8], sn[8];
-  if (a.cos_sin) {
-    const long long pos = a.positions[token];
-    known = pos >= 0 && pos < a.table_len;
-    const float* row = a.cos_sin + (known ? pos : 0) * (long long)a.rot;
-    if (rotated) {
-      if (a.vec_table && !a.interleaved) {
-        const int i0 = e0 < a.half ? e0 : e0 - a.half;
-        *(f32x4*)cs = *(const f32x4*)(row + i0);
-        *(f32x4*)(cs + 4) = *(const f32x4*)(row + i0 + 4);
-        *(f32x4*)sn = *(const f32x4*)(row + a.half + i0);
-        *(f32x4*)(sn + 4) = *(const f32x4*)(row + a.half + i0 + 4);
-      } else {
+  const long long pos = a.cos_sin ? a.positions[token] : 0;
+
+  const IT* p = t < a.q_heads ? (const IT*)a.q + token * a.qts + t * a.qhs
+                : t < last_k  ? (const IT*)a.k + token * a.kts + (t - a.q_heads) * a.khs
+                              : (const IT*)a.v + token * a.vts + (t - last_k) * a.vhs;
+  const Vec8<IT> own = load8<IT>(p + e0, VEC);
+  Vec8<IT> pair;
+  if (rotated && !a.interleaved) {
+    if constexpr (VEC) {
+      pair = load8<IT>(p + (e0 < a.half ? e0 + a.half : e0 - a.half), true);
+    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = e0 + j;
-          const int i = a.interleaved ? e >> 1 : (e < a.half ? e : e - a.half);
-          cs[j] = e < a.rot ? row[i] : 1.0f;
-          sn[j] = e < a.rot ? row[a.half + i] : 0.0f;
-        }
+      for (int j = 0; j < 8; ++j) {
+        const int e = e0 + j;
+        pair.e[j] = e < a.half ? p[e + a.half] : e < a.rot ? p[e - a.half] : (IT)0.0f;
       }
     }
   }
-  const long long room = (long long)a.c.pages << a.c.page_shift;
-  const bool kept = slot >= 0 && slot < room && known;
-  const uint32_t page = kept ? (uint32_t)slot >> a.c.page_shift : 0u;
-  const uint32_t off = (uint32_t)slot & a.c.page_mask;
-  const int kv = a.c.kv_heads, last_k = a.q_heads + kv;
-
-  for (int t0 = task; t0 < a.tasks; t0 += kAtOnce * kGroups) {
-    Vec8<IT> own[kAtOnce], pair[kAtOnce];
+  const bool known = !a.cos_sin || (pos >= 0 && pos < a.table_len);
+  float f[8];
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      const int t = t0 + u * kGroups;
-      if (t >= a.tasks) continue;
-      const IT* p = t < a.q_heads ? (const IT*)a.q + token * a.qts + t * a.qhs
-                    : t < last_k  ? (const IT*)a.k + token * a.kts + (t - a.q_heads) * a.khs
-                                  : (const IT*)a.v + token * a.vts + (t - last_k) * a.vhs;
-      own[u] = load8<IT>(p + e0, a.vec);
-      if (a.cos_sin && rotated && !a.interleaved && t < last_k) {
-        if (a.vec_pair) {
-          pair[u] = load8<IT>(p + (e0 < a.half ? e0 + a.half : e0 - a.half), true);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int e = e0 + j;
-            pair[u].e[j] = e < a.half ? p[e + a.half] : e < a.rot ? p[e - a.half] : (IT)0.0f;
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      const int t = t0 + u * kGroups;
-      if (t >= a.tasks) continue;
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = (float)own[u].e[j];
-      if (t < last_k) {
-        if (a.cos_sin && rotated) {
-          if (a.interleaved) {
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              const float x = f[j], y = f[j + 1];
-              f[j] = x * cs[j] - y * sn[j];
-              f[j + 1] = x * sn[j] + y * cs[j];
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float s = e0 + j < a.half ? -sn[j] : sn[j];
-              f[j] = f[j] * cs[j] + (float)pair[u].e[j] * s;
-            }
-          }
-        }
-        if (a.hadamard) hadamard<LPH>(f, lane, dim);
-      }
-      if (t < a.q_heads) {
-        if (!known) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = __builtin_nanf("");
-        }
-        put<IT>(a.q_out, (long long)token * a.q_heads + t, dim, e0, f);
-        continue;
-      }
-      if (!kept) continue;
-      const bool key = t < last_k;
-      const long long row = cache_row(a.c, page, key ? t - a.q_heads : t - last_k, off);
-      char* const base = key ? a.c.k : a.c.v;
-      if constexpr (sizeof(CT) == 1) {
-        // bit patterns of |x| order like the values, infinities and NaN last
-        unsigned m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const unsigned b = __builtin_bit_cast(unsigned, f[j]) & 0x7fffffffu;
-          m = m > b ? m : b;
-        }
-        // a group's idle lanes hold no part of the head; they have left, so
-        // the exchanges stay below the lanes in use
-        const int used = dim >> 3;
-        const bool whole = (used & (used - 1)) == 0;
-        if (whole) {
-          if (used > 1) m = umax_xor<1>(m);
-          if (used > 2) m = umax_xor<2>(m);
-          if (used > 4) m = umax_xor<4>(m);
-          if (LPH > 8 && used > 8) m = umax_xor<8>(m);
-          if (LPH > 16 && used > 16) m = umax_xor<16>(m);
-        } else {
-          const int first = (threadIdx.x & 63) & ~(LPH - 1);
-          unsigned all = 0;
-          for (int l = 0; l < used; ++l) {
-            const unsigned o = (unsigned)__shfl((int)m, first + l);
-            all = all > o ? all : o;
-          }
-          m = all;
-        }
-        const _Float16 scale = (_Float16)(__builtin_bit_cast(float, m) / 127.0f);
-        const float s = (float)scale;
-        union {
-          signed char b[8];
-          u32x2 w;
-        } o;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float q = s == 0.0f ? 0.0f : rintf(f[j] / s);
-          o.b[j] = (signed char)(int)fminf(fmaxf(q, -127.0f), 127.0f);
-        }
-        *(u32x2*)(base + row * dim + e0) = o.w;
-        if (lane == 0) (key ? a.c.ks : a.c.vs)[row] = scale;
+  for (int j = 0; j < 8; ++j) f[j] = (float)own.e[j];
+  if (rotated) {
+    const float* row = a.cos_sin + (known ? pos : 0) * (long long)a.rot;
+    if (a.interleaved) {
+      float c[4], s[4];
+      if constexpr (VEC) {
+        *(f32x4*)c = *(const f32x4*)(row + (e0 >> 1));
+        *(f32x4*)s = *(const f32x4*)(row + a.half + (e0 >> 1));
       } else {
-        put<CT>(base, row, dim, e0, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool in = e0 + 2 * j < a.rot;
+          c[j] = in ? row[(e0 >> 1) + j] : 1.0f;
+          s[j] = in ? row[a.half + (e0 >> 1) + j] : 0.0f;
+        }
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = f[2 * j], y = f[2 * j + 1];
+        f[2 * j] = x * c[j] - y * s[j];
+        f[2 * j + 1] = x * s[j] + y * c[j];
+      }
+    } else {
+      float c[8], s[8];
+      if constexpr (VEC) {
+        const int i0 = e0 < a.half ? e0 : e0 - a.half;
+        *(f32x4*)c = *(const f32x4*)(row + i0);
+        *(f32x4*)(c + 4) = *(const f32x4*)(row + i0 + 4);
+        *(f32x4*)s = *(const f32x4*)(row + a.half + i0);
+        *(f32x4*)(s + 4) = *(const f32x4*)(row + a.half + i0 + 4);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int e = e0 + j, i = e < a.half ? e : e - a.half;
+          c[j] = e < a.rot ? row[i] : 1.0f;
+          s[j] = e < a.rot ? row[a.half + i] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = f[j] * c[j] + (float)pair.e[j] * (e0 + j < a.half ? -s[j] : s[j]);
     }
+  }
+  if (a.hadamard && t < last_k) hadamard<LPH>(f, lane, dim);
+  if (t < a.q_heads) {
+    if (!known) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = __builtin_nanf("");
+    }
+    put<IT>(a.q_out, (long long)token * a.q_heads + t, dim, e0, f);
+    return;
+  }
+  const long long room = (long long)a.c.pages << a.c.page_shift;
+  if (slot < 0 || slot >= room || !known) return;
+  const bool key = t < last_k;
+  const long long row = cache_row(a.c, (uint32_t)slot >> a.c.page_shift, key ? t - a.q_heads : t - last_k,
+                                  (uint32_t)slot & a.c.page_mask);
+  char* const base = key ? a.c.k : a.c.v;
+  if constexpr (sizeof(CT) == 1) {
+    // bit patterns of |x| order like the values, infinities and NaN last
+    unsigned m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const unsigned b = __builtin_bit_cast(unsigned, f[j]) & 0x7fffffffu;
+      m = m > b ? m : b;
+    }
+    // a group's idle lanes hold no part of the head and have left: the
+    // exchanges stay below the lanes in use
+    const int used = dim >> 3;
+    if ((used & (used - 1)) == 0) {
+      if (used > 1) m = umax_xor<1>(m);
+      if (used > 2) m = umax_xor<2>(m);
+      if (used > 4) m = umax_xor<4>(m);
+      if (LPH > 8 && used > 8) m = umax_xor<8>(m);
+      if (LPH > 16 && used > 16) m = umax_xor<16>(m);
+    } else {
+      const int first = (threadIdx.x & 63) & ~(LPH - 1);
+      unsigned all = 0;
+      for (int l = 0; l < used; ++l) {
+        const unsigned o = (unsigned)__shfl((int)m, first + l);
+        all = all > o ? all : o;
+      }
+      m = all;
+    }
+    const _Float16 scale = (_Float16)(__builtin_bit_cast(float, m) / 127.0f);
+    const float s = (float)scale;
+    union {
+      signed char b[8];
+      u32x2 w;
+    } o;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float q = s == 0.0f ? 0.0f : rintf(f[j] / s);
+      o.b[j] = (signed char)(int)fminf(fmaxf(q, -127.0f), 127.0f);
+    }
+    *(u32x2*)(base + row * dim + e0) = o.w;
+    if (lane == 0) (key ? a.c.ks : a.c.vs)[row] = scale;
+  } else {
+    put<CT>(base, row, dim, e0, f);
   }
 }
 
@@ -312,10 +303,16 @@ hipError_t launch_append(AppendArgs& a, hipStream_t stream) {
   const int lph = a.c.head_dim <= 64 ? 8 : a.c.head_dim <= 128 ? 16 : 32;
   const int groups = 256 / lph;
   a.tokens_per_block = a.tasks >= groups ? 1 : groups / a.tasks;
-  const uint32_t blocks = (a.tokens + a.tokens_per_block - 1) / a.tokens_per_block;
-  if (lph == 8) append_kernel<IT, CT, 8><<<dim3(blocks), dim3(256), 0, stream>>>(a);
-  else if (lph == 16) append_kernel<IT, CT, 16><<<dim3(blocks), dim3(256), 0, stream>>>(a);
-  else append_kernel<IT, CT, 32><<<dim3(blocks), dim3(256), 0, stream>>>(a);
+  const dim3 grid((a.tokens + a.tokens_per_block - 1) / a.tokens_per_block, (a.tasks + groups - 1) / groups);
+  if (a.vec) {
+    if (lph == 8) append_kernel<IT, CT, 8, true><<<grid, dim3(256), 0, stream>>>(a);
+    else if (lph == 16) append_kernel<IT, CT, 16, true><<<grid, dim3(256), 0, stream>>>(a);
+    else append_kernel<IT, CT, 32, true><<<grid, dim3(256), 0, stream>>>(a);
+  } else {
+    if (lph == 8) append_kernel<IT, CT, 8, false><<<grid, dim3(256), 0, stream>>>(a);
+    else if (lph == 16) append_kernel<IT, CT, 16, false><<<grid, dim3(256), 0, stream>>>(a);
+    else append_kernel<IT, CT, 32, false><<<grid, dim3(256), 0, stream>>>(a);
+  }
   return hipGetLastError();
 }
 
@@ -384,8 +381,8 @@ extern "C" orbit_status orbit_kv_append(const orbit_kv_append_args* p, hipStream
   a.hadamard = p->hadamard != 0;
   a.vec = vector_rows(p->k, p->k_token_stride) && vector_rows(p->v, p->v_token_stride) && p->k_head_stride % 8 == 0 &&
           p->v_head_stride % 8 == 0 && (!queries || (vector_rows(p->q, p->q_token_stride) && p->q_head_stride % 8 == 0));
-  a.vec_pair = a.vec && a.half % 8 == 0;
-  a.vec_table = a.cos_sin && aligned_to(p->cos_sin, 16) && a.half % 8 == 0;
+  // halves lie whole vectors apart, interleaved pairs take four cosines
+  if (a.cos_sin) a.vec = a.vec && aligned_to(p->cos_sin, 16) && a.half % (a.interleaved ? 4 : 8) == 0;
   hipError_t e;
   switch (p->in_dtype) {
     case ORBIT_BF16: e = append_by_format<__bf16>(a, p->cache.format, stream); break;

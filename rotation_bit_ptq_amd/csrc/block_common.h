@@ -6,6 +6,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "orbit_internal.h"
 
 namespace orbit {
@@ -89,14 +91,15 @@ __device__ __forceinline__ float max_rows32(float v) {
   return fmaxf(__builtin_bit_cast(float, (unsigned)r[0]), __builtin_bit_cast(float, (unsigned)r[1]));
 }
 
-// Sum over the wave, the same bits in every lane.
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum over each row of 16 lanes, and over the wave: the same bits in every
+// lane of the row, of the wave.
+__device__ __forceinline__ float row_sum(float v) {
   v = dpp_add<kXor1>(v);
   v = dpp_add<kXor2>(v);
   v = dpp_add<kHalfMirror>(v);
-  v = dpp_add<kRowMirror>(v);
-  return add_rows32(add_rows16(v));
+  return dpp_add<kRowMirror>(v);
 }
+__device__ __forceinline__ float wave_sum(float v) { return add_rows32(add_rows16(row_sum(v))); }
 
 }  // namespace block
 }  // namespace orbit

@@ -78,19 +78,11 @@ extern "C" orbit_status orbit_block_norm(const orbit_block_norm_args* p, hipStre
   a.rho = p->residual_scale;
   a.eps = p->eps;
   a.width = (float)p->dim;
-  bool vec = p->dim % 8 == 0 && vector_rows(p->x, p->x_stride);
-  if (p->branch) vec = vec && vector_rows(p->branch, p->branch_stride) && vector_rows(p->r_out, p->r_stride);
-  if (norm) vec = vec && vector_rows(p->y_out, p->y_stride);
-  if (p->weight) vec = vec && vector_rows(p->weight, 0);
-  if (p->post_weight) vec = vec && vector_rows(p->post_weight, 0);
-  if (p->gate) vec = vec && vector_rows(p->gate, p->gate_stride);
-  if (p->scale) vec = vec && vector_rows(p->scale, p->scale_stride);
-  if (p->shift) vec = vec && vector_rows(p->shift, p->shift_stride);
   hipError_t e;
   switch (p->x_dtype) {
-    case ORBIT_BF16: e = launch_norm<__bf16, __bf16, __bf16>(a, vec, stream); break;
-    case ORBIT_F16: e = launch_norm<_Float16, _Float16, _Float16>(a, vec, stream); break;
-    default: e = launch_norm_f32(a, p->branch ? p->branch_dtype : ORBIT_F32, norm ? p->y_dtype : ORBIT_F32, vec, stream);
+    case ORBIT_BF16: e = launch_norm<__bf16, __bf16, __bf16>(a, stream); break;
+    case ORBIT_F16: e = launch_norm<_Float16, _Float16, _Float16>(a, stream); break;
+    default: e = launch_norm_f32(a, p->branch ? p->branch_dtype : ORBIT_F32, norm ? p->y_dtype : ORBIT_F32, stream);
   }
   return hip_status(e);
 }

@@ -1,7 +1,8 @@
 """Rotate-then-quantize linear layers on AMD MI355X (gfx950).
 
-A thin ctypes binding of ``liborbit.so`` (C ABI in ``include/orbit.h``).
-This module only marshals arguments: every step of the layer runs in the
+A thin binding of ``liborbit.so`` (C ABI in ``include/orbit.h``): ctypes for
+the layer, a native module (``csrc/binding.cpp``) for the operators between
+the layers.  This module only marshals arguments: every step runs in the
 library's HIP kernels on the caller's current torch stream.  Device buffers
 are torch tensors; there is no CPU path, and importing fails if the library
 has not been built (``__graft_entry__.build()`` or
@@ -25,7 +26,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 import numpy as np
 import torch
@@ -323,75 +323,30 @@ def int4_linear(xrot: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, group:
 
 # ---- what stands between the quantized projections of a block ---------------
 #
-# Tensors of these functions may be strided rows or heads: only the innermost
-# dimension has to be contiguous.  Argument structs of include/orbit.h are
-# packed field by field ("@": the C compiler's own layout).
+# Called once per layer and decode step, so checks, allocation and the call
+# itself are native (csrc/binding.cpp).  Tensors of these functions may be
+# strided rows or heads: only the innermost dimension has to be contiguous.
+# Work runs on the current stream of the GPU that the first tensor is on.
 
-_NORMS = {None: 0, "rms": 1, "layer": 2}
-_KV_FORMATS = {torch.bfloat16: 1, torch.float16: 2, torch.int8: 3}
-_NORM_ARGS = struct.Struct("@10P10q6i2f")
-_ADAPTER_ARGS = struct.Struct("@9P9q2i")
-_CACHE = struct.Struct("@4Pq4i")
-_APPEND_ARGS = struct.Struct("@4Pq4i7P9q4i")
-_ATTENTION_ARGS = struct.Struct("@4Pq4i6P8qfi")
-
-
-# These calls are made once per layer and decode step, so their checks are
-# counted in tenths of microseconds: one test of everything per tensor, and
-# the reason looked for only when it fails.
-
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-
-
-def _tensor(t, name, dev, shape, dtype):
-    """The strides of a tensor of this shape and dtype on GPU `dev` whose innermost
-    dimension is contiguous."""
-    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.shape == shape and t.dtype is dtype:
-        strides = t.stride()
-        if strides[-1] == 1 or t.shape[-1] <= 1 or t.numel() == 0:
-            return strides
-    raise OrbitError(_reason(t, name, dev, shape, dtype))
-
-
-def _reason(t, name, dev, shape, dtype):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        return f"{name} must be a torch tensor on a GPU"
-    if t.get_device() != dev:
-        return f"{name} must be on GPU {dev}, where the first argument is"
-    if t.shape != shape:
-        return f"{name} must be {list(shape)}, got {list(t.shape)}"
-    if t.dtype is not dtype:
-        return f"{name} must be {dtype}, got {t.dtype}"
-    return f"{name}'s innermost dimension must be contiguous"
-
-
-def _first(t, name, dims):
-    """The GPU of a call's first tensor."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise OrbitError(f"{name} must be a torch tensor on a GPU")
-    if t.dim() != dims:
-        raise OrbitError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    return t.get_device()
-
-
-def _float(t, name):
-    """A floating tensor's orbit_dtype."""
+def _load_binding():
     try:
-        return _DT[t.dtype]
-    except (KeyError, AttributeError):
-        raise OrbitError(f"{name} must be a float32, bfloat16 or float16 tensor") from None
+        from . import _binding
+    except ImportError as e:
+        raise ImportError("the native binding is not built (or older than torch); run "
+                          "__graft_entry__.build()") from e
+    _binding.start(OrbitError, torch._C._cuda_getCurrentRawStream)
+    return _binding
 
 
-def _launch(fn, what, dev, *args):
-    """Calls the library on the current stream of GPU `dev`, with that device current."""
-    if _current_device() == dev:
-        status = fn(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev))
-    if status:
-        _check(status, what)
+_binding = _load_binding()
+_NORMS = {None: 0, "rms": 1, "layer": 2}
+
+
+def _norm(kind):
+    try:
+        return _NORMS[kind]
+    except (KeyError, TypeError):
+        raise OrbitError(f"norm and post must be 'rms', 'layer' or None, got {kind!r}") from None
 
 
 def block_norm(x, branch=None, *, weight=None, norm="rms", post=None, post_weight=None,
@@ -412,72 +367,8 @@ def block_norm(x, branch=None, *, weight=None, norm="rms", post=None, post_weigh
     m // ceil(rows / G).  r has x's dtype, y out_dtype (x's; any where x is
     float32).  r_out may be x; out may be x or branch.
     """
-    dev = _first(x, "x", 2)
-    shape = x.shape
-    M, D = shape
-    xt = _float(x, "x")
-    dtype = x.dtype
-    xs = _tensor(x, "x", dev, shape, dtype)[0]
-    if norm not in _NORMS or post not in _NORMS:
-        raise OrbitError(f"norm and post must be 'rms', 'layer' or None, got {norm!r}, {post!r}")
-    bt = bp = bs = rp = rs = yt = yp = ys = 0
-    r = y = None
-    if branch is not None:
-        bt = _float(branch, "branch")
-        bs = _tensor(branch, "branch", dev, shape, branch.dtype)[0]
-        bp = branch.data_ptr()
-        r = x.new_empty(shape) if r_out is None else r_out
-        rs = _tensor(r, "r_out", dev, shape, dtype)[0]
-        rp = r.data_ptr()
-    elif norm is None:
-        raise OrbitError("block_norm needs a branch, a norm, or both")
-    elif post is not None or post_weight is not None or gate is not None or r_out is not None:
-        raise OrbitError("post, post_weight, gate and r_out need a branch")
-    if norm is not None:
-        if out is None:
-            y = x.new_empty(shape) if out_dtype is None or out_dtype is dtype else x.new_empty(shape, dtype=out_dtype)
-        else:
-            y = out
-        yt = _float(y, "out")
-        ys = _tensor(y, "out", dev, shape, out_dtype or y.dtype)[0]
-        yp = y.data_ptr()
-    elif weight is not None or scale is not None or shift is not None or out is not None:
-        raise OrbitError("weight, scale, shift and out need a norm")
-    G, pt, wp, pwp, gp, cp, hp, gs, cs, hs, ip = 1, None, 0, 0, 0, 0, 0, 0, 0, 0, 0
-    if weight is not None:
-        pt = getattr(weight, "dtype", None)
-        _tensor(weight, "weight", dev, (D,), pt)
-        wp = weight.data_ptr()
-    if post_weight is not None:
-        pt = pt or getattr(post_weight, "dtype", None)
-        _tensor(post_weight, "post_weight", dev, (D,), pt)
-        pwp = post_weight.data_ptr()
-    mod = gate if gate is not None else scale if scale is not None else shift
-    if mod is not None:
-        if not isinstance(mod, torch.Tensor) or mod.dim() != 2 or mod.shape[0] < 1:
-            raise OrbitError(f"gate, scale and shift must be tensors [groups, {D}]")
-        pt = pt or mod.dtype
-        G = mod.shape[0]
-        rows = (G, D)
-        if gate is not None:
-            gs = _tensor(gate, "gate", dev, rows, pt)[0]
-            gp = gate.data_ptr()
-        if scale is not None:
-            cs = _tensor(scale, "scale", dev, rows, pt)[0]
-            cp = scale.data_ptr()
-        if shift is not None:
-            hs = _tensor(shift, "shift", dev, rows, pt)[0]
-            hp = shift.data_ptr()
-    if pt is not None and pt not in _DT:
-        raise OrbitError("weight, post_weight, gate, scale and shift must be float32, bfloat16 or float16")
-    if groups is not None:
-        _tensor(groups, "groups", dev, (M,), torch.int32)
-        ip = groups.data_ptr()
-    if M:  # an empty branch has no address to tell it from none
-        _launch(lib.orbit_block_norm, "orbit_block_norm", dev, _NORM_ARGS.pack(
-            x.data_ptr(), bp, rp, yp, wp, pwp, gp, cp, hp, ip, xs, bs, rs, ys, gs, cs, hs, M, D, G, xt,
-            bt, yt, _DT[pt] if pt is not None else 0, _NORMS[norm], _NORMS[post], residual_scale, eps))
-    return y if r is None else r if y is None else (r, y)
+    return _binding.block_norm(x, branch, weight, _norm(norm), _norm(post), post_weight, gate, scale, shift,
+                               groups, residual_scale, eps, out_dtype, r_out, out)
 
 
 def adapter_add(y, x, A, B, ids, *, scale=None, ranks=None, out=None):
@@ -493,64 +384,7 @@ def adapter_add(y, x, A, B, ids, *, scale=None, ranks=None, out=None):
     weight-only layers x is the rotated x' they read, with A rotated once:
     rotate(rot, A.view(-1, K)).  out may be y.
     """
-    dev = _first(x, "x", 2)
-    M, K = x.shape
-    dtype = x.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise OrbitError("x must be bfloat16 or float16")
-    yt = _float(y, "y")
-    if not isinstance(A, torch.Tensor) or A.dim() != 3 or y.dim() != 2:
-        raise OrbitError("y must be [M, N] and A [adapters, R, K]")
-    L, R, N = A.shape[0], A.shape[1], y.shape[1]
-    xs = _tensor(x, "x", dev, x.shape, dtype)[0]
-    ys = _tensor(y, "y", dev, (M, N), y.dtype)[0]
-    _tensor(A, "A", dev, (L, R, K), dtype)
-    _tensor(B, "B", dev, (L, N, R), dtype)
-    if not A.is_contiguous() or not B.is_contiguous():
-        raise OrbitError("A and B must be contiguous")
-    _tensor(ids, "ids", dev, (M,), torch.int32)
-    sp = rp = 0
-    if scale is not None:
-        _tensor(scale, "scale", dev, (L,), torch.float32)
-        sp = scale.data_ptr()
-    if ranks is not None:
-        _tensor(ranks, "ranks", dev, (L,), torch.int32)
-        rp = ranks.data_ptr()
-    if out is None:
-        out = y.new_empty((M, N))
-    os_ = _tensor(out, "out", dev, (M, N), y.dtype)[0]
-    ws = lib.orbit_adapter_workspace(M, K, R)
-    if ws < 0:
-        raise OrbitError(f"orbit_adapter_add: invalid shape (M {M}, K {K}, rank {R})")
-    work = x.new_empty((ws,), dtype=torch.uint8)
-    _launch(lib.orbit_adapter_add, "orbit_adapter_add", dev, _ADAPTER_ARGS.pack(
-        x.data_ptr(), A.data_ptr(), B.data_ptr(), y.data_ptr(), out.data_ptr(), ids.data_ptr(), rp, sp,
-        work.data_ptr(), ws, xs, ys, os_, M, K, N, L, R, _DT[dtype], yt))
-    return out
-
-
-def _cache_fields(k_cache, v_cache, k_scale, v_scale, dev):
-    """The fields of orbit_kv_cache: caches [pages, heads, page size, head dim]."""
-    fmt = _KV_FORMATS.get(getattr(k_cache, "dtype", None))
-    if fmt is None:
-        raise OrbitError("k_cache and v_cache must be bfloat16, float16 or int8 tensors")
-    shape = k_cache.shape
-    if len(shape) != 4:
-        raise OrbitError("k_cache and v_cache must be [pages, kv_heads, page_size, dim]")
-    _tensor(k_cache, "k_cache", dev, shape, k_cache.dtype)
-    _tensor(v_cache, "v_cache", dev, shape, k_cache.dtype)
-    if not k_cache.is_contiguous() or not v_cache.is_contiguous():
-        raise OrbitError("k_cache and v_cache must be contiguous")
-    ks = vs = 0
-    if fmt == 3:
-        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            _tensor(t, name, dev, shape[:3], torch.float16)
-            if not t.is_contiguous():
-                raise OrbitError(f"{name} must be contiguous")
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    elif k_scale is not None or v_scale is not None:
-        raise OrbitError("k_scale and v_scale belong to an int8 cache")
-    return (k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, shape[0], shape[2], shape[1], shape[3], fmt)
+    return _binding.adapter_add(y, x, A, B, ids, scale, ranks, out)
 
 
 def kv_append(k, v, k_cache, v_cache, slots, *, positions=None, cos_sin=None, interleaved=False,
@@ -567,66 +401,15 @@ def kv_append(k, v, k_cache, v_cache, slots, *, positions=None, cos_sin=None, in
     cos_sin: float32 [positions, rot_dim], cosines then sines; positions:
     int64 [tokens].  Returns the rotated queries (None without q).
     """
-    dev = _first(k, "k", 3)
-    kt = _float(k, "k")
-    dtype = k.dtype
-    cache = _cache_fields(k_cache, v_cache, k_scale, v_scale, dev)
-    T, heads, dim = k.shape[0], cache[6], cache[7]
-    ks = _tensor(k, "k", dev, (T, heads, dim), dtype)
-    vs = _tensor(v, "v", dev, (T, heads, dim), dtype)
-    _tensor(slots, "slots", dev, (T,), torch.int64)
-    cp = pp = P = rot = 0
-    if cos_sin is not None:
-        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2 or not cos_sin.shape[0]:
-            raise OrbitError("cos_sin must be a tensor [positions, rot_dim] of at least one row")
-        P, rot = cos_sin.shape
-        _tensor(cos_sin, "cos_sin", dev, cos_sin.shape, torch.float32)
-        if not cos_sin.is_contiguous():
-            raise OrbitError("cos_sin must be contiguous")
-        if positions is None:
-            raise OrbitError("cos_sin needs positions")
-        _tensor(positions, "positions", dev, (T,), torch.int64)
-        cp, pp = cos_sin.data_ptr(), positions.data_ptr()
-    qp = qo = q0 = q1 = H = 0
-    if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
-            raise OrbitError("q must be a tensor [tokens, q_heads, dim]")
-        H = q.shape[1]
-        shape = (T, H, dim)
-        q0, q1, _ = _tensor(q, "q", dev, shape, dtype)
-        if q_out is None:
-            q_out = q.new_empty(shape)
-        else:
-            _tensor(q_out, "q_out", dev, shape, dtype)
-            if not q_out.is_contiguous():
-                raise OrbitError("q_out must be contiguous")
-        qp, qo = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise OrbitError("q_out needs q")
-    _launch(lib.orbit_kv_append, "orbit_kv_append", dev, _APPEND_ARGS.pack(
-        *cache, k.data_ptr(), v.data_ptr(), qp, qo, slots.data_ptr(), pp, cp, ks[0], ks[1], vs[0],
-        vs[1], q0, q1, T, H, P, rot, kt, bool(interleaved), bool(hadamard)))
-    return q_out
+    return _binding.kv_append(k, v, k_cache, v_cache, slots, positions, cos_sin, interleaved, q, q_out,
+                              k_scale, v_scale, hadamard)
 
 
 def kv_read(k_cache, v_cache, slots, *, k_scale=None, v_scale=None, dtype=None):
     """The keys and values of the tokens at `slots` (int64 [tokens]) as dense
     rows [tokens, kv_heads, dim] of `dtype` (default: the cache's; float16 for
     int8); zeros where a slot lies outside the cache."""
-    dev = _first(k_cache, "k_cache", 4)
-    cache = _cache_fields(k_cache, v_cache, k_scale, v_scale, dev)
-    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
-        raise OrbitError("slots must be a tensor of one dimension")
-    _tensor(slots, "slots", dev, slots.shape, torch.int64)
-    if dtype is None:
-        dtype = torch.float16 if cache[8] == 3 else k_cache.dtype
-    if dtype not in _DT:
-        raise OrbitError("dtype must be float32, bfloat16 or float16")
-    shape = (slots.shape[0], cache[6], cache[7])
-    k, v = k_cache.new_empty(shape, dtype=dtype), k_cache.new_empty(shape, dtype=dtype)
-    _launch(lib.orbit_kv_read, "orbit_kv_read", dev, _CACHE.pack(*cache), slots.data_ptr(),
-            shape[0], k.data_ptr(), v.data_ptr(), _DT[dtype])
-    return k, v
+    return _binding.kv_read(k_cache, v_cache, slots, k_scale, v_scale, dtype)
 
 
 def paged_attention(q, k_cache, v_cache, block_table, lengths, *, scale=None, window=0,
@@ -641,30 +424,5 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, *, scale=None, wi
     Returns out [batch, q_heads, dim], with return_lse also lse float32
     [batch, q_heads].
     """
-    dev = _first(q, "q", 3)
-    qt = _float(q, "q")
-    cache = _cache_fields(k_cache, v_cache, k_scale, v_scale, dev)
-    batch, H, dim = q.shape
-    q0, q1, _ = _tensor(q, "q", dev, (batch, H, cache[7]), q.dtype)
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise OrbitError("block_table must be a tensor [batch, pages]")
-    width = block_table.shape[1]
-    ts = _tensor(block_table, "block_table", dev, (batch, width), torch.int32)[0]
-    _tensor(lengths, "lengths", dev, (batch,), torch.int32)
-    if out is None:
-        out = q.new_empty((batch, H, dim))
-    else:
-        _tensor(out, "out", dev, (batch, H, dim), q.dtype)
-        if not out.is_contiguous():
-            raise OrbitError("out must be contiguous")
-    lse = q.new_empty((batch, H), dtype=torch.float32) if return_lse else None
-    ws = lib.orbit_paged_attention_workspace(batch, H, cache[6], dim, cache[5], width, window, cache[8])
-    if ws < 0:
-        raise OrbitError(f"orbit_paged_attention: invalid shape (batch {batch}, {H} query heads on "
-                         f"{cache[6]}, dim {dim}, window {window})")
-    work = q.new_empty((ws,), dtype=torch.uint8) if ws else None
-    _launch(lib.orbit_paged_attention, "orbit_paged_attention", dev, _ATTENTION_ARGS.pack(
-        *cache, q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-        block_table.data_ptr(), lengths.data_ptr(), 0 if work is None else work.data_ptr(), ws,
-        q0, q1, ts, batch, H, width, window, dim ** -0.5 if scale is None else scale, qt))
-    return (out, lse) if return_lse else out
+    return _binding.paged_attention(q, k_cache, v_cache, block_table, lengths, scale, window, k_scale, v_scale,
+                                    out, return_lse)

@@ -1,7 +1,9 @@
-"""Builds liborbit.so (the C-ABI library) in-tree for gfx950 with hipcc."""
+"""Builds liborbit.so (the C-ABI library) in-tree for gfx950 with hipcc, and
+the native torch binding of its per-step operators (_binding.so) with g++."""
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -10,6 +12,9 @@ OUT = os.path.join(HERE, "liborbit.so")
 # measured roofline ceilings for bench.py (not part of the layer's C ABI)
 PEAKS_SOURCES = ["peaks.hip"]
 PEAKS_OUT = os.path.join(HERE, "libpeaks.so")
+# the operators' binding to torch tensors (host code alone)
+BINDING_SOURCE = "binding.cpp"
+BINDING_OUT = os.path.join(HERE, "_binding.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["abi.cpp", "codebook.cpp", "rpbh_quant.hip", "rpbh_bf16_act.hip",
@@ -60,8 +65,9 @@ def build(verbose=False, incremental=False):
         objs = list(ex.map(lambda s: _compile(s, objdir, incremental, hdr), SOURCES))
     _link(objs, OUT)
     _link([_compile(s, objdir, incremental, hdr) for s in PEAKS_SOURCES], PEAKS_OUT)
+    _binding()
     if verbose:
-        print(f"built {OUT} and {PEAKS_OUT}")
+        print(f"built {OUT}, {PEAKS_OUT} and {BINDING_OUT}")
     return OUT
 
 
@@ -72,6 +78,26 @@ def _link(objs, out):
     if r.returncode != 0:
         raise RuntimeError(f"link of {out} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, out)
+
+
+def _binding():
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(HIPCC)))
+    include = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(rocm, "include"),
+               "/opt/rocm/include"]
+    tmp = BINDING_OUT + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for d in include if os.path.isdir(d) for x in ("-isystem", d)],
+           os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, "-L" + HERE, "-l:liborbit.so",
+           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-L/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_OUT)
 
 
 if __name__ == "__main__":

@@ -1,7 +1,9 @@
 """Argument checks of the operators between a block's projections: they run on
 the host before any HIP call, so they need no GPU; every address below is
 never dereferenced."""
-import ctypes
+import os
+import re
+import struct
 
 import pytest
 
@@ -10,6 +12,12 @@ import rotation_bit_ptq_amd as rbp
 OK, ARG, SHAPE, DTYPE = 0, 1, 2, 3
 P = 0x10000   # 16-byte aligned
 ODD = P + 8   # not
+# the argument structs of include/orbit.h, field by field, in the C compiler's layout
+NORM_ARGS = struct.Struct("@10P10q6i2f")
+ADAPTER_ARGS = struct.Struct("@9P9q2i")
+CACHE_ARGS = struct.Struct("@4Pq4i")
+APPEND_ARGS = struct.Struct("@4Pq4i7P9q4i")
+ATTENTION_ARGS = struct.Struct("@4Pq4i6P8qfi")
 INF, NAN = float("inf"), float("nan")
 
 
@@ -18,7 +26,7 @@ def _norm(**kw):
              gs=64, cs=64, hs=64, rows=0, dim=64, groups=1, xt=1, bt=1, yt=1, pt=0, norm=1, post=0, rho=1.0, eps=1e-6)
     assert not set(kw) - set(f)
     f.update(kw)
-    return rbp.lib.orbit_block_norm(rbp._NORM_ARGS.pack(*f.values()), None)
+    return rbp.lib.orbit_block_norm(NORM_ARGS.pack(*f.values()), None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -40,7 +48,7 @@ def _adapter(**kw):
              adapters=2, rank=8, xt=1, yt=0)
     assert not set(kw) - set(f)
     f.update(kw)
-    return rbp.lib.orbit_adapter_add(rbp._ADAPTER_ARGS.pack(*f.values()), None)
+    return rbp.lib.orbit_adapter_add(ADAPTER_ARGS.pack(*f.values()), None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -76,7 +84,7 @@ def _append(**kw):
              q_heads=4, table=10, rot=64, xt=1, inter=0, had=0)
     assert not set(kw) - set(f)
     f.update(kw)
-    return rbp.lib.orbit_kv_append(rbp._APPEND_ARGS.pack(*f.values()), None)
+    return rbp.lib.orbit_kv_append(APPEND_ARGS.pack(*f.values()), None)
 
 
 @pytest.mark.parametrize("kw,want", CACHE_CASES + [
@@ -94,7 +102,7 @@ def _read(tokens=0, slots=P, k=P, v=P, dt=1, **kw):
     f = dict(CACHE)
     assert not set(kw) - set(f)
     f.update(kw)
-    return rbp.lib.orbit_kv_read(rbp._CACHE.pack(*f.values()), slots, tokens, k, v, dt, None)
+    return rbp.lib.orbit_kv_read(CACHE_ARGS.pack(*f.values()), slots, tokens, k, v, dt, None)
 
 
 @pytest.mark.parametrize("kw,want", CACHE_CASES + [
@@ -111,7 +119,7 @@ def _attend(**kw):
              window=0, scale=0.125, qt=1)
     assert not set(kw) - set(f)
     f.update(kw)
-    return rbp.lib.orbit_paged_attention(rbp._ATTENTION_ARGS.pack(*f.values()), None)
+    return rbp.lib.orbit_paged_attention(ATTENTION_ARGS.pack(*f.values()), None)
 
 
 @pytest.mark.parametrize("kw,want", CACHE_CASES + [
@@ -140,12 +148,26 @@ def test_attention_workspace_of_invalid_sizes():
         assert f(*bad) == -1
 
 
-def test_structs_are_laid_out_as_the_compiler_does():
-    # the packed formats against ctypes' own layout of the same fields
-    for fmt, fields in ((rbp._CACHE, "4P1q4i"), (rbp._NORM_ARGS, "10P10q6i2f"), (rbp._ADAPTER_ARGS, "9P9q2i"),
-                        (rbp._APPEND_ARGS, "4P1q4i7P9q4i"), (rbp._ATTENTION_ARGS, "4P1q4i6P8q1f1i")):
-        types = {"P": ctypes.c_void_p, "q": ctypes.c_int64, "i": ctypes.c_int32, "f": ctypes.c_float}
-        import re
-        members = [types[t] for n, t in re.findall(r"(\d+)([Pqif])", fields) for _ in range(int(n))]
-        s = type("S", (ctypes.Structure,), {"_fields_": [(f"f{i}", t) for i, t in enumerate(members)]})
-        assert ctypes.sizeof(s) == fmt.size
+def test_structs_hold_the_headers_fields():
+    header = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "orbit.h")).read()
+    for fmt, name in ((CACHE_ARGS, "orbit_kv_cache"), (NORM_ARGS, "orbit_block_norm_args"), (ADAPTER_ARGS, "orbit_adapter_args"),
+                      (APPEND_ARGS, "orbit_kv_append_args"), (ATTENTION_ARGS, "orbit_paged_attention_args")):
+        end = header.index("} " + name + ";")
+        body = re.sub(r"/\*.*?\*/", "", header[header.rindex("typedef struct {", 0, end) + 16:end], flags=re.S)
+        got = "".join(("4Pq4i" if line.split()[0] == "orbit_kv_cache" else
+                       {"void": "P", "int32_t": "i", "int64_t": "q", "float": "f"}[line.replace("const ", "").split()[0]]
+                       if "*" not in line else "P") * len(line.split(","))
+                      for line in body.replace("\n", " ").split(";") if line.strip())
+        want = "".join(c * int(n or 1) for n, c in re.findall(r"(\d*)([Pqif])", fmt.format))
+        assert "".join(c * int(n or 1) for n, c in re.findall(r"(\d*)([Pqif])", got)) == want, name
+
+
+def test_the_binding_refuses_before_it_calls():
+    import torch
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    for f in (lambda: rbp.block_norm(x), lambda: rbp.block_norm(None), lambda: rbp.block_norm(x, norm="batch"),
+              lambda: rbp.adapter_add(x, x, x, x, i), lambda: rbp.kv_append(x, x, x, x, i), lambda: rbp.kv_read(x, x, i),
+              lambda: rbp.paged_attention(x, x, x, i, i), lambda: rbp.paged_attention(3, x, x, i, i)):
+        with pytest.raises(rbp.OrbitError):
+            f()

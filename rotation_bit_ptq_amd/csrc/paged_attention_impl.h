@@ -16,9 +16,11 @@
 //
 // Products on the matrix cores (16x16x32), also for a single query head: the
 // unused rows cost nothing that bounds the kernel.
-//   S^T = K Q^T: A = 16 tokens x 32 coordinates straight from memory (a
-//   lane's 16 contiguous bytes of a key are an operand), B = the queries,
-//   kept in registers.  A lane then holds head l % 16 and tokens 4 (l / 16)
+//   S^T = K Q^T: A = 16 tokens x 32 coordinates, B = the queries, kept in
+//   registers.  Keys are loaded like values, whole rows by neighbouring
+//   lanes, and pass through LDS: read from memory in the operands' order
+//   (neighbouring lanes in 16 rows) they cost the address unit four times
+//   the cycles, and the second load of a line waits for the first's.  A lane then holds head l % 16 and tokens 4 (l / 16)
 //   + i of each half tile.
 //   O^T = V^T P^T: those lanes' probabilities are the B operand as they
 //   stand if operand slot 8 g + j means token 4 g + j of the first half
@@ -112,15 +114,19 @@ constexpr int kWaves = 4;
 // cache took 165 us at two, 141 at three, 142 at four (spilling).
 constexpr int residents(int format, int dp, bool paged16) {
   if (format == ORBIT_KV_INT8) return dp == 64 ? 4 : dp == 128 ? 3 : 2;
-  return dp == 64 ? 4 : dp == 128 && paged16 ? 3 : 1;
+  return dp == 64 ? 4 : dp == 128 && paged16 ? 2 : 1;
 }
 
-template <int DP>
+// A wave's rows of a tile in LDS, of ROW bytes each, without padding: 16-byte
+// unit u of row r lies in place u ^ key(r).  The writes (a row's units side by
+// side), the operand reads (four units of 16 rows) and the transposing reads
+// (two units of 16 rows) then all touch every bank equally often.
+template <int ROW>
 struct Stage {
-  // four rows apart a quarter of the banks apart, so that the transposing
-  // read's four row groups meet in no bank
-  static constexpr int kStride = DP + 4;  // 16-bit elements
-  static constexpr int kWaveElems = kTile * kStride;
+  static constexpr int kBytes = kTile * ROW;
+  static __device__ __forceinline__ constexpr int key(int row) {
+    return ROW == 64 ? (row >> 2) & 3 : ROW == 128 ? (row >> 1) & 7 : row & 15;
+  }
 };
 
 // Two probabilities as a hi + lo pair of 16-bit numbers.  fp16: both parts
@@ -153,16 +159,18 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
   typedef typename M::V8 V8;
   typedef typename Mma<Q>::T QT;
   constexpr int kSteps = DP / 32;                   // products per tile half
-  constexpr int kLoads = kCoded ? DP / 64 : kSteps;  // 16-byte loads of one key per lane
+  constexpr int kReads = kCoded ? DP / 64 : kSteps;  // 16-byte operand reads of one key per lane
   constexpr int kRowLanes = kCoded ? DP / 16 : DP / 8;  // lanes on one value row
   constexpr int kRowsAtOnce = 64 / kRowLanes;
   constexpr int kVLoads = kTile / kRowsAtOnce;
   constexpr int kBlocks = DP / 16;
   constexpr int kElem = kCoded ? 1 : 2;
 
-  constexpr int kStageBytes = kWaves * Stage<DP>::kWaveElems * 2;
+  typedef Stage<DP * kElem> Sk;  // keys as the cache holds them
+  typedef Stage<DP * 2> Sv;      // values in 16 bits
+  constexpr int kStageBytes = kWaves * (Sk::kBytes + Sv::kBytes);
   constexpr int kSumBytes = kWaves * 16 * DP * 4 + kWaves * 16 * 8;
-  __shared__ __align__(16) char lds[kStageBytes > kSumBytes ? kStageBytes : kSumBytes];
+  __shared__ __align__(1024) char lds[kStageBytes > kSumBytes ? kStageBytes : kSumBytes];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r16 = lane & 15, lg = lane >> 4;
@@ -228,14 +236,10 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
   // head_dim the row's last vector again; scores of the former are masked and
   // their values cleared, the latter meet zeros of the queries or are results
   // that are not stored.
-  u32x4 kr[2][kLoads];
-  u32x4 vr[kVLoads];
+  u32x4 kr[kVLoads], vr[kVLoads];
   u32x2 ksr[2], vsr[2];
   const int row_bytes = dim * kElem;
   const uint32_t page_bytes = (uint32_t)row_bytes << a.c.page_shift;  // of one head
-  int koff[kLoads];
-#pragma unroll
-  for (int s = 0; s < kLoads; ++s) koff[s] = (PAGED16 ? r16 * row_bytes : 0) + min(s * 64 + lg * 16, row_bytes - 16);
   const int vcol = min((lane & (kRowLanes - 1)) * 16, row_bytes - 16);
   const int voff = (PAGED16 ? lane / kRowLanes * row_bytes : 0) + vcol;
 
@@ -277,58 +281,61 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
   };
   // The first byte of a head's part of a page, of its scales.
   auto head_of = [&](uint32_t page) { return ((uint64_t)page * a.c.kv_heads + head) * page_bytes; };
-  auto load_keys = [&](int tile, const Pages& p) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if constexpr (PAGED16) {
-        const uint32_t off = (uint32_t)(tile + half * 16) & a.c.page_mask;
-        const char* const at = a.c.k + head_of(p.page[half]) + off * (uint32_t)row_bytes;
-#pragma unroll
-        for (int s = 0; s < kLoads; ++s) kr[half][s] = *(const u32x4*)(at + koff[s]);
-        if constexpr (kCoded) {
-          const uint64_t row = (((uint64_t)p.page[half] * a.c.kv_heads + head) << a.c.page_shift) + off;
-          ksr[half] = *(const u32x2*)(a.c.ks + row + lg * 4);
-          vsr[half] = *(const u32x2*)(a.c.vs + row + lg * 4);
-        }
-      } else {
-        const int t = half * 16 + r16;
-        const uint32_t page = (uint32_t)__shfl((int)p.page[0], t);
-        const char* const at = a.c.k + head_of(page) + ((uint32_t)(tile + t) & a.c.page_mask) * (uint32_t)row_bytes;
-#pragma unroll
-        for (int s = 0; s < kLoads; ++s) kr[half][s] = *(const u32x4*)(at + koff[s]);
-        if constexpr (kCoded) {
-          // four neighbouring tokens lie in one page (page_size >= 4), whose
-          // number the first that is seen has
-          const int t4 = half * 16 + lg * 4;
-          const uint32_t four = (p.live >> t4) & 15u;
-          const uint32_t pg = (uint32_t)__shfl((int)p.page[0], t4 + (four ? __builtin_ctz(four) : 0));
-          const uint64_t row = (((uint64_t)pg * a.c.kv_heads + head) << a.c.page_shift) + ((uint32_t)(tile + t4) & a.c.page_mask);
-          ksr[half] = *(const u32x2*)(a.c.ks + row);
-          vsr[half] = *(const u32x2*)(a.c.vs + row);
-        }
-      }
-    }
-  };
-  auto load_values = [&](int tile, const Pages& p) {
+  auto load_rows = [&](u32x4 (&to)[kVLoads], const char* base, int tile, const Pages& p) {
 #pragma unroll
     for (int i = 0; i < kVLoads; ++i) {
       if constexpr (PAGED16) {
         const int half = i * 2 / kVLoads;
         const uint32_t off = ((uint32_t)(tile + half * 16) & a.c.page_mask) + (i - half * (kVLoads / 2)) * kRowsAtOnce;
-        vr[i] = *(const u32x4*)(a.c.v + head_of(p.page[half]) + off * (uint32_t)row_bytes + voff);
+        to[i] = *(const u32x4*)(base + head_of(p.page[half]) + off * (uint32_t)row_bytes + voff);
       } else {
         const int t = i * kRowsAtOnce + lane / kRowLanes;
         const uint32_t page = (uint32_t)__shfl((int)p.page[0], t);
-        vr[i] = *(const u32x4*)(a.c.v + head_of(page) + ((uint32_t)(tile + t) & a.c.page_mask) * (uint32_t)row_bytes + voff);
+        to[i] = *(const u32x4*)(base + head_of(page) + ((uint32_t)(tile + t) & a.c.page_mask) * (uint32_t)row_bytes + voff);
       }
     }
   };
+  auto load_keys = [&](int tile, const Pages& p) {
+    load_rows(kr, a.c.k, tile, p);
+    if constexpr (kCoded) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        // four neighbouring tokens lie in one page (page_size >= 4), whose
+        // number the first that is seen has
+        const int t4 = half * 16 + lg * 4;
+        uint32_t page;
+        if constexpr (PAGED16) {
+          page = p.page[half];
+        } else {
+          const uint32_t four = (p.live >> t4) & 15u;
+          page = (uint32_t)__shfl((int)p.page[0], t4 + (four ? __builtin_ctz(four) : 0));
+        }
+        const uint64_t row = (((uint64_t)page * a.c.kv_heads + head) << a.c.page_shift) + ((uint32_t)(tile + t4) & a.c.page_mask);
+        ksr[half] = *(const u32x2*)(a.c.ks + row);
+        vsr[half] = *(const u32x2*)(a.c.vs + row);
+      }
+    }
+  };
+  auto load_values = [&](int tile, const Pages& p) { load_rows(vr, a.c.v, tile, p); };
 
   f32x4 o[kBlocks];
 #pragma unroll
   for (int d = 0; d < kBlocks; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   float m_run = -__builtin_inff(), l_run = 0.0f;  // l: this lane's tokens alone
-  T* const stage = (T*)lds + wave * Stage<DP>::kWaveElems;
+  char* const kstage = lds + wave * Sk::kBytes;
+  char* const vstage = lds + kWaves * Sk::kBytes + wave * Sv::kBytes;
+  // Where this lane writes its first vectors (others: constants further, the
+  // keys' constant bits exchanged), and where it reads its first operands.
+  const int lrow = lane / kRowLanes, lcol = lane & (kRowLanes - 1);
+  const int kwrite = lrow * DP * kElem + ((lcol ^ Sk::key(lrow)) << 4);
+  const int vwrite = lrow * DP * 2 + ((lcol * (kCoded ? 2 : 1) ^ Sv::key(lrow)) << 4);
+  const int kread = r16 * DP * kElem + ((lg ^ Sk::key(r16)) << 4);  // row r16 + 16 has the same key
+  const int trow = lg * 4 + (r16 >> 2);
+  const int vread = trow * DP * 2 + ((((r16 & 3) >> 1) ^ Sv::key(trow)) << 4) + (r16 & 1) * 8;
+  auto order = [] {  // between writes and reads of the wave's rows by other lanes (LDS serves a wave in order)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
 
   int tile = c0 + wave * kTile;
   if (tile < c1) {
@@ -340,26 +347,30 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
     for (; tile < c1; tile += kStep) {
       const uint32_t live = now.live;
       // scores of the tile
+#pragma unroll
+      for (int i = 0; i < kVLoads; ++i)
+        *(u32x4*)(kstage + i * kRowsAtOnce * DP * kElem + (kwrite ^ (Sk::key(i * kRowsAtOnce) << 4))) = kr[i];
+      order();
       f32x4 s[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if constexpr (kCoded) {
+      for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int i = 0; i < kLoads; ++i) {
+        for (int i = 0; i < kReads; ++i) {
+          const u32x4 k = *(const u32x4*)(kstage + half * 16 * DP * kElem + (kread ^ (i << 6)));
+          if constexpr (kCoded) {
             union {
               u32x2 w[4];
               V8 v[2];
             } u;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) u.w[c] = codes_to_f16(kr[half][i][c]);
+            for (int c = 0; c < 4; ++c) u.w[c] = codes_to_f16(k[c]);
             s[half] = M::run(u.v[0], qf[2 * i], s[half]);
             s[half] = M::run(u.v[1], qf[2 * i + 1], s[half]);
+          } else {
+            s[half] = M::run(__builtin_bit_cast(V8, k), qf[i], s[half]);
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kLoads; ++i) s[half] = M::run(__builtin_bit_cast(V8, kr[half][i]), qf[i], s[half]);
         }
-      }
+      order();
       float z[8], vs[8];
 #pragma unroll
       for (int half = 0; half < 2; ++half)
@@ -420,40 +431,38 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
         for (int i = 0; i < kVLoads; ++i)
           vr[i] = (live >> (i * kRowsAtOnce + lane / kRowLanes)) & 1u ? vr[i] : u32x4{0u, 0u, 0u, 0u};
       }
-      {
-        const int e0 = (lane & (kRowLanes - 1)) * (kCoded ? 16 : 8);
 #pragma unroll
-        for (int i = 0; i < kVLoads; ++i) {
-          u32x2* const to = (u32x2*)(stage + (i * kRowsAtOnce + lane / kRowLanes) * Stage<DP>::kStride + e0);
-          if constexpr (kCoded) {
+      for (int i = 0; i < kVLoads; ++i) {
+        if constexpr (kCoded) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) to[c] = codes_to_f16(vr[i][c]);
-          } else {
-            to[0] = u32x2{vr[i].x, vr[i].y};
-            to[1] = u32x2{vr[i].z, vr[i].w};
+          for (int c = 0; c < 2; ++c) {
+            const u32x2 x = codes_to_f16(vr[i][2 * c]), y = codes_to_f16(vr[i][2 * c + 1]);
+            *(u32x4*)(vstage + i * kRowsAtOnce * DP * 2 + (vwrite ^ ((Sv::key(i * kRowsAtOnce) ^ c) << 4))) =
+                u32x4{x.x, x.y, y.x, y.y};
           }
+        } else {
+          *(u32x4*)(vstage + i * kRowsAtOnce * DP * 2 + (vwrite ^ (Sv::key(i * kRowsAtOnce) << 4))) = vr[i];
         }
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      order();
       load_values(tile + kStep, now);
       {
         typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-        const T* const at = stage + (lg * 4 + (r16 >> 2)) * Stage<DP>::kStride + (r16 & 3) * 4;
 #pragma unroll
         for (int d = 0; d < kBlocks; ++d) {
           union {
             s16x4 h[2];
             V8 v;
           } u;
-          u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + d * 16));
-          u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 16 * Stage<DP>::kStride + d * 16));
+          // units 2 d and 2 d + 1; rows 16 apart have the same key
+          const char* const at = vstage + (vread ^ (d << 5));
+          u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)at);
+          u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 16 * DP * 2));
           o[d] = M::run(u.v, hi, o[d]);
           o[d] = M::run(u.v, lo, o[d]);
         }
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      order();
     }
   }
   l_run = add_rows32(add_rows16(l_run));

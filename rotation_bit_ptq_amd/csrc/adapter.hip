@@ -21,12 +21,13 @@ struct AdapterArgs {
   uint32_t M, adapters;
   int K, N, R;
   int parts, k_part;  // K in parts of k_part, a workgroup each
+  int slices;  // of a tile's rows, see shrink_staged_kernel
   int columns, blocks;  // 256 columns a piece per workgroup; workgroups across N
 };
 
 constexpr int kWaves = 4;
 constexpr int kRequestsAtMost = 4;  // of a tile, past which its rows go one by one
-constexpr int kFewTokens = 64, kSomeTokens = 2048;  // see cut_of
+constexpr int kFewTokens = 128, kSomeTokens = 1024;  // see cut_of
 
 // The adapter's rank, 0 where there is none.
 __device__ __forceinline__ int rank_of(const AdapterArgs& a, int id) {
@@ -70,8 +71,8 @@ __device__ __forceinline__ float sum_of_four(const float (&s)[4]) {
   return dpp_add<kRowMirror>(v);
 }
 
-// v[m][r] = A[id][r] . x[m] over k0 <= k < k1 for RG rows and RW (1 or 4)
-// ranks from r0, by one wave without matrix cores: the lanes take
+// v[m][r] = A[id][r] . x[m] over k0 <= k < k1 for RG rows and RW ranks (1, 4
+// or 8) from r0, by one wave without matrix cores: the lanes take
 // neighbouring vectors of K, so that every load is one contiguous KB.  A is
 // read once for the rows that share an adapter.
 template <class T, int RG, int RW>
@@ -124,9 +125,13 @@ __device__ __forceinline__ void row_products(const AdapterArgs& a, uint32_t m0, 
     for (int h = g; h < RG; ++h) {
       float* const to = v + (long long)(m0 + h) * a.R + r0;
       const bool own = id[h] == id[g];
-      if constexpr (RW == 4) {
-        const float t = sum_of_four(s[h]);
-        if (own && (lane & 15) == 0 && r0 + (lane >> 4) < rank) to[lane >> 4] = t;
+      if constexpr (RW >= 4) {
+#pragma unroll
+        for (int i = 0; i < RW; i += 4) {
+          const float four[4] = {s[h][i], s[h][i + 1], s[h][i + 2], s[h][i + 3]};
+          const float t = sum_of_four(four);
+          if (own && (lane & 15) == 0 && r0 + i + (lane >> 4) < rank) to[i + (lane >> 4)] = t;
+        }
       } else {
         const float t = wave_sum(s[h][0]);
         if (own && lane == 0) *to = t;
@@ -135,38 +140,56 @@ __device__ __forceinline__ void row_products(const AdapterArgs& a, uint32_t m0, 
   }
 }
 
-template <class T, int RG, int RW>
+// One row and four ranks per workgroup, one rank per wave.
+template <class T>
 __global__ __launch_bounds__(256) void shrink_rows_kernel(AdapterArgs a) {
-  const int r0 = ((int)blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * RW;
-  row_products<T, RG, RW>(a, blockIdx.x * RG, r0, 0, a.K, a.v);
+  const int r0 = (int)blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  row_products<T, 1, 1>(a, blockIdx.x, r0, 0, a.K, a.v);
 }
 
-// out[m][n] = y[m][n] + s B[id][n] . v[m]: a thread per column.
-template <class T, class YT>
+// out[m][n] = y[m][n] + s B[id][n] . v[m]: a wave per row and 64 columns.  B's
+// block is read in the order of memory, all of it in flight at once; a lane's
+// eight ranks are summed over the lanes of a row of B.
+template <class T, class YT, int KB>
 __global__ __launch_bounds__(256) void expand_rows_kernel(AdapterArgs a) {
-  __shared__ float v[128];
-  const uint32_t m = blockIdx.x;
-  const int n = blockIdx.y * 256 + threadIdx.x;
-  const int id = a.ids[m], rank = rank_of(a, id);
-  if (rank > 0) {
-    const float s = a.scale ? a.scale[id] : 1.0f;
-    if ((int)threadIdx.x < a.R) v[threadIdx.x] = (int)threadIdx.x < rank ? a.v[(long long)m * a.R + threadIdx.x] * s : 0.0f;
-  }
-  __syncthreads();
-  if (n >= a.N) return;
-  float f = (float)((const YT*)a.y)[m * a.ys + n];
-  if (rank > 0) {
-    const T* const w = (const T*)a.B + ((long long)id * a.N + n) * a.R;
-    float d = 0.0f;
-    for (int r = 0; r < rank; r += 8) {
-      const Vec8<T> q = *(const Vec8<T>*)(w + r);
+  typedef typename Vec8Of<T>::V V8;
+  constexpr int kLanes = 4 * KB, kAcross = 64 / kLanes;  // lanes on a row of B, rows at once
+  __shared__ float sums[kWaves][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const long long m = blockIdx.x;
+  const int n0 = (int)blockIdx.y * 256 + wave * 64, n = n0 + lane;
+  if (n0 >= a.N) return;
+  const float y = (float)((const YT*)a.y)[m * a.ys + min(n, a.N - 1)];
+  const int id = a.ids[m];
+  float d = 0.0f;
+  if ((uint32_t)id < a.adapters) {
+    const int brow = lane / kLanes, bcol = lane % kLanes, r0 = bcol * 8 < a.R ? bcol * 8 : 0;
+    const T* const b = (const T*)a.B + (long long)id * a.N * a.R + r0;
+    u32x4 w[kLanes];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (r + j < rank) d = fmaf((float)q.e[j], v[r + j], d);
+    for (int c = 0; c < kLanes; ++c) w[c] = *(const u32x4*)(b + (long long)min(n0 + c * kAcross + brow, a.N - 1) * a.R);
+    const f32x4 v0 = *(const f32x4*)(a.v + m * a.R + r0), v1 = *(const f32x4*)(a.v + m * a.R + r0 + 4);
+    const int used = rank_of(a, id) - bcol * 8;  // of this lane's eight ranks; what v holds past them is anything
+    float own = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kLanes; ++c) {
+      const V8 q = __builtin_bit_cast(V8, w[c]);
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s = k < used ? fmaf((float)q[k], k < 4 ? v0[k & 3] : v1[k & 3], s) : s;
+      s = dpp_add<kXor1>(s);
+      s = dpp_add<kXor2>(s);
+      if (KB >= 2) s = dpp_add<kHalfMirror>(s);
+      if (KB >= 4) s = dpp_add<kRowMirror>(s);
+      if (bcol == c) own = s;  // the sum is in all lanes of the row: lane c keeps the c-th
     }
-    f += d;
+    sums[wave][bcol * kAcross + brow] = own;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    d = sums[wave][lane] * (a.scale ? a.scale[id] : 1.0f);
   }
-  ((YT*)a.out)[m * a.os + n] = (YT)f;
+  // no adapter, or one of rank 0: y as it is, whatever the scale
+  if (n < a.N) ((YT*)a.out)[m * a.os + n] = (YT)(rank_of(a, id) > 0 ? y + d : y);
 }
 
 // One row's request: its adapter (-1: none, or one of rank 0), rank, scale.
@@ -175,17 +198,32 @@ struct Request {
   float scale;
 };
 
-// Lane l's: that of row m0 + l of a tile of TM <= 64 rows.
+// Lane l's adapter: that of row m0 + l of a tile of TM <= 64 rows, -1: none.
 template <int TM>
-__device__ __forceinline__ Request request_of(const AdapterArgs& a, uint32_t m0, int lane) {
-  Request q = {-1, 0, 1.0f};
-  if (lane < TM && m0 + lane < a.M) {
-    q.id = a.ids[m0 + lane];
-    q.rank = rank_of(a, q.id);
-    if (q.rank == 0) q.id = -1;
-    else if (a.scale) q.scale = a.scale[q.id];
-  }
+__device__ __forceinline__ int id_of(const AdapterArgs& a, uint32_t m0, int lane) {
+  const int id = a.ids[min(m0 + lane, a.M - 1)];
+  return lane < TM && m0 + lane < a.M && (uint32_t)id < a.adapters ? id : -1;
+}
+// And its request.  Rank and scale are loaded whatever the row, so that they
+// wait for the id alone.
+__device__ __forceinline__ Request request_of(const AdapterArgs& a, int id) {
+  Request q = {id, a.R, 1.0f};
+  if (a.adapters == 0) return q;
+  if (a.ranks) q.rank = min(max(a.ranks[max(id, 0)], 0), a.R);
+  if (a.scale) q.scale = a.scale[max(id, 0)];
+  if (q.rank == 0) q.id = -1;
+  if (q.id < 0) q.rank = 0, q.scale = 1.0f;
   return q;
+}
+
+// Whether a tile, a row per lane, has more than kRequestsAtMost adapters.
+__device__ __forceinline__ bool many_requests(int id) {
+  unsigned long long rest = __ballot(id >= 0);
+  for (int n = 0; rest != 0; ++n) {
+    if (n == kRequestsAtMost) return true;
+    rest &= ~__ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctzll(rest)));
+  }
+  return false;
 }
 
 // The distinct adapters of a tile, one after the other.  Everything about
@@ -196,14 +234,6 @@ struct Requests {
   int id, rank;
 
   __device__ __forceinline__ void begin(const Request& mine) { rest = __ballot(mine.id >= 0); }
-  // Whether there are more than `most` of them.
-  static __device__ __forceinline__ bool exceed(const Request& mine, int most) {
-    Requests q;
-    q.begin(mine);
-    int n = 0;
-    while (n <= most && q.next(mine)) ++n;
-    return n > most;
-  }
   __device__ __forceinline__ bool next(const Request& mine) {
     if (rest == 0) return false;
     const int first = __builtin_ctzll(rest);
@@ -215,121 +245,138 @@ struct Requests {
   }
 };
 
+// Four rows and 16 ranks at a time.  Rows of one adapter: a wave takes four
+// ranks of all, so A is read once for them.  Else a wave takes a row (1003
+// tokens of 48 adapters, K 3072, rank 32 and less: 10 us; with all four rows
+// per wave in turn 19).
+template <class T>
+__device__ __forceinline__ void four_rows(const AdapterArgs& a, uint32_t m0, int r0) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int id = a.ids[min(m0 + (threadIdx.x & 3), a.M - 1)];
+  if (__ballot(id != __builtin_amdgcn_readfirstlane(id)) == 0) {
+    row_products<T, 4, 4>(a, m0, r0 + wave * 4, 0, a.K, a.v);
+  } else if (m0 + wave < a.M) {
+    row_products<T, 1, 8>(a, m0 + wave, r0, 0, a.K, a.v);
+    row_products<T, 1, 8>(a, m0 + wave, r0 + 8, 0, a.K, a.v);
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void shrink_fours_kernel(AdapterArgs a) {
+  four_rows<T>(a, blockIdx.x * 4, (int)blockIdx.y * 16);
+}
+
 // v = A x for many tokens, on the matrix cores: tiles of 64 rows, a part of K
-// in chunks of 128.  blockIdx.y takes part blockIdx.y of K; the parts are
-// summed, in a fixed order, by the second kernel, so no atomics.
+// in chunks of 128.  blockIdx.y takes a part of K; the parts are summed, in a
+// fixed order, by the second kernel, so no atomics.  The first a.slices of
+// blockIdx.y share the rows of a tile of many requests instead (their whole
+// sums go to the first part, zeros to the others) and mostly leave at once.
 // A chunk of x and of the request's A go through LDS: sixteen lanes read 256
 // contiguous bytes of a row (a matrix operand read from memory directly has
 // its neighbouring lanes in 16 different rows, which costs the address unit
-// four times the cycles), and the operands come back as 16-byte reads from
-// rows 16 bytes further than 256 apart, which spread over the banks.  The
+// four times the cycles), and the operands come back as 16-byte reads; the
+// 16-byte places of a row are exchanged by its number (place ^ row mod 16),
+// which spreads both over the banks.  The
 // next chunk's loads are in flight, in registers, while one is multiplied.
 // Wave w takes rows 16 w .. 16 w + 15 and all ranks, so sums stay in one
-// wave.  A tile of several requests runs over its part of K for each;
-// blockIdx.z takes every second of them, because where all workgroups are
-// resident at once a tile that runs twice (at the border of two prompts)
-// would double the kernel's time.
+// wave.  In a tile of several requests (at the border of two prompts) a chunk
+// of x is multiplied by each one's A before the next comes, with the other
+// requests' rows as zeros: x is read once, the sums stay in one set of
+// registers, and such a workgroup, of which some compute units get several,
+// ends soon after the others (16384 x 4096, rank 64, prompts of 1024 that end
+// inside a tile: 47 us; as a second pass over x 56; none ends inside: 41).
 template <class T, int RB>
-__global__ __launch_bounds__(256) void shrink_staged_kernel(AdapterArgs a) {
+__global__ __launch_bounds__(256, RB <= 4 ? 4 : 3) void shrink_staged_kernel(AdapterArgs a) {
   typedef typename Vec8Of<T>::V V8;
-  constexpr int TM = 64, KC = 128, kRow = KC + 8;
-  __shared__ __align__(16) T xs[TM][kRow], ws[16 * RB][kRow];
+  constexpr int TM = 64, KC = 128;
+  __shared__ __align__(16) T xs[TM][KC], ws[16 * RB][KC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, r16 = lane & 15, lg = lane >> 4;
   const int trow = threadIdx.x >> 4, tcol = (threadIdx.x & 15) * 8;  // this thread's place in 16 rows of a chunk
+  const int tplace = ((threadIdx.x & 15) ^ trow) * 8;  // and in LDS
   const uint32_t m0 = blockIdx.x * TM;
-  if (blockIdx.z) {  // mostly there is one request: leave at once
-    const int id = a.ids[min(m0 + lane, a.M - 1)];
-    if (__ballot(id != __builtin_amdgcn_readfirstlane(id)) == 0) return;
-  }
-  const Request mine = request_of<TM>(a, m0, lane);
-  const int first_k = (int)blockIdx.y * a.k_part, k1 = min(a.K, first_k + a.k_part);
-  if (Requests::exceed(mine, kRequestsAtMost)) {
-    // single tokens of many requests: row by row, half the rows to each z
-    for (int i = 0; i < 8; ++i)
-      for (int r = 0; r < a.R; r += 4)
-        row_products<T, 1, 4>(a, m0 + blockIdx.z * 32 + wave * 8 + i, r, first_k, k1, a.v + (long long)blockIdx.y * a.M * a.R);
+  const int id = id_of<TM>(a, m0, lane);
+  const bool many = many_requests(id);
+  if ((int)blockIdx.y < a.slices) {
+    if (!many) return;
+    const uint32_t rows = TM / a.slices, from = m0 + blockIdx.y * rows, to = min(from + rows, a.M);
+    for (uint32_t m = from; m < to; m += 4)
+      for (int r0 = 0; r0 < a.R; r0 += 16) four_rows<T>(a, m, r0);
+    for (int p = 1; p < a.parts; ++p)
+      for (uint32_t i = from * a.R + threadIdx.x; i < to * a.R; i += 256) a.v[(long long)p * a.M * a.R + i] = 0.0f;
     return;
   }
-  auto next = [&](Requests& q) {
-    bool more = q.next(mine);
-    for (unsigned z = 1; z < gridDim.z && more; ++z) more = q.next(mine);
-    return more;
-  };
-
+  if (many) return;
+  const Request mine = request_of(a, id);
+  const int part = (int)blockIdx.y - a.slices, first_k = part * a.k_part, k1 = min(a.K, first_k + a.k_part);
+  float* const v = a.v + (long long)part * a.M * a.R;
   const T* xrow[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t m = m0 + i * 16 + trow;
     xrow[i] = (const T*)a.x + (long long)(m < a.M ? m : a.M - 1) * a.xs;
   }
-  Requests ld, cp;
-  ld.begin(mine);
-  cp.begin(mine);
-  if (blockIdx.z) {
-    cp.next(mine);
-    ld.next(mine);
-  }
-  if (!cp.next(mine)) return;  // the same for the whole workgroup
-  ld.next(mine);
-  int lk = first_k, ck = first_k;
-  u32x4 xr[4], wr[RB];
-  const T* wrow[RB];
-  auto aim = [&]() {
-    const T* const w = (const T*)a.A + (long long)ld.id * a.R * a.K;
-#pragma unroll
-    for (int i = 0; i < RB; ++i) wrow[i] = w + (long long)min(i * 16 + trow, ld.rank - 1) * a.K;
-  };
-  auto load = [&]() {  // past the end: what was read before
-    const int at = lk + tcol < k1 ? lk + tcol : first_k;
+  u32x4 xr[4];
+  // past the end: what was read before
+  auto load_x = [&](int k) {
+    const int at = k + tcol < k1 ? k + tcol : first_k;
 #pragma unroll
     for (int i = 0; i < 4; ++i) xr[i] = *(const u32x4*)(xrow[i] + at);
+  };
+  Requests ld, cp;
+  ld.begin(mine);
+  if (!ld.next(mine)) return;  // the same for the whole workgroup
+  int lk = first_k;  // the chunk of A whose loads go out next, for request `ld`
+  u32x4 wr[RB];
+  auto load_w = [&]() {
+    const T* const w = (const T*)a.A + (long long)ld.id * a.R * a.K + (lk + tcol < k1 ? lk + tcol : first_k);
 #pragma unroll
-    for (int i = 0; i < RB; ++i) wr[i] = *(const u32x4*)(wrow[i] + at);
-    lk += KC;
-    if (lk >= k1 && next(ld)) {
-      lk = first_k;
-      aim();
+    for (int i = 0; i < RB; ++i) wr[i] = *(const u32x4*)(w + (long long)min(i * 16 + trow, ld.rank - 1) * a.K);
+    if (!ld.next(mine)) {
+      ld.begin(mine);
+      ld.next(mine);
+      lk += KC;
     }
   };
-  aim();
-  load();
+  load_x(first_k);
+  load_w();
   f32x4 acc[RB];
 #pragma unroll
   for (int i = 0; i < RB; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  while (true) {
+  for (int ck = first_k; ck < k1; ck += KC) {
     const bool in = ck + tcol < k1;
     const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *(u32x4*)&xs[i * 16 + trow][tcol] = in ? xr[i] : zero;
+    for (int i = 0; i < 4; ++i) *(u32x4*)&xs[i * 16 + trow][tplace] = in ? xr[i] : zero;
+    cp.begin(mine);
+    bool more = cp.next(mine), first = true;
+    do {
+      const bool own = (cp.rows >> (wave * 16 + r16)) & 1ull;
 #pragma unroll
-    for (int i = 0; i < RB; ++i) *(u32x4*)&ws[i * 16 + trow][tcol] = in ? wr[i] : zero;
-    __syncthreads();
-    load();
+      for (int i = 0; i < RB; ++i) *(u32x4*)&ws[i * 16 + trow][tplace] = in ? wr[i] : zero;
+      __syncthreads();
+      load_w();
+      if (first) load_x(ck + KC);
+      first = false;
 #pragma unroll
-    for (int k = 0; k < KC; k += 32) {
-      const V8 x = *(const V8*)&xs[wave * 16 + r16][k + lg * 8];
+      for (int k = 0; k < KC; k += 32) {
+        const int place = ((k / 8 + lg) ^ r16) * 8;
+        const u32x4 x = *(const u32x4*)&xs[wave * 16 + r16][place];
+        const V8 xo = __builtin_bit_cast(V8, own ? x : zero);
 #pragma unroll
-      for (int i = 0; i < RB; ++i) acc[i] = mma(x, *(const V8*)&ws[i * 16 + r16][k + lg * 8], acc[i]);
-    }
-    __syncthreads();
-    ck += KC;
-    if (ck >= k1) {
-      ck = first_k;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = wave * 16 + lg * 4 + j;
-        if ((cp.rows >> row) & 1ull) {
-          float* const v = a.v + ((long long)blockIdx.y * a.M + m0 + row) * a.R + r16;
-#pragma unroll
-          for (int i = 0; i < RB; ++i)
-            if (i * 16 + r16 < a.R) v[i * 16] = acc[i][j];
-        }
+        for (int i = 0; i < RB; ++i) acc[i] = mma(xo, *(const V8*)&ws[i * 16 + r16][place], acc[i]);
       }
+      more = cp.next(mine);
+      __syncthreads();
+    } while (more);
+  }
 #pragma unroll
-      for (int i = 0; i < RB; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (!next(cp)) break;
-    }
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t m = m0 + wave * 16 + lg * 4 + j;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+      if (i * 16 + r16 < a.R) v[(long long)m * a.R + i * 16 + r16] = acc[i][j];
   }
 }
 
@@ -382,7 +429,7 @@ struct alignas(VW * sizeof(YT)) Vector {
 };
 
 // The same for tiles of more than kRequestsAtMost requests (single tokens):
-// 16 rows of a tile of TM and 256 J columns, row by row without matrix cores.
+// the tile's rows, 16 at a time, and 256 J columns, without matrix cores.
 // A row's block of B is read in the order of memory, KB * 4 KB at a time; a
 // lane's eight ranks are summed over the lanes of a row of B.
 template <class T, class YT, int TM, int KB, int VW>
@@ -392,42 +439,47 @@ __global__ __launch_bounds__(256) void expand_singles_kernel(AdapterArgs a) {
   __shared__ __align__(16) float vf[16][RP + 4];
   __shared__ __align__(16) float turns[kWaves][16][68];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const Place place = place_of(a, (a.M + 15) / 16);
+  const Place place = place_of(a, (a.M + TM - 1) / TM);
   if (place.block >= a.blocks) return;
-  const uint32_t m0 = place.tile * 16 / TM * TM;
-  const int sub = (int)(place.tile * 16 - m0);  // these rows of the tile
-  const Request mine = request_of<TM>(a, m0, lane);
-  if (!Requests::exceed(mine, kRequestsAtMost)) return;  // expand_tiles_kernel's
-  for (int i = threadIdx.x; i < 16 * kLanes; i += 256) {
-    const int row = i / kLanes, r0 = (i - row * kLanes) * 8;
-    float f[8];
-    load_v(a, m0 + sub + row, r0, __shfl(mine.rank, sub + row), __shfl(mine.scale, sub + row), f);
-    *(f32x4*)&vf[row][r0] = f32x4{f[0], f[1], f[2], f[3]};
-    *(f32x4*)&vf[row][r0 + 4] = f32x4{f[4], f[5], f[6], f[7]};
-  }
-  __syncthreads();
+  const uint32_t m0 = place.tile * TM;
+  const int id = id_of<TM>(a, m0, lane);
+  if (!many_requests(id)) return;  // expand_tiles_kernel's
+  const Request mine = request_of(a, id);
   float(*const turn)[68] = turns[wave];
   const int brow = lane / kLanes, bcol = lane % kLanes, brank = bcol * 8;
   const int prow = lane / (64 / VW), pcol = (lane % (64 / VW)) * VW;
-  for (int j = 0; j < a.columns; ++j) {
-    const int n0 = (place.block * a.columns + j) * 256 + wave * 64;
-    if (n0 >= a.N) return;
-    constexpr int kAtOnce = KB == 1 ? 4 : 2;  // rows whose loads are in flight together
-#pragma unroll 1
-    for (int i = 0; i < 16; i += kAtOnce) {
+  constexpr int kAtOnce = KB == 1 ? 4 : 2;  // rows whose loads are in flight together
+  for (int sub = 0; sub < TM && m0 + sub < a.M; sub += 16) {
+    for (int i = threadIdx.x; i < 16 * kLanes; i += 256) {
+      const int row = i / kLanes, r0 = (i - row * kLanes) * 8;
+      float f[8];
+      load_v(a, m0 + sub + row, r0, __shfl(mine.rank, sub + row), __shfl(mine.scale, sub + row), f);
+      *(f32x4*)&vf[row][r0] = f32x4{f[0], f[1], f[2], f[3]};
+      *(f32x4*)&vf[row][r0 + 4] = f32x4{f[4], f[5], f[6], f[7]};
+    }
+    __syncthreads();
+    for (int j = 0; j < a.columns; ++j) {
+      const int n0 = (place.block * a.columns + j) * 256 + wave * 64;
+      if (n0 >= a.N) break;
       u32x4 w[kAtOnce][4 * KB];
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const int id = max(__builtin_amdgcn_readlane(mine.id, sub + i + u), 0);  // none: of rank 0, any will do
-        const int rank = __builtin_amdgcn_readlane(mine.rank, sub + i + u);
+      auto load_b = [&](int u, int row) {
+        const int id = max(__builtin_amdgcn_readlane(mine.id, sub + row), 0);  // none: of rank 0, any will do
+        const int rank = __builtin_amdgcn_readlane(mine.rank, sub + row);
         const T* const at = (const T*)a.B + (long long)id * a.N * a.R + (brank < rank ? brank : 0);
 #pragma unroll
         for (int c = 0; c < 4 * KB; ++c) w[u][c] = *(const u32x4*)(at + (long long)min(n0 + c * kAcross + brow, a.N - 1) * a.R);
-      }
+      };
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const int used = __builtin_amdgcn_readlane(mine.rank, sub + i + u) - brank;  // of this lane's eight ranks
-        const f32x4 v0 = *(const f32x4*)&vf[i + u][brank], v1 = *(const f32x4*)&vf[i + u][brank + 4];
+      for (int u = 0; u < kAtOnce; ++u) load_b(u, u);
+      Vector<YT, VW> y[16 / VW];  // N is a multiple of VW; past the end the last one
+#pragma unroll
+      for (int i = 0; i < 16 / VW; ++i)
+        y[i] = *(const Vector<YT, VW>*)((const YT*)a.y + (long long)min(m0 + sub + i * VW + prow, a.M - 1) * a.ys + min(n0 + pcol, a.N - VW));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int u = i % kAtOnce;
+        const int used = __builtin_amdgcn_readlane(mine.rank, sub + i) - brank;  // of this lane's eight ranks
+        const f32x4 v0 = *(const f32x4*)&vf[i][brank], v1 = *(const f32x4*)&vf[i][brank + 4];
         float own = 0.0f;
 #pragma unroll
         for (int c = 0; c < 4 * KB; ++c) {
@@ -441,23 +493,24 @@ __global__ __launch_bounds__(256) void expand_singles_kernel(AdapterArgs a) {
           if (KB >= 4) s = dpp_add<kRowMirror>(s);
           if (bcol == c) own = s;  // the sum is in all lanes of the row: lane c keeps the c-th
         }
-        if (bcol < 4 * KB) turn[i + u][bcol * kAcross + brow] = own;
+        turn[i][bcol * kAcross + brow] = own;
+        if (i + kAtOnce < 16) load_b(u, i + kAtOnce);
       }
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < 16 / VW; ++i) {
-      const uint32_t m = m0 + sub + i * VW + prow;
-      if (m >= a.M || n0 + pcol >= a.N) continue;
-      const Vector<YT, VW> y = *(const Vector<YT, VW>*)((const YT*)a.y + (long long)m * a.ys + n0 + pcol);
-      Vector<YT, VW> o;
+      for (int i = 0; i < 16 / VW; ++i) {
+        const uint32_t m = m0 + sub + i * VW + prow;
+        if (m >= a.M || n0 + pcol >= a.N) continue;
+        Vector<YT, VW> o;
 #pragma unroll
-      for (int c = 0; c < VW; ++c) o.e[c] = (YT)((float)y.e[c] + turn[i * VW + prow][pcol + c]);
-      *(Vector<YT, VW>*)((YT*)a.out + (long long)m * a.os + n0 + pcol) = o;
+        for (int c = 0; c < VW; ++c) o.e[c] = (YT)((float)y[i].e[c] + turn[i * VW + prow][pcol + c]);
+        *(Vector<YT, VW>*)((YT*)a.out + (long long)m * a.os + n0 + pcol) = o;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    __syncthreads();
   }
 }
 
@@ -496,10 +549,11 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(AdapterArgs a) {
   const Place place = place_of(a, (a.M + TM - 1) / TM);
   if (place.block >= a.blocks) return;
   const uint32_t m0 = place.tile * TM;
-  const Request mine = request_of<TM>(a, m0, lane);
+  const int id = id_of<TM>(a, m0, lane);
+  if (many_requests(id)) return;  // expand_singles_kernel's
+  const Request mine = request_of(a, id);
 
   // v of the tile: the parts of K summed, the adapter's scale applied, split
-  if (Requests::exceed(mine, kRequestsAtMost)) return;  // expand_singles_kernel's
   constexpr int kPer = RP / 8;  // threads on a row, within a wave
   for (int i = threadIdx.x; i < TM * kPer; i += 256) {
     const int row = i / kPer, r0 = (i - row * kPer) * 8;
@@ -691,11 +745,11 @@ template <class T>
 hipError_t launch_shrink(const AdapterArgs& a, hipStream_t stream) {
   const dim3 block(256);
   if (a.M <= kFewTokens) {
-    shrink_rows_kernel<T, 1, 1><<<dim3(a.M, (a.R + 3) / 4), block, 0, stream>>>(a);
+    shrink_rows_kernel<T><<<dim3(a.M, (a.R + 3) / 4), block, 0, stream>>>(a);
   } else if (a.M <= kSomeTokens) {
-    shrink_rows_kernel<T, 4, 4><<<dim3((a.M + 3) / 4, (a.R + 15) / 16), block, 0, stream>>>(a);
+    shrink_fours_kernel<T><<<dim3((a.M + 3) / 4, (a.R + 15) / 16), block, 0, stream>>>(a);
   } else {
-    const dim3 grid((a.M + 63) / 64, a.parts, 2);
+    const dim3 grid((a.M + 63) / 64, a.slices + a.parts);
     const int rb = (a.R + 15) / 16;
     if (rb == 1) shrink_staged_kernel<T, 1><<<grid, block, 0, stream>>>(a);
     else if (rb == 2) shrink_staged_kernel<T, 2><<<grid, block, 0, stream>>>(a);
@@ -711,7 +765,7 @@ hipError_t launch_expand_kb(AdapterArgs a, int mb, hipStream_t stream) {
     const uint64_t across = a.blocks >= 8 ? (a.blocks + 7) / 8 * 8 : a.blocks;
     return (a.M + rows - 1) / rows * across;
   };
-  if (grid(16) >= (1ull << 22)) return hipErrorInvalidConfiguration;  // 2^32 threads: no memory holds such an out
+  if (grid(16) >= (1ull << 24)) return hipErrorInvalidConfiguration;  // 2^32 threads
   constexpr int kInFlight = KB == 1 ? 4 : KB == 2 ? 2 : 1;  // requests whose blocks of B are loaded together
   if (mb == 1) expand_tiles_kernel<T, YT, 1, KB, VW, kInFlight><<<dim3(grid(16)), dim3(256), 0, stream>>>(a);
   else expand_tiles_kernel<T, YT, 4, KB, VW, 1><<<dim3(grid(64)), dim3(256), 0, stream>>>(a);
@@ -722,7 +776,7 @@ hipError_t launch_expand_kb(AdapterArgs a, int mb, hipStream_t stream) {
     a.blocks = (a.N + 255) / 256;
     expand_singles_kernel<T, YT, 16, KB, VW><<<dim3(grid(16)), dim3(256), 0, stream>>>(a);
   } else {
-    expand_singles_kernel<T, YT, 64, KB, VW><<<dim3(grid(16)), dim3(256), 0, stream>>>(a);
+    expand_singles_kernel<T, YT, 64, KB, VW><<<dim3(grid(64)), dim3(256), 0, stream>>>(a);
   }
   return hipGetLastError();
 }
@@ -738,7 +792,10 @@ hipError_t launch_expand(const AdapterArgs& a, int mb, hipStream_t stream) {
 template <class T, class YT>
 hipError_t launch_y(AdapterArgs& a, const Cut& c, hipStream_t stream) {
   if (c.mb == 0) {
-    expand_rows_kernel<T, YT><<<dim3(a.M, (a.N + 255) / 256), dim3(256), 0, stream>>>(a);
+    const dim3 grid(a.M, (a.N + 255) / 256);
+    if (a.R <= 32) expand_rows_kernel<T, YT, 1><<<grid, dim3(256), 0, stream>>>(a);
+    else if (a.R <= 64) expand_rows_kernel<T, YT, 2><<<grid, dim3(256), 0, stream>>>(a);
+    else expand_rows_kernel<T, YT, 4><<<grid, dim3(256), 0, stream>>>(a);
     return hipGetLastError();
   }
   // y's and out's rows in vectors of eight, four or single elements
@@ -811,6 +868,7 @@ extern "C" orbit_status orbit_adapter_add(const orbit_adapter_args* p, hipStream
   a.R = (int)p->rank;
   const Cut c = cut_of(p->M, p->K, p->N);
   a.parts = c.parts;
+  a.slices = p->M > 4096 ? 4 : 16;  // a thousand short workgroups at most, or 16 rows to each
   a.k_part = c.k_part;
   a.columns = c.columns;
   a.blocks = (a.N + 256 * c.columns - 1) / (256 * c.columns);

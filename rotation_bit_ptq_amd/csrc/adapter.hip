@@ -2,8 +2,11 @@
 // projection, out[m] = y[m] + s_a B_a (A_a x[m]), a = ids[m].
 //
 // Bound: memory (x, y and out once; the adapters in use once, then from L2).
-// Two launches: v = A x into the workspace, then out = y + s B v; v stays in
-// float32.
+// Two products: v = A x into the workspace, then out = y + s B v; v stays in
+// float32.  16384 tokens of 8 adapters, rank 64, 4096 -> 4096: 118 us (3.5
+// TB/s), 48 + 70; 1003 tokens of 48 adapters, rank 32 and less, 3072 ->
+// 12288, float32 y: 66 us; 64 tokens of 64 adapters, rank 16: 8 to 9 us,
+// twice the latency of a launch and of the chain id -> rank -> rows.
 #include "block_common.h"
 
 using namespace orbit;
@@ -26,8 +29,11 @@ struct AdapterArgs {
 };
 
 constexpr int kWaves = 4;
-constexpr int kRequestsAtMost = 4;  // of a tile, past which its rows go one by one
-constexpr int kFewTokens = 128, kSomeTokens = 1024;  // see cut_of
+// Adapters of a tile, past which its rows go one by one.  Tiles of 16 rows,
+// 1003 tokens, 3072 -> 12288, rank 32, the whole call: six adapters a tile
+// 58 us as a tile and 79 by rows, eight 64 and 73, sixteen 75 by rows.
+constexpr int kRequestsAtMost = 8;
+constexpr int kFewTokens = 256, kSomeTokens = 1024;  // see cut_of
 
 // The adapter's rank, 0 where there is none.
 __device__ __forceinline__ int rank_of(const AdapterArgs& a, int id) {
@@ -714,10 +720,16 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(AdapterArgs a) {
   }
 }
 
-// How a call is cut.
-//   up to kFewTokens: a wave per (token, rank), a thread per (token, column);
-//   up to kSomeTokens: a wave per (4 tokens, 4 ranks), expand in tiles;
-//   more: both in tiles, K in parts that fill the compute units.
+// How a call is cut (times in us, K = N = 4096, rank 64, first + second product):
+//   up to kFewTokens: a wave per (token, rank) and per (token, 64 columns).
+//     128 tokens: 13, in tiles 14 for one adapter and 26 for eight in turn;
+//     256 tokens: 21, in tiles 14 and 28 (rank 16: 12, in tiles 13 and 20);
+//   up to kSomeTokens: a workgroup per (4 tokens, 16 ranks), expand in tiles;
+//   more: both in tiles, K in parts that fill the compute units.  The first
+//     product of 1024 tokens: 16 for one adapter and 31 for eight in turn by
+//     fours, of 1025 in tiles 10 and 52.
+// Expand's tiles have 64 rows where that leaves four workgroups per compute
+// unit (B's block is then read a quarter as often), else 16.
 struct Cut {
   int mb;  // expand's tiles: 16 mb rows (0: rows one by one)
   int parts, k_part, columns;

@@ -286,10 +286,10 @@ __global__ __launch_bounds__(256) void shrink_fours_kernel(AdapterArgs a) {
 // next chunk's loads are in flight, in registers, while one is multiplied.
 // Wave w takes rows 16 w .. 16 w + 15 and all ranks, so sums stay in one
 // wave.  In a tile of several requests (at the border of two prompts) a chunk
-// of x is multiplied by each one's A before the next comes, with the other
-// requests' rows as zeros: x is read once, the sums stay in one set of
-// registers, and such a workgroup, of which some compute units get several,
-// ends soon after the others (16384 x 4096, rank 64, prompts of 1024 that end
+// of x is multiplied by each one's A before the next comes, and only its own
+// rows keep the sums (zeros for the others' x would not do: an infinite
+// weight would reach them).  So x is read once and such a workgroup, of which
+// some compute units get several, ends soon after the others (16384 x 4096, rank 64, prompts of 1024 that end
 // inside a tile: 47 us; as a second pass over x 56; none ends inside: 41).
 template <class T, int RB>
 __global__ __launch_bounds__(256, RB <= 4 ? 4 : 3) void shrink_staged_kernel(AdapterArgs a) {
@@ -357,21 +357,27 @@ __global__ __launch_bounds__(256, RB <= 4 ? 4 : 3) void shrink_staged_kernel(Ada
     cp.begin(mine);
     bool more = cp.next(mine), first = true;
     do {
-      const bool own = (cp.rows >> (wave * 16 + r16)) & 1ull;
 #pragma unroll
       for (int i = 0; i < RB; ++i) *(u32x4*)&ws[i * 16 + trow][tplace] = in ? wr[i] : zero;
       __syncthreads();
       load_w();
       if (first) load_x(ck + KC);
       first = false;
+      f32x4 sum[RB];
+#pragma unroll
+      for (int i = 0; i < RB; ++i) sum[i] = acc[i];
 #pragma unroll
       for (int k = 0; k < KC; k += 32) {
         const int place = ((k / 8 + lg) ^ r16) * 8;
-        const u32x4 x = *(const u32x4*)&xs[wave * 16 + r16][place];
-        const V8 xo = __builtin_bit_cast(V8, own ? x : zero);
+        const V8 x = *(const V8*)&xs[wave * 16 + r16][place];
 #pragma unroll
-        for (int i = 0; i < RB; ++i) acc[i] = mma(xo, *(const V8*)&ws[i * 16 + r16][place], acc[i]);
+        for (int i = 0; i < RB; ++i) sum[i] = mma(x, *(const V8*)&ws[i * 16 + r16][place], sum[i]);
       }
+      const uint32_t own = (uint32_t)(cp.rows >> (wave * 16 + lg * 4));
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = (own >> j) & 1u ? sum[i][j] : acc[i][j];
       more = cp.next(mine);
       __syncthreads();
     } while (more);

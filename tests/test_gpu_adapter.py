@@ -167,6 +167,30 @@ def test_a_broken_adapter_or_token_stays_alone(gpu_lib, M, xt):
     assert torch.isnan(got[ids == 2]).all() and not torch.isfinite(got[ids == 1]).any()
 
 
+@pytest.mark.parametrize("M", [400, 1100, 2100])
+@pytest.mark.parametrize("run", [1, 3, 9, 50])
+def test_a_broken_adapter_stays_alone_among_many_tokens(gpu_lib, M, run):
+    # runs of `run` tokens of each of 13 adapters: tiles of one, a few and many
+    # of them, borders inside tiles; R 40: three blocks of ranks, one not whole
+    rng = np.random.default_rng(M + run)
+    L, R, t = 13, 40, torch.float16
+    x, _ = draw(rng, (M, 264), t)
+    y, _ = draw(rng, (M, 136), torch.float32)
+    A, _ = draw(rng, (L, R, 264), t, 1 / 16)
+    B, _ = draw(rng, (L, 136, R), t)
+    ids = torch.tensor([m // run % (L + 1) - 1 for m in range(M)], dtype=torch.int32, device="cuda")
+    good = gpu_lib.adapter_add(y, x, A, B, ids)
+    A2, B2, x2 = A.clone(), B.clone(), x.clone()
+    A2[2] = float("inf")
+    A2[5] = float("nan")
+    B2[7] = float("nan")
+    x2[ids == 9] = float("nan")
+    got = gpu_lib.adapter_add(y, x2, A2, B2, ids)
+    bad = (ids == 2) | (ids == 5) | (ids == 7) | (ids == 9)
+    assert torch.equal(got[~bad], good[~bad])
+    assert torch.isfinite(good).all() and not torch.isfinite(got[bad]).any()
+
+
 @pytest.mark.parametrize("M", [10, 150])
 def test_large_values_do_not_overflow_between_the_products(gpu_lib, M):
     # A x reaches 4e6, past float16's largest number; B brings it back

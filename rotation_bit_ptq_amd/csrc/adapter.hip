@@ -309,7 +309,8 @@ __global__ __launch_bounds__(256, RB <= 4 ? 4 : 3) void shrink_staged_kernel(Ada
     for (uint32_t m = from; m < to; m += 4)
       for (int r0 = 0; r0 < a.R; r0 += 16) four_rows<T>(a, m, r0);
     for (int p = 1; p < a.parts; ++p)
-      for (uint32_t i = from * a.R + threadIdx.x; i < to * a.R; i += 256) a.v[(long long)p * a.M * a.R + i] = 0.0f;
+      for (long long i = (long long)from * a.R + threadIdx.x; i < (long long)to * a.R; i += 256)
+        a.v[(long long)p * a.M * a.R + i] = 0.0f;
     return;
   }
   if (many) return;

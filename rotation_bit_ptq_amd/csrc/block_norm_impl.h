@@ -9,7 +9,10 @@
 // elements (two, past 4096), so that registers stay few and many waves have
 // their loads in flight: with up to eight vectors per lane and one wave per
 // row, without any barrier, 16384 rows of 3072 took 133 us.  The parameters'
-// loads go out before the reductions and come from L1 or L2.
+// loads go out before the reductions and come from L1 or L2.  4096 x 3072
+// bf16 with gate, scale and shift: 21 us (4.8 TB/s, a copy's rate); 32768 x
+// 2048 float32 with float32 parameters and a norm on both sides: 188 us (4.3
+// TB/s: a row's parameters are 40 KB from L2 beside its 24 KB).
 //
 // A layer norm centres the values before it squares them: each wave about
 // its own mean, joined by M2 = sum M2_w + sum n_w (mean_w - mean)^2, which

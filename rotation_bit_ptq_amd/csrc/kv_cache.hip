@@ -11,7 +11,8 @@
 // register stages and log2(D / 8) exchanges between lanes of the group, the
 // row maximum one reduction over it.  The other half of a pair (x[i + rot/2])
 // is loaded a second time rather than exchanged: the line is in L1, and any
-// rot_dim works alike.
+// rot_dim works alike.  16384 tokens of 32 + 8 + 8 heads of 128 in bf16: 88
+// us (4.7 TB/s); 4099 of 24 + 4 + 4 in the int8 cache 17 us, read back 5.
 #include "kv_cache.h"
 
 using namespace orbit;

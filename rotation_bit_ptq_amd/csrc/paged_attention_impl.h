@@ -5,7 +5,10 @@
 // cache).
 //
 // Bound: memory; per byte of a 16-bit cache there are 2 (q_heads / kv_heads)
-// multiply-adds.
+// multiply-adds.  64 ragged requests of up to 8192 tokens, 32 / 8 heads of
+// 128 in bf16: 180 us (5.2 TB/s); 16 of up to 65000 in int8, 24 / 4 heads:
+// 124 us (3.8 TB/s, bound by the loads that three workgroups per compute unit
+// keep in flight); one of 700 tokens: 10 us, two launches.
 //
 // Split.  A workgroup of four waves takes one key head of one request, up to
 // 16 of the query heads that share it, and `chunk` tokens; wave w takes the
@@ -20,8 +23,8 @@
 //   registers.  Keys are loaded like values, whole rows by neighbouring
 //   lanes, and pass through LDS: read from memory in the operands' order
 //   (neighbouring lanes in 16 rows) they cost the address unit four times
-//   the cycles, and the second load of a line waits for the first's.  A lane then holds head l % 16 and tokens 4 (l / 16)
-//   + i of each half tile.
+//   the cycles, and the second load of a line waits for the first's.  A lane
+//   then holds head l % 16 and tokens 4 (l / 16) + i of each half tile.
 //   O^T = V^T P^T: those lanes' probabilities are the B operand as they
 //   stand if operand slot 8 g + j means token 4 g + j of the first half
 //   (j < 4) or 4 g + j - 4 of the second.  A = V^T needs four tokens of one

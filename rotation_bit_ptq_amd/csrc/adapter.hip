@@ -5,7 +5,7 @@
 // Two products: v = A x into the workspace, then out = y + s B v; v stays in
 // float32.  16384 tokens of 8 adapters, rank 64, 4096 -> 4096: 118 us (3.5
 // TB/s), 48 + 70; 1003 tokens of 48 adapters, rank 32 and less, 3072 ->
-// 12288, float32 y: 66 us; 64 tokens of 64 adapters, rank 16: 8 to 9 us,
+// 12288, float32 y: 66 us; 64 tokens of 64 adapters, rank 16: 8.2 to 9.0 us,
 // twice the latency of a launch and of the chain id -> rank -> rows.
 #include "block_common.h"
 

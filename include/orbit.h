@@ -462,7 +462,10 @@ orbit_status orbit_kv_read(const orbit_kv_cache *cache, const int64_t *slots, in
  * page_size].  A row with nothing to see (len <= 0) gives out = 0, lse =
  * -inf; lengths past table_width * page_size are cut there, and a table
  * entry outside the cache hides its page's tokens.  What lies in the cache
- * outside the seen tokens is never used.
+ * outside the seen tokens is never used.  Scores, maxima and denominators
+ * are float32; a weight is multiplied with its value as two 16-bit numbers,
+ * within 2^-16 of itself in a BF16 cache, and in F16 and INT8 caches within
+ * 2^-21 or 2^-39 of the head's largest, whichever is more.
  * q: [batch, q_heads, head_dim] by strides, rows 16-byte aligned, BF16 or
  * F16; its type is the cache's, either one for an int8 cache.  out: [batch,
  * q_heads, head_dim] contiguous, of q's type, 16-byte aligned.  lse: float

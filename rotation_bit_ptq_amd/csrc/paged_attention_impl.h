@@ -31,13 +31,22 @@
 //   coordinate side by side: values go through the wave's own LDS rows and
 //   come back by the transposing read (ds_read_b64_tr_b16).
 // Probabilities are multiplied as hi + lo pairs of 16-bit numbers (two
-// products), so no accuracy is lost to the operand type.
+// products): 16 bits of each in bf16, for an output that keeps 8; 22 in fp16,
+// for one that keeps 11 (8 with bf16 queries on an int8 cache).  bf16 has
+// float32's range.  fp16 does not, and a context's many small weights may be
+// all there is of an output (where the largest belongs to a token whose value
+// is zero), so fp16 operands hold 2^15 p (kLift): their steps begin at 2^-39
+// of the largest weight, a loss of 2^-19 of it over a million tokens (without
+// the factor they began at 2^-24, and such outputs were 3 % off where the
+// largest score led by 14; the time is the same, 124.6 us for the int8 case).
+// The denominator is a float32 sum of unsplit weights.
 //
 // INT8 cache: codes become fp16 integers exactly (a byte permute and one
 // packed subtraction).  A key's scale multiplies its score.  A value's scale
 // goes into its probability, with the running maximum taken of z_t +
 // log2(scale_t), so that the products stay in [0, 1] whatever the scales'
-// size.  Queries are scaled by a power of two per head to fit fp16.
+// size (before the lift).  Queries are scaled by a power of two per head to
+// fit fp16.
 #pragma once
 
 #include "kv_cache.h"
@@ -132,8 +141,12 @@ struct Stage {
   }
 };
 
-// Two probabilities as a hi + lo pair of 16-bit numbers.  fp16: both parts
-// rounded toward zero (one instruction for two), 20 bits together.
+// log2 of the factor on the probabilities: 2^15 is half of fp16's range, and
+// rounding of large scores (a step of 16 at 2^27) stays within the other half.
+constexpr float lift_of(int format) { return format == ORBIT_KV_BF16 ? 0.0f : 15.0f; }
+
+// Two probabilities as a hi + lo pair of 16-bit numbers.  fp16: hi is rounded
+// toward zero and lo to nearest (one instruction for two each).
 __device__ __forceinline__ void split2(float p0, float p1, bf16x8& hi, bf16x8& lo, int j) {
   hi[j] = (__bf16)p0;
   hi[j + 1] = (__bf16)p1;
@@ -143,7 +156,8 @@ __device__ __forceinline__ void split2(float p0, float p1, bf16x8& hi, bf16x8& l
 __device__ __forceinline__ void split2(float p0, float p1, f16x8& hi, f16x8& lo, int j) {
   typedef _Float16 h2 __attribute__((ext_vector_type(2)));
   const h2 h = __builtin_bit_cast(h2, __builtin_amdgcn_cvt_pkrtz(p0, p1));
-  const h2 l = __builtin_bit_cast(h2, __builtin_amdgcn_cvt_pkrtz(p0 - (float)h[0], p1 - (float)h[1]));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const h2 l = __builtin_convertvector((f2{p0 - (float)h[0], p1 - (float)h[1]}), h2);
   hi[j] = h[0];
   hi[j + 1] = h[1];
   lo[j] = l[0];
@@ -168,6 +182,7 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
   constexpr int kVLoads = kTile / kRowsAtOnce;
   constexpr int kBlocks = DP / 16;
   constexpr int kElem = kCoded ? 1 : 2;
+  constexpr float kLift = lift_of(F);
 
   typedef Stage<DP * kElem> Sk;  // keys as the cache holds them
   typedef Stage<DP * 2> Sv;      // values in 16 bits
@@ -415,7 +430,7 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
 #pragma unroll
         for (int d = 0; d < kBlocks; ++d) o[d] *= alpha;
       }
-      const float m_use = m_run == -__builtin_inff() ? 0.0f : m_run;
+      const float m_use = m_run == -__builtin_inff() ? 0.0f : m_run - kLift;
       V8 hi, lo;
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
@@ -470,7 +485,9 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
   }
   l_run = add_rows32(add_rows16(l_run));
 
-  // the four waves' sums meet
+  // the four waves' sums meet; from here on the maximum stands for the lifted
+  // one, that the sums are relative to
+  m_run -= kLift;
   __syncthreads();
   float* const so = (float*)lds;                     // [wave][head][DP]
   float* const sm = (float*)(lds + kWaves * 16 * DP * 4);  // [wave][head], then the sums

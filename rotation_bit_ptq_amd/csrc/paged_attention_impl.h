@@ -251,9 +251,10 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
 
   // Loads are unconditional, so that none waits for another: tokens that are
   // not seen read page 0 (or the rest of their own page), coordinates past
-  // head_dim the row's last vector again; scores of the former are masked and
-  // their values cleared, the latter meet zeros of the queries or are results
-  // that are not stored.
+  // head_dim the row's last vector again.  Scores of the former are masked and
+  // their values cleared.  The latter are results that are not stored (values)
+  // or meet zeros of the queries (keys: codes are finite, 16-bit ones are
+  // cleared, as an infinite one times zero would be NaN).
   u32x4 kr[kVLoads], vr[kVLoads];
   u32x2 ksr[2], vsr[2];
   const int row_bytes = dim * kElem;
@@ -365,6 +366,10 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
     for (; tile < c1; tile += kStep) {
       const uint32_t live = now.live;
       // scores of the tile
+      if (!kCoded && dim < DP) {
+#pragma unroll
+        for (int i = 0; i < kVLoads; ++i) kr[i] = lcol * 8 < dim ? kr[i] : u32x4{0u, 0u, 0u, 0u};
+      }
 #pragma unroll
       for (int i = 0; i < kVLoads; ++i)
         *(u32x4*)(kstage + i * kRowsAtOnce * DP * kElem + (kwrite ^ (Sk::key(i * kRowsAtOnce) << 4))) = kr[i];

@@ -391,7 +391,9 @@ int64_t orbit_adapter_workspace(int64_t M, int64_t K, int64_t rank);
  * ORBIT_KV_F16 hold the values; ORBIT_KV_INT8 holds codes, symmetric in
  * [-127, 127] with one fp16 scale per (token, head), scale =
  * fp16(max|x| / 127), code = round_half_even(x / scale) (0 where scale is
- * 0): the group format of orbit_int8_pack_weights with group = head_dim.
+ * 0; where max|x| is infinite, NaN, or past fp16's range times 127, the scale
+ * is not finite and the head's values read back as infinities or NaN): the
+ * group format of orbit_int8_pack_weights with group = head_dim.
  * k_scale, v_scale: device uint16 (fp16 bits) [pages, kv_heads, page_size],
  * INT8 only, 16-byte aligned.  page_size a power of two, 1 .. 1024 (INT8: 4
  * .. 1024); head_dim a multiple of 8 (INT8: 16), 8 .. 256; 1 <= kv_heads <=

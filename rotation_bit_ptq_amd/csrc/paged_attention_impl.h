@@ -40,6 +40,13 @@
 // the factor they began at 2^-24, and such outputs were 3 % off where the
 // largest score led by 14; the time is the same, 124.6 us for the int8 case).
 // The denominator is a float32 sum of unsplit weights.
+// Such a pair has no product with an infinite value: lo may be zero or below.
+// A wave that ends with a NaN therefore looks through its tokens once more,
+// outside the loop: the infinite values decide (the test for a NaN takes 0.6 of
+// the 180 us; pairs that are never zero or below would take a maximum each, in
+// the loop, and add a little of every hidden weight).  Factors on sums (rescaling,
+// joining) do not go below float32's smallest normal number, so that an
+// infinite sum stays infinite.
 //
 // INT8 cache: codes become fp16 integers exactly (a byte permute and one
 // packed subtraction).  A key's scale multiplies its score.  A value's scale
@@ -163,6 +170,9 @@ __device__ __forceinline__ void split2(float p0, float p1, f16x8& hi, f16x8& lo,
   lo[j] = l[0];
   lo[j + 1] = l[1];
 }
+
+// A factor on sums: never zero, so that an infinite one stays infinite.
+__device__ __forceinline__ float factor(float log2) { return fmaxf(__builtin_amdgcn_exp2f(log2), 1.17549435e-38f); }
 
 // Q: the queries' format (BF16 or F16); F: the cache's; DP: head_dim rounded
 // up to 64, 128 or 256; PAGED16: pages of 16 tokens or more, so that half a
@@ -429,7 +439,7 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
       mt = max_rows32(max_rows16(mt));
       if (__any(mt > m_run)) {
         const float m_new = fmaxf(m_run, mt);
-        const float alpha = __builtin_amdgcn_exp2f(m_run - (m_new == -__builtin_inff() ? 0.0f : m_new));
+        const float alpha = factor(m_run - (m_new == -__builtin_inff() ? 0.0f : m_new));
         m_run = m_new;
         l_run *= alpha;
 #pragma unroll
@@ -488,6 +498,60 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
       order();
     }
   }
+  if constexpr (!kCoded) {
+    f32x4 all = o[0];
+#pragma unroll
+    for (int d = 1; d < kBlocks; ++d) all += o[d];
+    const float one = (all[0] + all[1]) + (all[2] + all[3]);
+    if (__any(one != one)) {  // a NaN, or infinities of both signs
+      uint64_t lost = 0;      // bit 4 d + i: sum i of block d is NaN
+#pragma unroll
+      for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lost |= (uint64_t)(o[d][i] != o[d][i]) << (4 * d + i);
+      // Such a sum again, of the infinite (and NaN) values alone: each by 1 if
+      // its token has a weight, by 0 at a score of minus infinity, by NaN at
+      // one that is infinite or NaN.
+#pragma unroll
+      for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d][i] = (lost >> (4 * d + i)) & 1u ? 0.0f : o[d][i];
+#pragma unroll 1
+      for (int from = c0 + wave * kTile; from < c1; from += kWaves * kTile)
+#pragma unroll 1
+        for (int t = max(from, span.lo); t < min(from + kTile, c1); ++t) {
+          const uint32_t page = (uint32_t)table[t >> a.c.page_shift];
+          if (page >= a.c.pages) continue;
+          const long long at = cache_row(a.c, page, head, (uint32_t)t & a.c.page_mask) * dim;
+          float z = 0.0f;
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            if (s * 32 + lg * 8 >= dim) continue;
+            const Vec8<T> k = *(const Vec8<T>*)((const T*)a.c.k + at + s * 32 + lg * 8);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z = fmaf((float)qf[s][j], (float)k.e[j], z);
+          }
+          z = add_rows32(add_rows16(z)) * zscale;
+          const float w = z == -__builtin_inff() ? 0.0f : z < __builtin_inff() ? 1.0f : __builtin_nanf("");
+#pragma unroll
+          for (int d = 0; d < kBlocks; ++d) {
+            if (d * 16 + lg * 4 >= dim) continue;
+            T v[4];
+            __builtin_memcpy(v, (const T*)a.c.v + at + d * 16 + lg * 4, sizeof v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float x = fabsf((float)v[i]) < __builtin_inff() ? 0.0f : (float)v[i];
+              o[d][i] = (lost >> (4 * d + i)) & 1u ? fmaf(w, x, o[d][i]) : o[d][i];
+            }
+          }
+        }
+      // none of them: the NaN has another cause, and stays
+#pragma unroll
+      for (int d = 0; d < kBlocks; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d][i] = (lost >> (4 * d + i)) & 1u && o[d][i] == 0.0f ? __builtin_nanf("") : o[d][i];
+    }
+  }
   l_run = add_rows32(add_rows16(l_run));
 
   // the four waves' sums meet; from here on the maximum stands for the lifted
@@ -514,7 +578,7 @@ __global__ __launch_bounds__(256, residents(F, DP, PAGED16)) void attend_kernel(
     float l = 0.0f, f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      const float e = __builtin_amdgcn_exp2f(sm[w * 16 + h] - m_use);
+      const float e = factor(sm[w * 16 + h] - m_use);
       l = fmaf(e, sm[kWaves * 16 + w * 16 + h], l);
       const f32x4 x = *(const f32x4*)(so + (w * 16 + h) * DP + d), y = *(const f32x4*)(so + (w * 16 + h) * DP + d + 4);
 #pragma unroll
@@ -571,7 +635,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a) {
 #pragma unroll 4
     for (int c = g; c < n; c += groups) {
       const float2 x = ml[c];
-      const float e = __builtin_amdgcn_exp2f(x.x - m_use);
+      const float e = factor(x.x - m_use);
       const f32x4 v = part[(long long)c * lanes];
       l = fmaf(e, x.y, l);
 #pragma unroll

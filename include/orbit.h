@@ -368,6 +368,9 @@ orbit_status orbit_block_norm(const orbit_block_norm_args *args, hipStream_t str
  * 0 <= M < ORBIT_MAX_ROWS, 0 <= N <= 2^22.
  * workspace: device, 16-byte aligned, orbit_adapter_workspace(M, K, rank)
  * bytes, overwritten; it holds A x, in float32, as partial sums over K.
+ * Sums are float32.  A x enters the second product in 24 bits, or, above 256
+ * tokens, in 22 bits of the token's largest for F16 x and in 16 bits for BF16
+ * x where y is not F32.
  * Errors: ORBIT_E_ARG, ORBIT_E_SHAPE, ORBIT_E_DTYPE, ORBIT_E_HIP. */
 typedef struct {
   const void *x, *A, *B, *y;

@@ -529,9 +529,12 @@ __global__ __launch_bounds__(256) void expand_singles_kernel(AdapterArgs a) {
 
 // out = y + s B v for tiles of 16 MB rows and 256 J columns, on the matrix
 // cores with the product transposed (rows of B are the A operand), so that a
-// lane's four results are neighbouring columns.  v enters as a pair of
-// 16-bit numbers (hi + lo, two products; for fp16 scaled by a power of two
-// per row), so it keeps float32's range and 16 (bf16) or 21 (fp16) bits.
+// lane's four results are neighbouring columns.  v enters as kTerms 16-bit
+// numbers, a product each: fp16 (scaled by a power of two per row, which keeps
+// float32's range) as two, 22 bits; bf16 as three, all 24 bits, where y is
+// float32, and as two, 16 bits, where out is rounded to 8 or 11 bits anyway.
+// (bf16 to float32, the third term: 16384 tokens, 4096 -> 4096, rank 64, 194 ->
+// 196 us; 8192 tokens, 2048 -> 4096, rank 128, 120 -> 124.)
 // The products of a tile's requests are kept in float32, each in its own
 // rows, and leave through the wave's LDS rows, 16 at a time, in the order in
 // which y is read and out written: neighbouring lanes on neighbouring
@@ -544,9 +547,8 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(AdapterArgs a) {
   typedef Vector<YT, VW> Part;
   constexpr int kRow = RP + 8;  // 16 bytes further per row: the operand reads spread over the banks
   constexpr int kPasses = 16 / VW;  // of VW rows each over 16 rows, 64 / VW lanes on a row
-  __shared__ __align__(16) T vpair[2][TM][kRow];
-  T(*const vhi)[kRow] = vpair[0];
-  T(*const vlo)[kRow] = vpair[1];
+  constexpr int kTerms = __is_same(T, __bf16) && sizeof(YT) == 4 ? 3 : 2;
+  __shared__ __align__(16) T vterms[kTerms][TM][kRow];
   __shared__ float up[TM];
   // B's block of a request and the products' way out share the wave's rows
   constexpr bool kStaged = KB <= 2;
@@ -582,16 +584,19 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(AdapterArgs a) {
       for (int d = 1; d < kPer; d *= 2) m8 = fmaxf(m8, __shfl_xor(m8, d));
       e = m8 > 0.0f && m8 < __builtin_inff() ? __builtin_amdgcn_frexp_expf(m8) : 0;
     }
-    Vec8<T> hi, lo;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = ldexpf(f[j], -e);
-      hi.e[j] = (T)x;
-      const float h = (float)hi.e[j];
-      lo.e[j] = (T)(fabsf(h) < __builtin_inff() ? x - h : 0.0f);
+    for (int j = 0; j < 8; ++j) f[j] = ldexpf(f[j], -e);
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) {
+      Vec8<T> term;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        term.e[j] = (T)f[j];
+        const float h = (float)term.e[j];
+        f[j] = fabsf(h) < __builtin_inff() ? f[j] - h : 0.0f;
+      }
+      *(Vec8<T>*)&vterms[t][row][r0] = term;
     }
-    *(Vec8<T>*)&vhi[row][r0] = hi;
-    *(Vec8<T>*)&vlo[row][r0] = lo;
     if (r0 == 0) up[row] = ldexpf(1.0f, e);
   }
   __syncthreads();
@@ -694,13 +699,13 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(AdapterArgs a) {
         for (int nb = 0; nb < 4; ++nb) acc[nb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int kk = 0; kk < KB; ++kk) {
-          const V8 hi = *(const V8*)&vhi[mb * 16 + r16][kk * 32 + lg * 8];
-          const V8 lo = *(const V8*)&vlo[mb * 16 + r16][kk * 32 + lg * 8];
+          V8 v[kTerms];
 #pragma unroll
-          for (int nb = 0; nb < 4; ++nb) {
-            acc[nb] = mma(__builtin_bit_cast(V8, bf[p][nb][kk]), hi, acc[nb]);
-            acc[nb] = mma(__builtin_bit_cast(V8, bf[p][nb][kk]), lo, acc[nb]);
-          }
+          for (int t = 0; t < kTerms; ++t) v[t] = *(const V8*)&vterms[t][mb * 16 + r16][kk * 32 + lg * 8];
+#pragma unroll
+          for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t) acc[nb] = mma(__builtin_bit_cast(V8, bf[p][nb][kk]), v[t], acc[nb]);
         }
         const bool own = (rows >> r16) & 1u;
         const float s = up[mb * 16 + r16];

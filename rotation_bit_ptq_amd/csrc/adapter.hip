@@ -533,6 +533,9 @@ __global__ __launch_bounds__(256) void expand_singles_kernel(AdapterArgs a) {
 // numbers, a product each: fp16 (scaled by a power of two per row, which keeps
 // float32's range) as two, 22 bits; bf16 as three, all 24 bits, where y is
 // float32, and as two, 16 bits, where out is rounded to 8 or 11 bits anyway.
+// Split terms have no product with an infinite weight (one may be zero or of
+// the other sign), nor have the zeros past an adapter's rank, so products that
+// came out NaN are summed again in float32, outside the matrix cores.
 // (bf16 to float32, the third term: 16384 tokens, 4096 -> 4096, rank 64, 194 ->
 // 196 us; 8192 tokens, 2048 -> 4096, rank 128, 120 -> 124.)
 // The products of a tile's requests are kept in float32, each in its own
@@ -540,8 +543,10 @@ __global__ __launch_bounds__(256) void expand_singles_kernel(AdapterArgs a) {
 // which y is read and out written: neighbouring lanes on neighbouring
 // vectors of VW columns (in the products' own order neighbouring lanes would
 // be in 16 different rows, which takes the address unit four times longer).
+// (Two workgroups per compute unit where 256 registers hold all of it: the sum
+// in float32 would take a few more for 16-bit y in vectors of four.)
 template <class T, class YT, int MB, int KB, int VW, int P>
-__global__ __launch_bounds__(256) void expand_tiles_kernel(AdapterArgs a) {
+__global__ __launch_bounds__(256, sizeof(YT) == 2 && KB <= 2 ? 2 : 1) void expand_tiles_kernel(AdapterArgs a) {
   typedef typename Vec8Of<T>::V V8;
   constexpr int TM = 16 * MB, RP = 32 * KB;
   typedef Vector<YT, VW> Part;
@@ -582,7 +587,7 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(AdapterArgs a) {
       for (int j = 0; j < 8; ++j) m8 = fmaxf(m8, fabsf(f[j]));
 #pragma unroll
       for (int d = 1; d < kPer; d *= 2) m8 = fmaxf(m8, __shfl_xor(m8, d));
-      e = m8 > 0.0f && m8 < __builtin_inff() ? __builtin_amdgcn_frexp_expf(m8) : 0;
+      e = m8 > 0.0f && m8 < __builtin_inff() ? min(__builtin_amdgcn_frexp_expf(m8), 127) : 0;  // 2^127 is the last power
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = ldexpf(f[j], -e);
@@ -615,6 +620,25 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(AdapterArgs a) {
       for (int i = 0; i < kPasses; ++i) {
         const uint32_t m = min(m0 + mb * 16 + i * VW + prow, a.M - 1);
         y[i] = *(const Part*)((const YT*)a.y + (long long)m * a.ys + min(n0 + pcol, a.N - VW));
+      }
+    };
+    // the products of 16 rows lie in `turn`, some of them NaN
+    auto sum_again = [&](int mb) {
+      order();
+#pragma unroll 1
+      for (int row = 0; row < 16; ++row) {
+        const int id = __builtin_amdgcn_readlane(mine.id, mb * 16 + row), rank = __builtin_amdgcn_readlane(mine.rank, mb * 16 + row);
+        if (id < 0 || turn[row][lane] == turn[row][lane]) continue;
+        const T* const b = (const T*)a.B + ((long long)id * a.N + min(n0 + lane, a.N - 1)) * a.R;
+        float s = 0.0f;
+#pragma unroll 1
+        for (int r = 0; r < rank; ++r) {
+          float v = 0.0f;
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t) v += (float)vterms[t][mb * 16 + row][r];
+          s = fmaf((float)b[r], v * up[mb * 16 + row], s);
+        }
+        turn[row][lane] = s;
       }
     };
     auto finish = [&](int mb, const Part (&y)[kPasses]) {  // the products of 16 rows lie in `turn`
@@ -727,6 +751,9 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(AdapterArgs a) {
       order();
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) *(f32x4*)&turn[r16][nb * 16 + lg * 4] = f[mb][nb];
+      const f32x4 all = (f[mb][0] + f[mb][1]) + (f[mb][2] + f[mb][3]);
+      const float one = (all[0] + all[1]) + (all[2] + all[3]);
+      if (__any(one != one)) sum_again(mb);  // a NaN, or infinities of both signs
       finish(mb, yv[mb]);
     }
   }

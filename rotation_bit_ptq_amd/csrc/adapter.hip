@@ -892,7 +892,7 @@ extern "C" orbit_status orbit_adapter_add(const orbit_adapter_args* p, hipStream
   if (p->M == 0 || p->N == 0) return ORBIT_OK;
   const int64_t yb = dtype_bytes(p->y_dtype);
   if (!p->x || !p->y || !p->out || !p->ids || !aligned_to(p->ids, 4)) return ORBIT_E_ARG;
-  if (!vector_rows(p->x, p->x_stride) || !aligned_to(p->y, yb) || !aligned_to(p->out, yb)) return ORBIT_E_ARG;
+  if (!vector_rows(p->x, p->M > 1 ? p->x_stride : 0) || !aligned_to(p->y, yb) || !aligned_to(p->out, yb)) return ORBIT_E_ARG;
   if (p->adapters > 0 && (!p->A || !p->B || !aligned_to(p->A, 16) || !aligned_to(p->B, 16))) return ORBIT_E_ARG;
   if ((p->ranks && !aligned_to(p->ranks, 4)) || (p->scale && !aligned_to(p->scale, 4))) return ORBIT_E_ARG;
   if (p->M > 1 && p->out_stride < p->N) return ORBIT_E_SHAPE;  // output rows that overlap would race
@@ -909,9 +909,9 @@ extern "C" orbit_status orbit_adapter_add(const orbit_adapter_args* p, hipStream
   a.ranks = p->ranks;
   a.scale = p->scale;
   a.v = (float*)p->workspace;
-  a.xs = p->x_stride;
-  a.ys = p->y_stride;
-  a.os = p->out_stride;
+  a.xs = p->M > 1 ? p->x_stride : 0;  // one row's stride says nothing
+  a.ys = p->M > 1 ? p->y_stride : 0;
+  a.os = p->M > 1 ? p->out_stride : 0;
   a.M = (uint32_t)p->M;
   a.adapters = (uint32_t)p->adapters;
   a.K = (int)p->K;

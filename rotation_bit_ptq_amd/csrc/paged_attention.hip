@@ -72,7 +72,9 @@ extern "C" orbit_status orbit_paged_attention(const orbit_paged_attention_args* 
   if (p->q_batch_stride < 0 || p->q_head_stride < 0 || p->table_stride < 0) return ORBIT_E_SHAPE;
   if (p->batch == 0) return ORBIT_OK;
   if (!p->q || !p->out || !p->lengths || !aligned_to(p->out, 16) || !aligned_to(p->lengths, 4)) return ORBIT_E_ARG;
-  if (!vector_rows(p->q, p->q_batch_stride) || p->q_head_stride % 8) return ORBIT_E_ARG;
+  // the stride of one request or head says nothing
+  const int64_t qbs = p->batch > 1 ? p->q_batch_stride : 0, qhs = p->q_heads > 1 ? p->q_head_stride : 0;
+  if (!vector_rows(p->q, qbs) || qhs % 8) return ORBIT_E_ARG;
   if (p->table_width > 0 && (!p->block_table || !aligned_to(p->block_table, 4))) return ORBIT_E_ARG;
   if (p->lse && !aligned_to(p->lse, 4)) return ORBIT_E_ARG;
   const Split s = split_of(p->batch, p->q_heads, c.kv_heads, c.head_dim, c.format, p->table_width * c.page_size, p->window);
@@ -86,8 +88,8 @@ extern "C" orbit_status orbit_paged_attention(const orbit_paged_attention_args* 
   a.table = p->block_table;
   a.lengths = p->lengths;
   a.part = (float*)p->workspace;
-  a.qbs = p->q_batch_stride;
-  a.qhs = p->q_head_stride;
+  a.qbs = qbs;
+  a.qhs = qhs;
   a.table_stride = p->table_stride;
   a.part_ml = p->batch * p->q_heads * s.chunks * (int64_t)c.head_dim;
   a.q_heads = (int)p->q_heads;

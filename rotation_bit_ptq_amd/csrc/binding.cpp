@@ -19,7 +19,7 @@ namespace {
 PyObject* g_error = nullptr;       // rotation_bit_ptq_amd.OrbitError
 PyObject* g_raw_stream = nullptr;  // the current stream of a GPU, as an integer
 
-// A refusal: the message becomes an OrbitError.
+// A refusal: Python's error is set, by refuse() an OrbitError.
 struct Refused {};
 
 template <class... A>
@@ -85,6 +85,11 @@ int64_t integer(PyObject* o) {
   const int64_t v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw Refused();
   return v;
+}
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused();  // the object's own error
+  return v != 0;
 }
 
 at::Tensor fresh(const at::Tensor& like, at::IntArrayRef shape, at::ScalarType type) {
@@ -318,8 +323,8 @@ PyObject* kv_append(PyObject* const* v) {
     a.table_len = table.size(0);
     a.rot_dim = (int32_t)table.size(1);
   }
-  a.interleaved = PyObject_IsTrue(v[7]);
-  a.hadamard = PyObject_IsTrue(v[12]);
+  a.interleaved = truth(v[7]);
+  a.hadamard = truth(v[12]);
   at::Tensor q_out;
   if (v[8] != Py_None) {
     const at::Tensor& q = tensor(v[8], "q", 3);
@@ -392,7 +397,7 @@ PyObject* paged_attention(PyObject* const* v) {
     dense(out, "out");
   }
   a.out = out.data_ptr();
-  const bool with_lse = PyObject_IsTrue(v[10]) != 0;
+  const bool with_lse = truth(v[10]);
   if (with_lse) {
     lse = fresh(q, {B, H}, at::kFloat);
     a.lse = (float*)lse.data_ptr();

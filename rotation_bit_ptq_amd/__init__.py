@@ -6,7 +6,8 @@ the layers.  This module only marshals arguments: every step runs in the
 library's HIP kernels on the caller's current torch stream.  Device buffers
 are torch tensors; there is no CPU path, and importing fails if the library
 has not been built (``__graft_entry__.build()`` or
-``python rotation_bit_ptq_amd/build.py``).
+``python rotation_bit_ptq_amd/build.py``).  The native module is built for one
+torch: where it cannot be loaded the layer works, and the operators raise.
 
 Method (OrbitQuant paper page, Method): a randomized permuted block-Hadamard
 rotation Pi = blkdiag(H_h D_i) P_pi is absorbed offline into the weights
@@ -328,12 +329,23 @@ def int4_linear(xrot: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, group:
 # strided rows or heads: only the innermost dimension has to be contiguous.
 # Work runs on the current stream of the GPU that the first tensor is on.
 
+class _NotBuilt:
+    """Stands for a binding that cannot be loaded: the layer above works
+    without it, the functions below say what is missing."""
+
+    def __init__(self, cause):
+        self._cause = cause
+
+    def __getattr__(self, name):
+        raise ImportError(f"the native binding cannot be loaded ({self._cause}): it is not built, or built "
+                          "for another torch; run __graft_entry__.build()")
+
+
 def _load_binding():
     try:
         from . import _binding
     except ImportError as e:
-        raise ImportError("the native binding is not built (or older than torch); run "
-                          "__graft_entry__.build()") from e
+        return _NotBuilt(e)
     _binding.start(OrbitError, torch._C._cuda_getCurrentRawStream)
     return _binding
 

@@ -29,10 +29,15 @@ struct AdapterArgs {
 };
 
 constexpr int kWaves = 4;
-// Adapters of a tile, past which its rows go one by one.  Tiles of 16 rows,
-// 1003 tokens, 3072 -> 12288, rank 32, the whole call: six adapters a tile
-// 58 us as a tile and 79 by rows, eight 64 and 73, sixteen 75 by rows.
-constexpr int kRequestsAtMost = 8;
+// Adapters of a tile, past which its rows go one by one.  The whole call:
+//   16 rows (1003 tokens, 3072 -> 12288, rank 32): six adapters a tile 58 us as
+//     a tile and 79 by rows, eight 64 and 73, sixteen 75 by rows;
+//   64 rows (4096 tokens, 4096 -> 4096, rank 64): nine 107 as a tile and 277 by
+//     rows, 24 193 and 282, 48 304 and 290; 16384 tokens: 24 640 and 1231, 64
+//     1312 and 1356; rank 16, 4096 tokens: 16 97 and 121, 32 139 and 123;
+//     nearly the first product alone (1100 tokens, 4096 -> 64): rank 64, 24 87
+//     and 148; rank 16, 16 42 and 47, 24 54 and 46.
+constexpr int requests_at_most(int rows) { return rows == 64 ? 24 : 8; }
 constexpr int kFewTokens = 256, kSomeTokens = 1024;  // see cut_of
 
 // The adapter's rank, 0 where there is none.
@@ -222,11 +227,12 @@ __device__ __forceinline__ Request request_of(const AdapterArgs& a, int id) {
   return q;
 }
 
-// Whether a tile, a row per lane, has more than kRequestsAtMost adapters.
+// Whether a tile of TM rows, one per lane, has more adapters than it takes.
+template <int TM>
 __device__ __forceinline__ bool many_requests(int id) {
   unsigned long long rest = __ballot(id >= 0);
   for (int n = 0; rest != 0; ++n) {
-    if (n == kRequestsAtMost) return true;
+    if (n == requests_at_most(TM)) return true;
     rest &= ~__ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctzll(rest)));
   }
   return false;
@@ -302,7 +308,7 @@ __global__ __launch_bounds__(256, RB <= 4 ? 4 : 3) void shrink_staged_kernel(Ada
   const int tplace = ((threadIdx.x & 15) ^ trow) * 8;  // and in LDS
   const uint32_t m0 = blockIdx.x * TM;
   const int id = id_of<TM>(a, m0, lane);
-  const bool many = many_requests(id);
+  const bool many = many_requests<TM>(id);
   if ((int)blockIdx.y < a.slices) {
     if (!many) return;
     const uint32_t rows = TM / a.slices, from = m0 + blockIdx.y * rows, to = min(from + rows, a.M);
@@ -441,7 +447,7 @@ struct alignas(VW * sizeof(YT)) Vector {
   YT e[VW];
 };
 
-// The same for tiles of more than kRequestsAtMost requests (single tokens):
+// The same for tiles of more than requests_at_most() requests (single tokens):
 // the tile's rows, 16 at a time, and 256 J columns, without matrix cores.
 // A row's block of B is read in the order of memory, KB * 4 KB at a time; a
 // lane's eight ranks are summed over the lanes of a row of B.
@@ -456,7 +462,7 @@ __global__ __launch_bounds__(256) void expand_singles_kernel(AdapterArgs a) {
   if (place.block >= a.blocks) return;
   const uint32_t m0 = place.tile * TM;
   const int id = id_of<TM>(a, m0, lane);
-  if (!many_requests(id)) return;  // expand_tiles_kernel's
+  if (!many_requests<TM>(id)) return;  // expand_tiles_kernel's
   const Request mine = request_of(a, id);
   float(*const turn)[68] = turns[wave];
   const int brow = lane / kLanes, bcol = lane % kLanes, brank = bcol * 8;
@@ -570,7 +576,7 @@ __global__ __launch_bounds__(256, sizeof(YT) == 2 && KB <= 2 ? 2 : 1) void expan
   if (place.block >= a.blocks) return;
   const uint32_t m0 = place.tile * TM;
   const int id = id_of<TM>(a, m0, lane);
-  if (many_requests(id)) return;  // expand_singles_kernel's
+  if (many_requests<TM>(id)) return;  // expand_singles_kernel's
   const Request mine = request_of(a, id);
 
   // v of the tile: the parts of K summed, the adapter's scale applied, split

@@ -417,7 +417,8 @@ typedef struct {
  *   position rotation of the first rot_dim coordinates, pairs (a, b) =
  *   (x[i], x[i + rot_dim/2]), or (x[2i], x[2i + 1]) where interleaved:
  *   a' = a cos - b sin, b' = a sin + b cos, with cos = cos_sin[p][i], sin =
- *   cos_sin[p][rot_dim/2 + i], p = positions[token]  (no table: no rotation);
+ *   cos_sin[p][rot_dim/2 + i], p = positions[token]  (no
+ *   table, or rot_dim 0: no rotation, and no positions are read);
  *   then, where hadamard is set, H_head_dim / sqrt(head_dim) (Sylvester
  *   order) on keys and queries: orthogonal, so q' . k' = q . k, while a
  *   key's outlier channels are spread before they are coded (OrbitQuant

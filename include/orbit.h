@@ -296,6 +296,43 @@ orbit_status orbit_int4_linear(const void *Xrot, orbit_dtype xrot_dtype, int64_t
                                int64_t N, const void *bias, orbit_dtype bias_dtype,
                                void *out, orbit_dtype out_dtype, hipStream_t stream);
 
+/* Rows in 8 bits with one float32 scale each, rotated on the way: the tokens
+ * and, offline, the weights of orbit_int8_qlinear (rotate, then quantize, as
+ * orbit_int8_pack_weights, with the whole row as the group):
+ *   x' = Pi x (x itself: rot NULL), s = max|x'| / 127,
+ *   q = round_half_even(x' * (127 / max|x'|)), in float32.
+ * A row of zeros gives s = 0 and codes 0; a row with an infinity or a NaN
+ * gives s = NaN and codes 0.  Because W x = (W Pi^T)(Pi x), tokens and
+ * weights coded with the same rotation multiply to the layer's product.
+ * X: device [M, K] by row stride (in elements), F32, BF16 or F16, any
+ * alignment of its type; q_out: device int8 [M, K] contiguous, 16-byte
+ * aligned; s_out: device float [M].  K a multiple of 16, 16 <= K <=
+ * ORBIT_MAX_D (and what rot asks for); 0 <= M < 2^22.
+ * Errors: ORBIT_E_ARG, ORBIT_E_SHAPE, ORBIT_E_DTYPE, ORBIT_E_HIP. */
+orbit_status orbit_int8_quant_rows(const orbit_rpbh *rot, const void *X, orbit_dtype x_dtype,
+                                   int64_t M, int64_t K, int64_t x_stride, int8_t *q_out,
+                                   float *s_out, hipStream_t stream);
+
+/* The product of 8-bit integers with a scale for each token and each channel:
+ *   out[m, n] = act(sx[m] * sw[n] * sum_k qx[m, k] qw[n, k] (+ bias[n])).
+ * The sums are exact (int32); sx * sw, the product with it, the bias and the
+ * activation are float32, rounded once to out's type.
+ * qx: device int8 [M, K], qw: device int8 [N, K], contiguous, 16-byte
+ * aligned, any values; sx: device float [M], sw: device float [N]; bias:
+ * optional device [N], F32, BF16 or F16; out: device [M, N] contiguous, F32,
+ * BF16 or F16.  K a multiple of 16, 16 <= K <= 65536; 0 <= M, N < 2^22.
+ * Errors: ORBIT_E_ARG, ORBIT_E_SHAPE, ORBIT_E_DTYPE, ORBIT_E_HIP. */
+typedef struct {
+  const int8_t *qx, *qw;
+  const float *sx, *sw;
+  const void *bias;
+  void *out;
+  int64_t M, N, K;
+  int32_t bias_dtype, out_dtype, act; /* orbit_dtype, orbit_dtype, orbit_act */
+} orbit_int8_qlinear_args;
+
+orbit_status orbit_int8_qlinear(const orbit_int8_qlinear_args *args, hipStream_t stream);
+
 /* ---- What stands between the quantized projections of a block ----------
  *
  * The operators a transformer block needs beside its linear layers when it

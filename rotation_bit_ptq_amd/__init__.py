@@ -34,7 +34,7 @@ import torch
 __all__ = [
     "OrbitError", "Codebook", "Rotation", "fit_codebook", "pack_weights",
     "quant_act", "qlinear", "rotate", "int8_pack_weights", "int8_linear",
-    "int4_pack_weights", "int4_linear",
+    "int4_pack_weights", "int4_linear", "int8_quant_rows", "int8_qlinear",
     "block_norm", "adapter_add", "kv_append", "kv_read", "paged_attention",
     "packed_row_bytes", "LIB_PATH",
 ]
@@ -97,6 +97,8 @@ def _load():
         "orbit_kv_read": ([P, P, I64, P, P, ctypes.c_int, P], ctypes.c_int),
         "orbit_paged_attention": ([P, P], ctypes.c_int),
         "orbit_paged_attention_workspace": ([I64] * 7 + [I32], I64),
+        "orbit_int8_quant_rows": ([P, P, ctypes.c_int, I64, I64, I64, P, P, P], ctypes.c_int),
+        "orbit_int8_qlinear": ([P, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         try:
@@ -322,7 +324,8 @@ def int4_linear(xrot: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, group:
     return out
 
 
-# ---- what stands between the quantized projections of a block ---------------
+# ---- what stands between the quantized projections of a block, and the int8
+# layer whose tokens are coded too ---------------------------------------------
 #
 # Called once per layer and decode step, so checks, allocation and the call
 # itself are native (csrc/binding.cpp).  Tensors of these functions may be
@@ -351,6 +354,43 @@ def _load_binding():
 
 
 _binding = _load_binding()
+
+
+def int8_quant_rows(rot, X: torch.Tensor):
+    """Rows in 8 bits with a scale each, rotated on the way (rot None: not):
+
+        x' = Pi x,  s = max|x'| / 127,  q = round(x' * (127 / max|x'|))
+
+    X: [M, K] float32, bfloat16 or float16, rows of any stride.  Returns
+    (q int8 [M, K], s float32 [M]): online the tokens of int8_qlinear, offline
+    its weights, a scale for each output channel (rotated alike, since W x =
+    (W Pi^T)(Pi x)).  A row of zeros has s = 0, one with an infinity or a NaN
+    s = NaN; their codes are 0.
+    """
+    if rot is None:
+        return _binding.int8_quant_rows(0, None, X)
+    if not isinstance(rot, Rotation):
+        raise OrbitError("rot must be a Rotation or None")
+    return _binding.int8_quant_rows(ctypes.addressof(rot.struct), rot.perm, X)
+
+
+def int8_qlinear(qx, sx, qw, sw, *, bias=None, out_dtype=None, out=None, act=None):
+    """out[m, n] = act(sx[m] * sw[n] * sum_k qx[m, k] qw[n, k] (+ bias[n])):
+    the product of 8-bit integers with a scale for each token and channel.
+
+    qx: int8 [M, K], sx: float32 [M], qw: int8 [N, K], sw: float32 [N]
+    (int8_quant_rows gives both pairs); K a multiple of 16; bias: [N] of any
+    floating type; act: None or "gelu".  out: [M, N] of out_dtype (bfloat16
+    by default, or out's).  The sums are exact; NaN scales (rows that could
+    not be coded) give NaN.
+    """
+    try:
+        act = ACTS[act]
+    except (KeyError, TypeError):
+        raise OrbitError(f"unknown activation {act!r}") from None
+    return _binding.int8_qlinear(qx, sx, qw, sw, bias, act, out_dtype, out)
+
+
 _NORMS = {None: 0, "rms": 1, "layer": 2}
 
 

@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <vector>
 
+#include "int8_rows.h"
 #include "orbit_internal.h"
 
 using orbit::hip_status;
@@ -351,6 +352,35 @@ orbit_status orbit_int4_pack_weights(const orbit_rpbh* rot, const void* W, orbit
                                      uint16_t* scale_f16_out, hipStream_t stream) {
   return group_pack(orbit::RowMode::kInt4Pack, rot, W, w_dtype, N, K, group, (int8_t*)q_out,
                     scale_f16_out, stream);
+}
+
+orbit_status orbit_int8_quant_rows(const orbit_rpbh* rot, const void* X, orbit_dtype x_dtype, int64_t M, int64_t K,
+                                   int64_t x_stride, int8_t* q_out, float* s_out, hipStream_t stream) {
+  if (rot) {
+    const orbit_status st = check_rot(rot, K);
+    if (st != ORBIT_OK) return st;
+  }
+  if (M < 0 || M >= ORBIT_MAX_ROWS || K < 16 || K > ORBIT_MAX_D || K % 16 || x_stride < 0) return ORBIT_E_SHAPE;
+  if (x_dtype != ORBIT_F32 && x_dtype != ORBIT_BF16 && x_dtype != ORBIT_F16) return ORBIT_E_DTYPE;
+  if (M == 0) return ORBIT_OK;
+  const int64_t eb = x_dtype == ORBIT_F32 ? 4 : 2;
+  if (!X || (uintptr_t)X % eb || !q_out || !aligned16(q_out) || !s_out || (uintptr_t)s_out % 4) return ORBIT_E_ARG;
+  orbit::Int8RowArgs a = {};
+  a.in = X;
+  a.q_out = q_out;
+  a.s_out = s_out;
+  a.rows = M;
+  a.stride = M > 1 ? x_stride : 0;  // the stride of one row says nothing
+  a.d = (int)K;
+  a.inv_sqrt_h = 1.0f;
+  a.vec = aligned16(X) && a.stride % 8 == 0;
+  if (rot) {
+    a.perm = rot->perm;
+    a.sign_bits = rot->sign_bits;
+    a.h = rot->h;
+    a.inv_sqrt_h = (float)(1.0 / std::sqrt((double)rot->h));
+  }
+  return hip_status(orbit::launch_int8_rows(a, x_dtype, rot != nullptr, stream));
 }
 
 orbit_status orbit_int4_linear(const void* Xrot, orbit_dtype xrot_dtype, int64_t M, int64_t K,

@@ -414,6 +414,62 @@ PyObject* paged_attention(PyObject* const* v) {
   return with_lse ? pair(out, lse) : wrap(out);
 }
 
+// rot (an orbit_rpbh's address, or 0), rot's perm (or None), X
+PyObject* int8_quant_rows(PyObject* const* v) {
+  const at::Tensor& x = tensor(v[2], "X", 2);
+  const int dev = x.get_device();
+  const int64_t M = x.size(0), K = x.size(1);
+  const int32_t type = dtype(x.scalar_type(), "X");
+  check(x, "X", dev, {M, K}, x.scalar_type());
+  const orbit_rpbh* const rot = (const orbit_rpbh*)PyLong_AsVoidPtr(v[0]);
+  if (PyErr_Occurred()) throw Refused();
+  if (rot) check(tensor(v[1], "rot", 1), "rot", dev, {rot->d}, at::kInt);
+  const at::Tensor q = fresh(x, {M, K}, at::kChar), s = fresh(x, {M}, at::kFloat);
+  launch("orbit_int8_quant_rows", dev, [&](hipStream_t st) {
+    return orbit_int8_quant_rows(rot, x.data_ptr(), (orbit_dtype)type, M, K, x.stride(0), (int8_t*)q.data_ptr(), (float*)s.data_ptr(), st);
+  });
+  return pair(q, s);
+}
+
+// qx, sx, qw, sw, bias, act, out_dtype, out
+PyObject* int8_qlinear(PyObject* const* v) {
+  const at::Tensor& qx = tensor(v[0], "qx", 2);
+  const int dev = qx.get_device();
+  const at::Tensor& qw = tensor(v[2], "qw", 2);
+  orbit_int8_qlinear_args a = {};
+  a.M = qx.size(0);
+  a.K = qx.size(1);
+  a.N = qw.size(0);
+  check(qx, "qx", dev, {a.M, a.K}, at::kChar);
+  check(qw, "qw", dev, {a.N, a.K}, at::kChar);
+  dense(qx, "qx");
+  dense(qw, "qw");
+  a.qx = (const int8_t*)qx.data_ptr();
+  a.qw = (const int8_t*)qw.data_ptr();
+  a.sx = (const float*)checked(v[1], "sx", dev, {a.M}, at::kFloat).data_ptr();
+  a.sw = (const float*)checked(v[3], "sw", dev, {a.N}, at::kFloat).data_ptr();
+  if (v[4] != Py_None) {
+    const at::Tensor& b = tensor(v[4], "bias", 1);
+    a.bias_dtype = dtype(b.scalar_type(), "bias");
+    check(b, "bias", dev, {a.N}, b.scalar_type());
+    a.bias = b.data_ptr();
+  }
+  a.act = (int32_t)integer(v[5]);
+  at::Tensor out;
+  if (v[7] == Py_None) {
+    out = fresh(qx, {a.M, a.N}, type_of(v[6], at::kBFloat16));
+  } else {
+    const at::Tensor& given = tensor(v[7], "out", 2);
+    check(given, "out", dev, {a.M, a.N}, type_of(v[6], given.scalar_type()));
+    dense(given, "out");
+    out = given;
+  }
+  a.out_dtype = dtype(out.scalar_type(), "out");
+  a.out = out.data_ptr();
+  launch("orbit_int8_qlinear", dev, [&](hipStream_t s) { return orbit_int8_qlinear(&a, s); });
+  return wrap(out);
+}
+
 // One entry: the number of arguments is checked, refusals and torch's own
 // exceptions (out of memory) become Python's.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
@@ -451,6 +507,8 @@ PyMethodDef g_methods[] = {
     ENTRY(kv_append, 13),
     ENTRY(kv_read, 6),
     ENTRY(paged_attention, 11),
+    ENTRY(int8_quant_rows, 3),
+    ENTRY(int8_qlinear, 8),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,235 @@
+// orbit_int8_quant_rows: rows to 8 bits with one float32 scale each, rotated
+// on the way:
+//   x' = Pi x (or x),  s = max|x'| / 127,  q = rint(x' * 127 / max|x'|).
+//
+// Bound: memory, one pass: a row stays in registers between the rotation,
+// its maximum and its codes.  The hot shapes (bf16, blocks of 128 or 256,
+// rows of 1024 .. 16384) run on the matrix cores (rpbh_m2_q.hip); this file
+// has the kernel for everything else: float32 and fp16 rows, other blocks,
+// odd lengths, and rows that are not rotated.
+//
+// A workgroup of up to four waves takes a row in rounds of 1024 coordinates:
+// lane l of a round's wave holds coordinates 16 l .. 16 l + 15, so that four
+// of the Hadamard's stages are in registers, six between lanes, and codes
+// leave as 16-byte words.  Blocks of 2048 and 4096 (rows of at most 4096)
+// take their last two stages between the waves, through LDS.  The gather
+// goes through an LDS copy of the row; its offsets (with the signs) are kept
+// in registers for all rows of a workgroup.
+//
+// Codes: t = fma(x', 127 / max, 1.5 * 2^23) holds the rounded integer in its
+// low byte (one rounding of the exact product, half to even; |x'| <= max, so
+// there is nothing to clamp).  A row with an infinity or a NaN takes s = NaN
+// and codes 0, so that all that is made of it is NaN.
+#include "block_common.h"
+#include "int8_rows.h"
+
+using namespace orbit;
+using namespace orbit::block;
+
+namespace {
+
+template <int M>
+__device__ __forceinline__ float lane_xor(float v) {
+  const int b = __builtin_bit_cast(int, v);
+  if constexpr (M == 1) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, kXor1, 0xf, 0xf, true));
+  if constexpr (M == 2) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, kXor2, 0xf, 0xf, true));
+  return __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(b, (M << 10) | 0x1f));
+}
+
+template <int M>
+__device__ __forceinline__ void butterfly(float (&f)[16], int lane) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float o = lane_xor<M>(f[j]);
+    f[j] = lane & M ? o - f[j] : f[j] + o;
+  }
+}
+__device__ __forceinline__ void butterfly32(float (&f)[16], int lane) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const unsigned u = __builtin_bit_cast(unsigned, f[j]);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const float lo = __builtin_bit_cast(float, (unsigned)r[0]), hi = __builtin_bit_cast(float, (unsigned)r[1]);
+    f[j] = lane & 32 ? lo - hi : lo + hi;
+  }
+}
+
+// NR: rounds of 1024 coordinates per wave; W waves (blockDim / 64) of them.
+template <class IT, bool ROT, int NR>
+__global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
+  extern __shared__ __align__(16) char smem[];
+  unsigned* const top = (unsigned*)(smem + a.lds_row);  // the waves' maxima, behind the row's copy
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, waves = (int)blockDim.x >> 6;
+  // where each coordinate comes from, bit 15: with its sign flipped
+  uint32_t from[ROT ? NR : 1][8];
+  if constexpr (ROT) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int k0 = (r * waves + wave) * 1024 + lane * 16;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) from[r][j] = 0;
+      if (k0 < a.d) {
+        const uint32_t sign = a.sign_bits[k0 >> 5] >> (k0 & 31);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          from[r][j >> 1] |= ((uint32_t)a.perm[k0 + j] | ((sign >> j) & 1u) << 15) << (16 * (j & 1));
+      }
+    }
+  }
+  const IT* const base = (const IT*)a.in;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const IT* const x = base + row * a.stride;
+    float f[NR][16];
+    if constexpr (ROT) {
+      IT* const copy = (IT*)smem;
+      if (a.vec) {
+        for (int i = t * 8; i < a.d; i += (int)blockDim.x * 8) *(Vec8<IT>*)(copy + i) = *(const Vec8<IT>*)(x + i);
+      } else {
+        for (int i = t; i < a.d; i += (int)blockDim.x) copy[i] = x[i];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t w = from[r][j >> 1] >> (16 * (j & 1));
+          const float v = (float)copy[w & 0x3fffu];
+          f[r][j] = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) ^ ((w & 0x8000u) << 16));
+        }
+    } else {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const int k0 = (r * waves + wave) * 1024 + lane * 16;
+        Vec8<IT> v[2];
+        if (k0 < a.d) {
+          if (a.vec) {
+            v[0] = *(const Vec8<IT>*)(x + k0);
+            v[1] = *(const Vec8<IT>*)(x + k0 + 8);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j >> 3].e[j & 7] = x[k0 + j];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[r][j] = k0 < a.d ? (float)v[j >> 3].e[j & 7] : 0.0f;
+      }
+    }
+    unsigned m = 0;  // bit patterns of |x'| order like the values, infinities and NaN last
+    if constexpr (ROT) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        // lanes past the row hold the first coordinate again, and whole blocks of it: cleared below
+#pragma unroll
+        for (int s = 1; s < 16; s *= 2)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (!(j & s)) {
+              const float p = f[r][j], q = f[r][j | s];
+              f[r][j] = p + q;
+              f[r][j | s] = p - q;
+            }
+        if (a.h > 16) butterfly<1>(f[r], lane);
+        if (a.h > 32) butterfly<2>(f[r], lane);
+        if (a.h > 64) butterfly<4>(f[r], lane);
+        if (a.h > 128) butterfly<8>(f[r], lane);
+        if (a.h > 256) butterfly<16>(f[r], lane);
+        if (a.h > 512) butterfly32(f[r], lane);
+      }
+      if constexpr (NR == 1) {
+        // rows of at most 4096: a round is a wave's, its block's others are the neighbouring waves'
+#pragma unroll 1
+        for (int s = 1; s * 1024 < a.h; s *= 2) {
+          float* const all = (float*)smem;  // [wave][j][lane], over the row's copy
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) all[(wave * 16 + j) * 64 + lane] = f[0][j];
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float o = all[((wave ^ s) * 16 + j) * 64 + lane];
+            f[0][j] = wave & s ? o - f[0][j] : f[0][j] + o;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const bool in = (r * waves + wave) * 1024 + lane * 16 < a.d;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const unsigned b = __builtin_bit_cast(unsigned, f[r][j]) & 0x7fffffffu;
+        m = in && b > m ? b : m;
+      }
+    }
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) {
+      const unsigned o = (unsigned)__shfl_xor((int)m, s);
+      m = o > m ? o : m;
+    }
+    if (waves > 1) {
+      if (lane == 0) top[wave] = m;
+      __syncthreads();  // and every lane has gathered: the copy may be overwritten
+      m = top[0];
+      for (int w = 1; w < waves; ++w) m = top[w] > m ? top[w] : m;
+    }
+    const Int8Scale s = int8_scale(m, a.inv_sqrt_h);
+    if (t == 0) a.s_out[row] = s.s;
+    if (s.pre != 1.0f) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[r][j] *= s.pre;
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int k0 = (r * waves + wave) * 1024 + lane * 16;
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = int8_codes(&f[r][4 * j], s);
+      if (k0 < a.d) *(u32x4*)(a.q_out + row * a.d + k0) = u32x4{w[0], w[1], w[2], w[3]};
+    }
+    if (ROT || waves > 1) __syncthreads();  // the row's copy and the maxima have been read
+  }
+}
+
+template <class IT, bool ROT>
+hipError_t launch(Int8RowArgs a, hipStream_t stream) {
+  const int rounds = (a.d + 1023) / 1024, waves = rounds < 4 ? rounds : 4, nr = (rounds + waves - 1) / waves;
+  int lds = 0;
+  if (ROT) {
+    lds = a.d * (int)sizeof(IT);
+    if (a.h > 1024 && lds < waves * 4096) lds = waves * 4096;
+  }
+  a.lds_row = lds;
+  lds += 16;
+  // about as many workgroups as are resident, so that the offsets are read
+  // once for many rows; unrotated rows have none to keep
+  const long long cap = ROT ? (long long)kUnits * (nr == 1 ? 24 / waves : 4) : a.rows;
+  const dim3 grid((unsigned)(a.rows < cap ? a.rows : cap)), block(64 * waves);
+  hipError_t e = hipSuccess;
+  auto go = [&](auto n) {
+    auto kern = rows_kernel<IT, ROT, decltype(n)::value>;
+    static LaunchCache cache;
+    e = prepare_launch(cache, (const void*)kern, 256, lds, nullptr);
+    if (e != hipSuccess) return;
+    kern<<<grid, block, lds, stream>>>(a);
+    e = hipGetLastError();
+  };
+  if (nr == 1) go(std::integral_constant<int, 1>{});
+  else if (nr == 2) go(std::integral_constant<int, 2>{});
+  else if (nr == 3) go(std::integral_constant<int, 3>{});
+  else go(std::integral_constant<int, 4>{});
+  return e;
+}
+
+}  // namespace
+
+namespace orbit {
+hipError_t launch_int8_rows(const Int8RowArgs& a, int dtype, bool rotated, hipStream_t stream) {
+  switch (dtype) {
+    case ORBIT_BF16: return rotated ? launch<__bf16, true>(a, stream) : launch<__bf16, false>(a, stream);
+    case ORBIT_F16: return rotated ? launch<_Float16, true>(a, stream) : launch<_Float16, false>(a, stream);
+    default: return rotated ? launch<float, true>(a, stream) : launch<float, false>(a, stream);
+  }
+}
+}  // namespace orbit

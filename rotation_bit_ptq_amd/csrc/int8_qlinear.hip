@@ -6,14 +6,16 @@
 //
 // Two kernels.
 // * tile_kernel, for products with enough tiles to fill the chip.  Bound: the
-//   matrix cores.
+//   matrix cores, and what a compute unit takes in (launch_product).  16384 x
+//   4096 -> 4096 260 us (2.1 POP/s, as the library's int8 product of 8192^3;
+//   that size here 2.3), 4096 x 3072 -> 3072 43 us.
 // * thin_kernel, for few tokens or few tiles.  Bound: the weights' bytes, or
-//   latency.
+//   what a compute unit takes in.  16 x 3072 -> 18432 15 us (3.8 TB/s).
 // Everywhere the weights are the matrix instruction's A operand (rows) and
 // the tokens its B operand (columns), so that a lane's results are
 // neighbouring channels of one token.
 //
-// K is a multiple of 16.  What lies past a row's end inside a 64-byte chunk is
+// K is a multiple of 16.  What lies past a row's end inside a chunk is
 // read at an address that is valid and multiplied as zero.
 #include "block_common.h"
 
@@ -45,9 +47,20 @@ __device__ __forceinline__ float bias_of(const ProductArgs& a, long long n) {
     default: return ((const float*)a.bias)[n];
   }
 }
-// GELU in its erf form.
+// GELU in its erf form, y / 2 (1 + erf(y / sqrt 2)), with 1 - erf(x) = (a1 t + ..
+// + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x >= 0, by Abramowitz & Stegun,
+// Handbook of Mathematical Functions, 7.1.26 (within 1.5e-7); below zero 1 + erf
+// is that small term itself.  333 x 2064 -> 8200 in float32: 27 us with erff.
 __device__ __forceinline__ float activate(float y, int act) {
-  return act == ORBIT_ACT_GELU ? 0.5f * y * (1.0f + erff(y * 0.70710678118f)) : y;
+  if (act != ORBIT_ACT_GELU) return y;
+  const float x = fabsf(y) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f) * t;
+  const float rest = p * __builtin_amdgcn_exp2f(-(x * x) * 1.4426950408889634f);
+  return 0.5f * y * (y < 0.0f ? rest : 2.0f - rest);
 }
 template <class OT>
 __device__ __forceinline__ void store8(OT* p, const float (&f)[8]) {
@@ -93,96 +106,335 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const int* sums, in
   }
 }
 
-// ---- few tokens, few tiles ---------------------------------------------------
+// The loads that go from memory straight to LDS are inline assembly with
+// explicit waits: they have no register results, and the compiler would wait
+// for every one of them before each LDS read.
+__device__ __forceinline__ void load_lds(uint32_t to, uint32_t offset, const char* base) {  // 1 KB: lane l's 16 bytes to `to` + 16 l
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // until at most N loads of this wave are in flight, and no LDS read
+  static_assert(N >= 0 && N < 64);
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+}
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+
+// ---- few tokens ---------------------------------------------------------------
 //
-// A workgroup of eight waves takes 16 RB channels and up to 16 MB tokens;
-// the waves take the 128-byte chunks w, w + 8, ... of K, two in flight ahead
-// of the one that is multiplied, and add their sums in LDS (integers: the
-// order does not matter).
-template <class OT, int RB, int MB>
+// A workgroup of eight waves takes 16 RB channels and up to 16 MB tokens
+// (v_mfma_i32_16x16x64_i8); wave w the 128-byte chunks w, w + 8, ... of K,
+// through an LDS ring of its own, so that no barrier stands between two
+// chunks and 100 KB or more are in flight in a compute unit.  The waves' sums
+// are added in LDS (integers: the order does not matter).
+// A chunk is blocks of 8 rows, one load instruction each (whole lines: blocks
+// of 16 rows of 64 bytes were 5 to 10 % slower); 16-byte unit u of row r lies
+// at 128 r + 16 (u ^ (r / 2) % 8), which puts the 16 rows that LDS serves at
+// once in 16 different places of 256 bytes.
+template <class OT, int MB, int RB, int S>
 __global__ __launch_bounds__(512) void thin_kernel(ProductArgs a) {
-  constexpr int kPitch = 16 * RB + 4;
-  __shared__ __align__(16) int sums[16 * MB * kPitch];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int r16 = lane & 15, kq = (lane >> 4) * 16;
+  constexpr int kPitch = 16 * RB + 4, kChunk = (MB + RB) * 2048, kLoads = 2 * (MB + RB);
+  extern __shared__ __align__(16) char smem[];
+  int* const sums = (int*)smem;
+  static_assert(16 * MB * kPitch * 4 <= 8 * S * kChunk, "the sums lie over the rings");
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
   const long long n0 = (long long)blockIdx.x * (16 * RB), m0 = (long long)blockIdx.y * (16 * MB);
-  const char *wrow[RB], *xrow[MB];
+  const char *const wbase = a.w + n0 * a.K, *const xbase = a.x + m0 * a.K;
+  // this lane's sources: row lane / 4 of each block (past the end: the last
+  // row again, whose results are dropped)
+  const uint32_t unit = ((uint32_t)lane & 7u) ^ ((uint32_t)lane >> 4);
+  uint32_t from[kLoads];
 #pragma unroll
-  for (int i = 0; i < RB; ++i) wrow[i] = a.w + min(n0 + 16 * i + r16, a.N - 1) * a.K;
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = (i < 2 * RB ? i : i - 2 * RB) * 8 + (lane >> 3);
+    from[i] = (uint32_t)min((long long)r, (i < 2 * RB ? a.N - n0 : a.M - m0) - 1) * (uint32_t)a.K + (unit ^ (i & 1 ? 4u : 0u)) * 16u;
+  }
+  const int chunks = (a.K + 127) / 128, mine = (chunks - wave + 7) / 8;  // 0 where K is short
+  // bytes past the row's end: the row's last 16 again (multiplied as zero)
+  auto back = [&](int b) { return (uint32_t)max(0, (chunks - 1) * 128 + (int)((unit ^ (b & 1 ? 4u : 0u)) * 16u) - (a.K - 16)); };
+  const uint32_t ring = (uint32_t)wave * (S * kChunk);
+  auto issue = [&](int i) {
+    const int c = wave + 8 * i;
+    const uint32_t at = (uint32_t)c * 128u, st = ring + (uint32_t)(i % S) * kChunk;
 #pragma unroll
-  for (int i = 0; i < MB; ++i) xrow[i] = a.x + min(m0 + 16 * i + r16, a.M - 1) * a.K;
-  for (int i = t; i < 16 * MB * kPitch; i += 512) sums[i] = 0;
+    for (int b = 0; b < kLoads; ++b) load_lds(st + b * 1024u, from[b] + at - (c == chunks - 1 ? back(b) : 0u), b < 2 * RB ? wbase : xbase);
+  };
   i32x4 acc[RB][MB];
 #pragma unroll
   for (int i = 0; i < RB; ++i)
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-
-  constexpr int kAhead = 2;
-  i32x4 wv[kAhead][2][RB], xv[kAhead][2][MB];
-  auto load = [&](int slot, int c) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int k = c * 128 + s * 64 + kq, at = min(k, a.K - 16);
+  for (int i = 0; i < S; ++i)
+    if (i < mine) issue(i);
+  const uint32_t at = ring + (uint32_t)r16 * 128u, key = (uint32_t)r16 >> 1;
+  for (int i = 0; i < mine; ++i) {
+    if (mine - 1 - i >= S - 1) wait_loads<(S - 1) * kLoads>();
+    else wait_loads<0>();  // the last few
+    const char* const st = smem + at + (uint32_t)(i % S) * kChunk;
+    i32x4 wv[2][RB], xv[2][MB];
 #pragma unroll
-      for (int i = 0; i < RB; ++i) wv[slot][s][i] = *(const i32x4*)(wrow[i] + at);
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t u = ((uint32_t)(4 * h + g) ^ key) << 4;
 #pragma unroll
-      for (int i = 0; i < MB; ++i) xv[slot][s][i] = *(const i32x4*)(xrow[i] + at);
+      for (int b = 0; b < RB; ++b) wv[h][b] = *(const i32x4*)(st + u + b * 2048);
+#pragma unroll
+      for (int b = 0; b < MB; ++b) xv[h][b] = *(const i32x4*)(st + u + (RB + b) * 2048);
     }
-  };
-  auto compute = [&](int slot, int c) {
+    const int c = wave + 8 * i;
+    if (c * 128 + 128 > a.K) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (c * 128 + s * 64 + 64 > a.K) {
-        const bool in = c * 128 + s * 64 + kq < a.K;
+      for (int h = 0; h < 2; ++h) {
+        const bool in = c * 128 + h * 64 + g * 16 < a.K;
 #pragma unroll
-        for (int i = 0; i < RB; ++i) wv[slot][s][i] = in ? wv[slot][s][i] : i32x4{0, 0, 0, 0};
+        for (int b = 0; b < RB; ++b) wv[h][b] = in ? wv[h][b] : i32x4{0, 0, 0, 0};
       }
-#pragma unroll
-      for (int i = 0; i < RB; ++i)
-#pragma unroll
-        for (int j = 0; j < MB; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[slot][s][i], xv[slot][s][j], acc[i][j], 0, 0, 0);
     }
-  };
-  const int chunks = (a.K + 127) / 128;
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // this stage has been read
+    asm volatile("" ::: "memory");
+    if (i + S < mine) issue(i + S);
 #pragma unroll
-  for (int p = 0; p < kAhead; ++p) load(p, wave + 8 * p);
-  for (int c = wave; c < chunks; c += 8 * kAhead) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int p = 0; p < kAhead; ++p) {
-      compute(p, c + 8 * p);  // a chunk past the end is all zeros
-      load(p, c + 8 * (p + kAhead));
-    }
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int m = 0; m < MB; ++m) acc[b][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[h][b], xv[h][m], acc[b][m], 0, 0, 0);
   }
+  __syncthreads();
+  for (int i = t; i < 16 * MB * kPitch; i += 512) sums[i] = 0;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < RB; ++i)
 #pragma unroll
     for (int j = 0; j < MB; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        atomicAdd(&sums[(16 * j + r16) * kPitch + 16 * i + (lane >> 4) * 4 + q], acc[i][j][q]);
+      for (int q = 0; q < 4; ++q) atomicAdd(&sums[(16 * j + r16) * kPitch + 16 * i + g * 4 + q], acc[i][j][q]);
   __syncthreads();
   finish<OT>(a, sums, kPitch, 16 * MB, 16 * RB, m0, n0, t, 512);
 }
 
-template <class OT>
-hipError_t launch_thin(const ProductArgs& a, hipStream_t stream) {
-  const int mb = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
-  const int64_t gm = (a.M + 16 * mb - 1) / (16 * mb);
-  const bool wide = (a.N + 31) / 32 * gm >= kUnits;  // 32 channels a workgroup: half the token reads
-  const dim3 grid((unsigned)((a.N + (wide ? 31 : 15)) / (wide ? 32 : 16)), (unsigned)gm), block(512);
-  if (wide) {
-    if (mb == 1) thin_kernel<OT, 2, 1><<<grid, block, 0, stream>>>(a);
-    else if (mb == 2) thin_kernel<OT, 2, 2><<<grid, block, 0, stream>>>(a);
-    else thin_kernel<OT, 2, 4><<<grid, block, 0, stream>>>(a);
-  } else {
-    if (mb == 1) thin_kernel<OT, 1, 1><<<grid, block, 0, stream>>>(a);
-    else if (mb == 2) thin_kernel<OT, 1, 2><<<grid, block, 0, stream>>>(a);
-    else thin_kernel<OT, 1, 4><<<grid, block, 0, stream>>>(a);
-  }
+template <class OT, int MB, int RB, int S>
+hipError_t launch_thin(ProductArgs a, hipStream_t stream) {
+  constexpr int kLds = 8 * S * (MB + RB) * 2048;
+  auto kern = thin_kernel<OT, MB, RB, S>;
+  static LaunchCache cache;
+  const hipError_t e = prepare_launch(cache, (const void*)kern, 512, kLds, nullptr);
+  if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)((a.N + 16 * RB - 1) / (16 * RB)), (unsigned)((a.M + 16 * MB - 1) / (16 * MB)));
+  kern<<<grid, dim3(512), kLds, stream>>>(a);
   return hipGetLastError();
+}
+
+// ---- many tiles ---------------------------------------------------------------
+//
+// A workgroup of WGM x WGN waves takes TM tokens x TN channels, a wave BM x BN
+// blocks of 32 x 32 (v_mfma_i32_32x32x32_i8: lane l holds row or column l % 32
+// and 16 bytes of k, the instruction's slots 16 (l / 32) ..).
+// Chunks of 128 bytes of K of both operands pass through a ring of S LDS
+// stages: while a chunk is multiplied, S - 1 are in flight.  Chunks of 64
+// bytes in rings of twice the stages took 281 us for 260 (16384 x 4096 ->
+// 4096).  A stage is laid out as the thin kernel's chunk.  A lane reads unit
+// 2 s + l / 32 in step s (of four): both operands alike, so the order of k
+// does not matter.
+template <class OT, int WGM, int WGN, int BM, int BN, int S>
+__global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs a) {
+  constexpr int kWaves = WGM * WGN, TM = 32 * WGM * BM, TN = 32 * WGN * BN;
+  constexpr int kStage = (TM + TN) * 128, kBlocks = (TM + TN) / 8;
+  constexpr int kLoads = (kBlocks + kWaves - 1) / kWaves, kRest = kBlocks % kWaves;  // waves below kRest load one more
+  constexpr int kPitch = 32 * BN + 4;
+  static_assert(kWaves * 32 * kPitch * 4 <= S * kStage, "the results pass through the ring's memory");
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WGN, wn = wave - wm * WGN;
+
+  // Each XCD (workgroups go round them) takes a row of neighbouring tiles, in
+  // groups of 8 token tiles, so that what runs at once shares its operands in
+  // the XCD's L2.
+  const int tiles = a.tiles_m * a.tiles_n, each = (tiles + 7) / 8;
+  const int tile = ((int)blockIdx.x & 7) * each + ((int)blockIdx.x >> 3);
+  if (((int)blockIdx.x >> 3) >= each || tile >= tiles) return;
+  const int group = tile / (8 * a.tiles_n), in_group = tile - group * 8 * a.tiles_n;
+  const int height = min(8, a.tiles_m - group * 8);
+  const int tn = in_group / height, tm = group * 8 + in_group - tn * height;
+  const long long m0 = (long long)tm * TM, n0 = (long long)tn * TN;
+
+  // this lane's sources (rows past the end: the last one again, whose results are dropped)
+  const char* const xbase = a.x + m0 * a.K;
+  const char* const wbase = a.w + n0 * a.K;
+  const int last = (a.K + 127) / 128 - 1;
+  // key of row r: (r / 2) % 8; a block's rows begin at a multiple of 8
+  const uint32_t unit = ((uint32_t)lane & 7u) ^ ((uint32_t)lane >> 4);
+  uint32_t from[kLoads];
+  #pragma unroll
+  for (int q = 0; q < kLoads; ++q) {
+    const int blk = q * kWaves + wave, r = blk * 8 + (lane >> 3);
+    const long long row = blk < TM / 8 ? min((long long)r, a.M - 1 - m0) : min((long long)r - TM, a.N - 1 - n0);
+    from[q] = (uint32_t)row * (uint32_t)a.K + (unit ^ (blk & 1 ? 4u : 0u)) * 16u;
+  }
+  // bytes past the row's end in the last chunk: the row's last 16 again (multiplied as zero, below)
+  auto back = [&](int blk) { return (uint32_t)max(0, last * 128 + (int)((unit ^ (blk & 1 ? 4u : 0u)) * 16u) - (a.K - 16)); };
+  auto issue = [&](int c) {
+    const uint32_t st = (uint32_t)(c % S) * kStage;
+    const uint32_t at = (uint32_t)c * 128u;
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const int blk = q * kWaves + wave;
+      if (kRest && q == kLoads - 1 && blk >= kBlocks) break;
+      load_lds(st + (uint32_t)blk * 1024u, from[q] + at - (c == last ? back(blk) : 0u), blk < TM / 8 ? xbase : wbase);
+    }
+  };
+  // chunk c has landed, for this wave's loads: `later` chunks may be in flight
+  auto landed = [&](int later) {
+    const bool more = kRest == 0 || wave < kRest;
+    constexpr int kLess = kRest ? kLoads - 1 : kLoads;
+    auto wait = [&](auto n) { more ? wait_loads<decltype(n)::value * kLoads>() : wait_loads<decltype(n)::value * kLess>(); };
+    if (later >= S - 1) wait(std::integral_constant<int, S - 1>{});
+    else if (later == S - 2) wait(std::integral_constant<int, S - 2>{});
+    else if (later >= 1) wait(std::integral_constant<int, 1>{});
+    else wait_loads<0>();
+  };
+  // where K ends inside the last chunk, its weights' other bytes become zeros
+  auto arrived = [&](int c) {
+    if (c == last && (a.K & 127)) {
+      char* const st = smem + (c % S) * kStage + TM * 128;
+      for (int i = threadIdx.x; i < TN * 8; i += 64 * kWaves) {
+        const int r = i >> 3, u = (i & 7) ^ ((r >> 1) & 7);
+        if (c * 128 + u * 16 >= a.K) *(i32x4*)(st + i * 16) = i32x4{0, 0, 0, 0};
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+      meet();
+    }
+  };
+
+  const int r32 = lane & 31, half = lane >> 5;
+  const uint32_t key = ((uint32_t)r32 >> 1) & 7u;
+  const uint32_t rx = (uint32_t)(wm * BM * 32 + r32) * 128u, rw = (uint32_t)(TM + wn * BN * 32 + r32) * 128u;
+  i32x4 xv[2][BM], wv[2][BN];
+  auto read = [&](int set, int c, int step) {
+    const char* const st = smem + (c % S) * kStage + (((uint32_t)(2 * step + half) ^ key) << 4);
+#pragma unroll
+    for (int j = 0; j < BN; ++j) wv[set][j] = *(const i32x4*)(st + rw + j * 4096);
+#pragma unroll
+    for (int i = 0; i < BM; ++i) xv[set][i] = *(const i32x4*)(st + rx + i * 4096);
+  };
+  i32x16 acc[BN][BM];
+#pragma unroll
+  for (int j = 0; j < BN; ++j)
+#pragma unroll
+    for (int i = 0; i < BM; ++i)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[j][i][q] = 0;
+  auto mma = [&](int set) {
+#pragma unroll
+    for (int j = 0; j < BN; ++j)
+#pragma unroll
+      for (int i = 0; i < BM; ++i) acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[set][j], xv[set][i], acc[j][i], 0, 0, 0);
+  };
+  // the next step's reads go out between this one's products
+  auto interleave = [&] {
+#pragma unroll
+    for (int q = 0; q < BM * BN; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+#pragma unroll
+  for (int c = 0; c < S; ++c)
+    if (c <= last) issue(c);
+  landed(min(last, S - 1));
+  meet();
+  arrived(0);
+  read(0, 0, 0);
+  for (int c = 0; c <= last; ++c) {
+#pragma unroll
+    for (int step = 0; step < 3; ++step) {
+      read((step + 1) & 1, c, step + 1);
+      mma(step & 1);
+      interleave();
+    }
+    // chunk c + 1 is there, and nobody reads chunk c any more
+    landed(min(last - c - 1, S - 2));
+    meet();
+    if (c + S <= last) issue(c + S);
+    arrived(c + 1);
+    read(0, c + 1, 0);  // behind the last chunk: memory of the ring, not used
+    mma(1);
+    interleave();
+  }
+  __syncthreads();
+
+  int* const mine = (int*)smem + wave * 32 * kPitch;
+#pragma unroll
+  for (int i = 0; i < BM; ++i) {
+#pragma unroll
+    for (int j = 0; j < BN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(i32x4*)(mine + r32 * kPitch + 32 * j + 8 * q + 4 * half) =
+            i32x4{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+    // the wave's own rows: LDS serves a wave in order
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    finish<OT>(a, mine, kPitch, 32, 32 * BN, m0 + (wm * BM + i) * 32, n0 + wn * BN * 32, lane, 64);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <class OT, int WGM, int WGN, int BM, int BN, int S>
+hipError_t launch_tiles(ProductArgs a, hipStream_t stream) {
+  constexpr int TM = 32 * WGM * BM, TN = 32 * WGN * BN, kLds = S * (TM + TN) * 128;
+  a.tiles_m = (int)((a.M + TM - 1) / TM);
+  a.tiles_n = (int)((a.N + TN - 1) / TN);
+  auto kern = tile_kernel<OT, WGM, WGN, BM, BN, S>;
+  static LaunchCache cache;
+  const hipError_t e = prepare_launch(cache, (const void*)kern, 64 * WGM * WGN, kLds, nullptr);
+  if (e != hipSuccess) return e;
+  const long long each = ((long long)a.tiles_m * a.tiles_n + 7) / 8;
+  kern<<<dim3((unsigned)(8 * each)), dim3(64 * WGM * WGN), kLds, stream>>>(a);
+  return hipGetLastError();
+}
+
+// The variant that the sizes give the least time by this estimate: a compute
+// unit takes ceil(workgroups / units) workgroups, each as long as its
+// (TM + TN) K operand bytes at 50 KB/us (what a unit was seen to take in, from
+// one workgroup on the whole chip to several on each unit) or its 2 TM TN K
+// operations at 9 per ps (the chip's settled 2.3 POP/s, shared), whichever is
+// longer.  Measured, us (thin tile of 64 x 64, 128 x 128, 256 x 192, 256 x 256):
+// 256 x 4096 -> 4096 11.3, 20, 39, 48; 1024 x 4096 -> 4096 42, 27, 41, 50;
+// 4096 x 3072 -> 3072 (-), 50, 43, 45; 16384 x 4096 -> 4096 (-), 297, 299,
+// 260; 64 x 4096 -> 4096 with thin tiles of 16 x 32, 32 x 32, 64 x 32, 64 x 64:
+// 9.7, 7.4, 8.1, 10.4.
+template <class OT>
+hipError_t launch_product(const ProductArgs& a, hipStream_t stream) {
+  typedef hipError_t (*Launch)(ProductArgs, hipStream_t);
+  static const struct {
+    int tm, tn;
+    Launch launch;
+  } kVariants[] = {
+      {16, 16, launch_thin<OT, 1, 1, 4>}, {16, 32, launch_thin<OT, 1, 2, 3>},  {32, 32, launch_thin<OT, 2, 2, 2>},
+      {64, 32, launch_thin<OT, 4, 2, 1>}, {64, 64, launch_thin<OT, 4, 4, 1>},  {128, 128, launch_tiles<OT, 2, 2, 2, 2, 2>},
+      {256, 192, launch_tiles<OT, 4, 2, 2, 3, 2>}, {256, 256, launch_tiles<OT, 2, 4, 4, 2, 2>}};
+  Launch best = nullptr;
+  double least = 0.0;
+  for (const auto& v : kVariants) {
+    const long long groups = ((a.M + v.tm - 1) / v.tm) * ((a.N + v.tn - 1) / v.tn);
+    if ((a.M + v.tm - 1) / v.tm > 65535) continue;  // the grid's second dimension
+    const double bytes = (v.tm + v.tn) / 50e3, ops = 2.0 * v.tm * v.tn / 9e6;
+    const double us = (double)((groups + kUnits - 1) / kUnits) * (bytes > ops ? bytes : ops);
+    if (!best || us < least) {
+      best = v.launch;
+      least = us;
+    }
+  }
+  return best(a, stream);
 }
 
 }  // namespace
@@ -213,9 +465,9 @@ extern "C" orbit_status orbit_int8_qlinear(const orbit_int8_qlinear_args* p, hip
   a.vec = vector_rows(p->out, p->N);
   hipError_t e;
   switch (p->out_dtype) {
-    case ORBIT_BF16: e = launch_thin<__bf16>(a, stream); break;
-    case ORBIT_F16: e = launch_thin<_Float16>(a, stream); break;
-    default: e = launch_thin<float>(a, stream);
+    case ORBIT_BF16: e = launch_product<__bf16>(a, stream); break;
+    case ORBIT_F16: e = launch_product<_Float16>(a, stream); break;
+    default: e = launch_product<float>(a, stream);
   }
   return hip_status(e);
 }

@@ -544,6 +544,60 @@ int64_t orbit_paged_attention_workspace(int64_t batch, int64_t q_heads, int64_t 
                                         int64_t table_width, int64_t window,
                                         int32_t format);
 
+/* Attention of several new tokens per request over the paged cache, their own
+ * keys and values appended already: a run of tokens (a prompt, a piece of one,
+ * a chain of drafted tokens), or a tree of drafted tokens.
+ * Request b's new tokens are the rows starts[b] .. starts[b + 1] - 1 of q, n
+ * of them, and the last n of its len = lengths[b] tokens (cut at table_width *
+ * page_size): new token i lies at base + i, base = len - n.  It sees token t <
+ * base + n with (window 0, or t > p - window, or t < sinks), where
+ *   without tree: p = base + i, and t <= p;
+ *   with tree: new token j (t = base + j) is seen exactly if bit j % 64 of
+ *   word j / 64 of its row of `tree` is set, whatever the window (its own bit
+ *   is the caller's to set); for the others (t < base) p = base + (the number
+ *   of its bits) - 1, its place along its branch.
+ *   out[i, h] = sum_t softmax_t(sm_scale * q[i, h] . k[t]) v[t].
+ * starts NULL: one new token per request (tokens = batch, no tree).  Rows of
+ * q outside starts[0] .. starts[batch] are left as they were in out and lse;
+ * starts must not decrease (which rows are written is otherwise unspecified),
+ * and is cut to 0 .. tokens.  Rows with nothing to see, cut lengths, table
+ * entries outside the cache, head groups and roundings as in
+ * orbit_paged_attention.
+ * q: [tokens, q_heads, head_dim] by strides, rows 16-byte aligned, BF16 or
+ * F16; its type is the cache's, either one for an int8 cache.  out: [tokens,
+ * q_heads, head_dim] contiguous, of q's type, 16-byte aligned.  lse: float
+ * [tokens, q_heads], optional.  block_table: int32 [batch, table_width] by row
+ * stride.  lengths: int32 [batch]; starts: int32 [batch + 1]; tree: uint64
+ * [tokens, tree_words] contiguous, 1 <= tree_words <= 1024.  batch <= 65535;
+ * 0 <= tokens < ORBIT_MAX_ROWS, tokens * q_heads / kv_heads < 2^30; 0 <=
+ * window, sinks <= 2^30; table_width *
+ * page_size <= 2^30; sm_scale finite.
+ * workspace: device, 16-byte aligned, orbit_tree_attention_workspace bytes
+ * (may be 0), overwritten.
+ * Errors: ORBIT_E_ARG, ORBIT_E_SHAPE, ORBIT_E_DTYPE, ORBIT_E_HIP. */
+typedef struct {
+  orbit_kv_cache cache;
+  const void *q;
+  void *out;
+  float *lse;
+  const int32_t *block_table, *lengths, *starts;
+  const uint64_t *tree;
+  void *workspace;
+  int64_t workspace_bytes;
+  int64_t q_token_stride, q_head_stride, table_stride;
+  int64_t tokens, batch, q_heads, table_width, tree_words, window, sinks;
+  float sm_scale;
+  int32_t q_dtype;
+} orbit_tree_attention_args;
+
+orbit_status orbit_tree_attention(const orbit_tree_attention_args *args, hipStream_t stream);
+
+/* Bytes of orbit_tree_attention's workspace for these sizes (single: without
+ * starts); -1 for invalid ones.  Host only. */
+int64_t orbit_tree_attention_workspace(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads,
+                                       int64_t head_dim, int64_t page_size, int64_t table_width,
+                                       int64_t window, int64_t sinks, int32_t single);
+
 #ifdef __cplusplus
 }
 #endif

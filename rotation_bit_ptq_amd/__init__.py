@@ -36,6 +36,7 @@ __all__ = [
     "quant_act", "qlinear", "rotate", "int8_pack_weights", "int8_linear",
     "int4_pack_weights", "int4_linear", "int8_quant_rows", "int8_qlinear",
     "block_norm", "adapter_add", "kv_append", "kv_read", "paged_attention",
+    "paged_tree_attention",
     "packed_row_bytes", "LIB_PATH",
 ]
 
@@ -97,6 +98,8 @@ def _load():
         "orbit_kv_read": ([P, P, I64, P, P, ctypes.c_int, P], ctypes.c_int),
         "orbit_paged_attention": ([P, P], ctypes.c_int),
         "orbit_paged_attention_workspace": ([I64] * 7 + [I32], I64),
+        "orbit_tree_attention": ([P, P], ctypes.c_int),
+        "orbit_tree_attention_workspace": ([I64] * 9 + [I32], I64),
         "orbit_int8_quant_rows": ([P, P, ctypes.c_int, I64, I64, I64, P, P, P], ctypes.c_int),
         "orbit_int8_qlinear": ([P, P], ctypes.c_int),
     }
@@ -464,7 +467,7 @@ def kv_read(k_cache, v_cache, slots, *, k_scale=None, v_scale=None, dtype=None):
     return _binding.kv_read(k_cache, v_cache, slots, k_scale, v_scale, dtype)
 
 
-def paged_attention(q, k_cache, v_cache, block_table, lengths, *, scale=None, window=0,
+def paged_attention(q, k_cache, v_cache, block_table, lengths, *, scale=None, window=0, sinks=0,
                     k_scale=None, v_scale=None, out=None, return_lse=False):
     """Attention of one new token per request over the paged cache.
 
@@ -472,9 +475,37 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, *, scale=None, wi
     for int8); block_table: int32 [batch, width], the pages of each request;
     lengths: int32 [batch], the tokens each sees (0: the output is 0, its lse
     -inf).  Head h reads the keys of head h // (q_heads // kv_heads).  scale:
-    1 / sqrt(dim) by default.  window > 0: the last `window` tokens alone.
-    Returns out [batch, q_heads, dim], with return_lse also lse float32
-    [batch, q_heads].
+    1 / sqrt(dim) by default.  window > 0: the last `window` tokens alone, and
+    the first `sinks` ones, which stay visible.  Returns out [batch, q_heads,
+    dim], with return_lse also lse float32 [batch, q_heads].
     """
+    if sinks and window:
+        return _binding.tree_attention(q, k_cache, v_cache, block_table, lengths, None, None, scale, window, sinks,
+                                       k_scale, v_scale, out, return_lse)
+    if sinks < 0:
+        raise OrbitError(f"sinks must not be negative, got {sinks}")
     return _binding.paged_attention(q, k_cache, v_cache, block_table, lengths, scale, window, k_scale, v_scale,
                                     out, return_lse)
+
+
+def paged_tree_attention(q, k_cache, v_cache, block_table, lengths, starts, *, tree=None, scale=None, window=0, sinks=0,
+                         k_scale=None, v_scale=None, out=None, return_lse=False):
+    """Attention of several new tokens per request over the paged cache, to
+    which their own keys and values have been appended: runs (prompts, pieces
+    of them, chains of drafted tokens), or trees of drafted tokens.
+
+    q: [tokens, q_heads, dim]; starts: int32 [batch + 1]: request b's n new
+    tokens are rows starts[b] .. starts[b + 1] - 1 and the last n of its
+    lengths[b] tokens.  New token i sees every token up to itself; with tree
+    (int64 [tokens, words]) those before the new ones, and new token j of its
+    request if bit j % 64 of word j // 64 of its row is set (its own too).
+    window > 0: of the tokens up to its place p (its own, in a tree that along
+    its branch: base + the number of its bits - 1) those after p - window, and
+    the first `sinks`; the tokens of a tree's mask are seen whatever the
+    window.  Rows outside starts[0] .. starts[batch] are left as they were.
+    The rest as in paged_attention.
+    """
+    if starts is None:
+        raise OrbitError("starts must be a torch tensor on a GPU")
+    return _binding.tree_attention(q, k_cache, v_cache, block_table, lengths, starts, tree, scale, window, sinks,
+                                   k_scale, v_scale, out, return_lse)

@@ -29,7 +29,7 @@ SOURCES = ["abi.cpp", "codebook.cpp", "rpbh_quant.hip", "rpbh_bf16_act.hip",
            "qgemm_a2.hip", "qgemm_a3.hip", "qgemm_a4.hip", "qgemm_a6.hip", "qgemm_a8.hip",
            "block_norm.hip", "block_norm_f32.hip", "kv_cache.hip",
            "paged_attention.hip", "paged_attention_int8.hip", "adapter.hip",
-           "int8_rows.hip", "int8_qlinear.hip"]
+           "int8_rows.hip", "int8_qlinear.hip", "paged_tree.hip", "paged_tree_bf16.hip", "paged_tree_int8.hip"]
 # Packed fp32 VALU instructions are kept out of the generated code.
 FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

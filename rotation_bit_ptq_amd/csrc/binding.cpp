@@ -414,6 +414,67 @@ PyObject* paged_attention(PyObject* const* v) {
   return with_lse ? pair(out, lse) : wrap(out);
 }
 
+// q, k_cache, v_cache, block_table, lengths, starts (None: one token each),
+// tree, scale, window, sinks, k_scale, v_scale, out, return_lse
+PyObject* tree_attention(PyObject* const* v) {
+  const at::Tensor& q = tensor(v[0], "q", 3);
+  const int dev = q.get_device();
+  const at::ScalarType qt = q.scalar_type();
+  orbit_tree_attention_args a = {};
+  a.q_dtype = dtype(qt, "q");
+  a.cache = cache_of(v[1], v[2], v[10], v[11], dev);
+  const int64_t T = q.size(0), H = q.size(1), D = a.cache.head_dim;
+  check(q, "q", dev, {T, H, D}, qt);
+  const at::Tensor &table = tensor(v[3], "block_table", 2), &lengths = tensor(v[4], "lengths", 1);
+  const int64_t B = lengths.size(0);
+  check(table, "block_table", dev, {B, table.size(1)}, at::kInt);
+  check(lengths, "lengths", dev, {B}, at::kInt);
+  const bool single = v[5] == Py_None;
+  if (single && B != T) refuse("q must have a row for each of %lld requests, got %lld", (long long)B, (long long)T);
+  if (!single) a.starts = (const int32_t*)checked(v[5], "starts", dev, {B + 1}, at::kInt).data_ptr();
+  if (v[6] != Py_None) {
+    if (single) refuse("tree needs starts");
+    const at::Tensor& tree = tensor(v[6], "tree", 2);
+    check(tree, "tree", dev, {T, tree.size(1)}, at::kLong);
+    dense(tree, "tree");
+    a.tree_words = tree.size(1);
+    if (a.tree_words < 1 || a.tree_words > 1024) refuse("tree must have 1 to 1024 words for each token, got %lld", (long long)a.tree_words);
+    a.tree = (const uint64_t*)tree.data_ptr();
+  }
+  a.q = q.data_ptr();
+  a.q_token_stride = q.stride(0);
+  a.q_head_stride = q.stride(1);
+  a.block_table = (const int32_t*)table.data_ptr();
+  a.table_stride = table.stride(0);
+  a.table_width = table.size(1);
+  a.lengths = (const int32_t*)lengths.data_ptr();
+  a.tokens = T;
+  a.batch = B;
+  a.q_heads = H;
+  a.window = integer(v[8]);
+  a.sinks = integer(v[9]);
+  a.sm_scale = v[7] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : (float)number(v[7]);
+  const at::Tensor out = v[12] == Py_None ? fresh(q, {T, H, D}, qt) : checked(v[12], "out", dev, {T, H, D}, qt);
+  dense(out, "out");
+  a.out = out.data_ptr();
+  at::Tensor lse, work;
+  const bool with_lse = truth(v[13]);
+  if (with_lse) {
+    lse = fresh(q, {T, H}, at::kFloat);
+    a.lse = (float*)lse.data_ptr();
+  }
+  a.workspace_bytes = orbit_tree_attention_workspace(T, B, H, a.cache.kv_heads, D, a.cache.page_size, a.table_width, a.window, a.sinks, single);
+  if (a.workspace_bytes < 0)
+    refuse("orbit_tree_attention: invalid shape (%lld tokens, batch %lld, %lld query heads on %d, dim %lld, window %lld, sinks %lld)",
+           (long long)T, (long long)B, (long long)H, (int)a.cache.kv_heads, (long long)D, (long long)a.window, (long long)a.sinks);
+  if (a.workspace_bytes) {
+    work = fresh(q, {a.workspace_bytes}, at::kByte);
+    a.workspace = work.data_ptr();
+  }
+  launch("orbit_tree_attention", dev, [&](hipStream_t s) { return orbit_tree_attention(&a, s); });
+  return with_lse ? pair(out, lse) : wrap(out);
+}
+
 // rot (an orbit_rpbh's address, or 0), rot's perm (or None), X
 PyObject* int8_quant_rows(PyObject* const* v) {
   const at::Tensor& x = tensor(v[2], "X", 2);
@@ -507,6 +568,7 @@ PyMethodDef g_methods[] = {
     ENTRY(kv_append, 13),
     ENTRY(kv_read, 6),
     ENTRY(paged_attention, 11),
+    ENTRY(tree_attention, 14),
     ENTRY(int8_quant_rows, 3),
     ENTRY(int8_qlinear, 8),
     {nullptr, nullptr, 0, nullptr}};

@@ -487,6 +487,50 @@ typedef struct {
 
 orbit_status orbit_kv_append(const orbit_kv_append_args *args, hipStream_t stream);
 
+/* Norms of queries and keys for each head, before their position rotation:
+ *   x^ = x / sqrt(mean x^2 + eps) * w                          (RMS)
+ *   x^ = (x - mean x) / sqrt(mean (x - mean x)^2 + eps) * w    (LAYER)
+ * over the head_dim coordinates of a head, in float32.  q_weight, k_weight:
+ * head_dim weights of w_dtype (F32, BF16 or F16), optional (all 1), those of
+ * the next head a stride further (0: the same for all heads). */
+typedef struct {
+  const void *q_weight, *k_weight;
+  int64_t q_weight_stride, k_weight_stride; /* elements */
+  int32_t w_dtype, norm;                    /* orbit_dtype, orbit_norm (not NONE) */
+  float eps;
+} orbit_head_norm;
+
+/* orbit_kv_append with its keys and queries normed first: norm, position
+ * rotation, Hadamard rotation, then the cache's format, in one pass.
+ * Arguments and errors as there, and ORBIT_E_ARG / ORBIT_E_DTYPE /
+ * ORBIT_E_SHAPE for the norm's. */
+orbit_status orbit_kv_append_normed(const orbit_kv_append_args *args, const orbit_head_norm *norm,
+                                    hipStream_t stream);
+
+/* The same for queries and keys that stay rows (attention without a cache):
+ * q_out, k_out = rotations of the normed q, k.
+ * q, q_out: [tokens, q_heads, head_dim], k, k_out: [tokens, k_heads, head_dim]
+ * (k_heads 0: queries alone) by token and head strides, all of dtype, F32,
+ * BF16 or F16, any alignment of it; q_out may be q itself and k_out k itself
+ * (same pointer and strides), otherwise outputs alias nothing.  Rotations,
+ * table and positions as in orbit_kv_append; rows whose position is outside
+ * the table are NaN.  head_dim a multiple of 8, 8 .. 256; 1 <= q_heads, 0 <=
+ * k_heads <= 65536; 0 <= tokens < ORBIT_MAX_ROWS.
+ * Errors: ORBIT_E_ARG, ORBIT_E_SHAPE, ORBIT_E_DTYPE, ORBIT_E_HIP. */
+typedef struct {
+  orbit_head_norm norm;
+  const void *q, *k;
+  void *q_out, *k_out;
+  const int64_t *positions;
+  const float *cos_sin;
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+  int64_t q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride;
+  int64_t tokens, q_heads, k_heads, head_dim, table_len;
+  int32_t rot_dim, dtype, interleaved, hadamard;
+} orbit_qk_norm_args;
+
+orbit_status orbit_qk_norm(const orbit_qk_norm_args *args, hipStream_t stream);
+
 /* Reads tokens of the cache back to dense rows, the inverse of the append:
  * k_out[t], v_out[t] = the values (int8: code * scale, rounded once) of
  * token slots[t], zeros where that slot is outside the cache.  k_out, v_out:

@@ -35,7 +35,7 @@ __all__ = [
     "OrbitError", "Codebook", "Rotation", "fit_codebook", "pack_weights",
     "quant_act", "qlinear", "rotate", "int8_pack_weights", "int8_linear",
     "int4_pack_weights", "int4_linear", "int8_quant_rows", "int8_qlinear",
-    "block_norm", "adapter_add", "kv_append", "kv_read", "paged_attention",
+    "block_norm", "adapter_add", "qk_norm", "kv_append", "kv_read", "paged_attention",
     "paged_tree_attention",
     "packed_row_bytes", "LIB_PATH",
 ]
@@ -98,6 +98,8 @@ def _load():
         "orbit_kv_read": ([P, P, I64, P, P, ctypes.c_int, P], ctypes.c_int),
         "orbit_paged_attention": ([P, P], ctypes.c_int),
         "orbit_paged_attention_workspace": ([I64] * 7 + [I32], I64),
+        "orbit_kv_append_normed": ([P, P, P], ctypes.c_int),
+        "orbit_qk_norm": ([P, P], ctypes.c_int),
         "orbit_tree_attention": ([P, P], ctypes.c_int),
         "orbit_tree_attention_workspace": ([I64] * 9 + [I32], I64),
         "orbit_int8_quant_rows": ([P, P, ctypes.c_int, I64, I64, I64, P, P, P], ctypes.c_int),
@@ -442,8 +444,30 @@ def adapter_add(y, x, A, B, ids, *, scale=None, ranks=None, out=None):
     return _binding.adapter_add(y, x, A, B, ids, scale, ranks, out)
 
 
+def qk_norm(q, k=None, *, norm="rms", q_weight=None, k_weight=None, eps=1e-6, positions=None, cos_sin=None,
+            interleaved=False, hadamard=False, q_out=None, k_out=None):
+    """Norms of queries and keys for each head, with the position rotation
+    (and, with hadamard, the orthonormal Hadamard rotation) in the same pass:
+
+        x^ = norm(x) * weight,  then (a, b) -> (a cos - b sin, a sin + b cos)
+
+    norm: "rms" or "layer", over a head's coordinates in float32; q:
+    [tokens, q_heads, dim], k: [tokens, k_heads, dim] (or None), strided heads
+    for instance; q_weight: [dim] or [q_heads, dim], k_weight: [dim] or
+    [k_heads, dim], both of one floating type (None: ones); cos_sin,
+    positions, interleaved as in kv_append, which does the same on the way
+    into a cache.  Returns (q', k'), q' alone without k; q_out may be q, k_out
+    may be k.
+    """
+    if norm is None:
+        raise OrbitError("norm must be 'rms' or 'layer'")
+    return _binding.qk_norm(q, k, _norm(norm), q_weight, k_weight, eps, positions, cos_sin, interleaved, hadamard,
+                            q_out, k_out)
+
+
 def kv_append(k, v, k_cache, v_cache, slots, *, positions=None, cos_sin=None, interleaved=False,
-              q=None, q_out=None, k_scale=None, v_scale=None, hadamard=False):
+              q=None, q_out=None, k_scale=None, v_scale=None, hadamard=False, norm=None, q_weight=None,
+              k_weight=None, eps=1e-6):
     """Appends a key and a value per token and head to the paged cache, the
     position rotation (and, with hadamard, the orthonormal Hadamard rotation
     of each head) applied to keys on the way, and to the queries if given.
@@ -454,10 +478,12 @@ def kv_append(k, v, k_cache, v_cache, slots, *, positions=None, cos_sin=None, in
     [pages, kv_heads, page_size].  slots: int64 [tokens], page * page_size +
     offset, all different; a slot outside the cache (-1) stores nothing.
     cos_sin: float32 [positions, rot_dim], cosines then sines; positions:
-    int64 [tokens].  Returns the rotated queries (None without q).
+    int64 [tokens].  norm: "rms" or "layer": keys and queries are normed for
+    each head before the rotations (qk_norm).  Returns the rotated queries
+    (None without q).
     """
     return _binding.kv_append(k, v, k_cache, v_cache, slots, positions, cos_sin, interleaved, q, q_out,
-                              k_scale, v_scale, hadamard)
+                              k_scale, v_scale, hadamard, _norm(norm), q_weight, k_weight, eps)
 
 
 def kv_read(k_cache, v_cache, slots, *, k_scale=None, v_scale=None, dtype=None):

@@ -27,7 +27,7 @@ SOURCES = ["abi.cpp", "codebook.cpp", "rpbh_quant.hip", "rpbh_bf16_act.hip",
            "rpbh_m2_a128.hip", "rpbh_m2_a256.hip", "rpbh_m2_w128.hip", "rpbh_m2_w256.hip",
            "rpbh_m2_r.hip", "rpbh_m2_big.hip", "qgemm.hip", "qgemm_int8.hip",
            "qgemm_a2.hip", "qgemm_a3.hip", "qgemm_a4.hip", "qgemm_a6.hip", "qgemm_a8.hip",
-           "block_norm.hip", "block_norm_f32.hip", "kv_cache.hip",
+           "block_norm.hip", "block_norm_f32.hip", "kv_cache.hip", "kv_append_norm.hip",
            "paged_attention.hip", "paged_attention_int8.hip", "adapter.hip",
            "int8_rows.hip", "int8_qlinear.hip", "paged_tree.hip", "paged_tree_bf16.hip", "paged_tree_int8.hip"]
 # Packed fp32 VALU instructions are kept out of the generated code.

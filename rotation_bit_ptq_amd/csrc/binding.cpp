@@ -291,8 +291,39 @@ orbit_kv_cache cache_of(PyObject* ko, PyObject* vo, PyObject* kso, PyObject* vso
   return c;
 }
 
+// The norm of queries and keys [.., heads, dim]: kind, weights [dim] or [heads,
+// dim], eps.
+orbit_head_norm head_norm(PyObject* norm, PyObject* q_weight, PyObject* k_weight, PyObject* eps, int dev, int64_t q_heads, int64_t k_heads,
+                          int64_t dim) {
+  orbit_head_norm n = {};
+  n.norm = (int32_t)integer(norm);
+  n.eps = (float)number(eps);
+  if (n.norm == ORBIT_NORM_NONE && (q_weight != Py_None || k_weight != Py_None)) refuse("q_weight and k_weight need a norm");
+  at::ScalarType wt = at::kFloat;
+  bool typed = false;
+  auto weight = [&](PyObject* o, const char* name, int64_t heads, const void*& to, int64_t& stride) {
+    if (o == Py_None) return;
+    const at::Tensor& t = tensor(o, name, -1);
+    if (!typed) {
+      wt = t.scalar_type();
+      n.w_dtype = dtype(wt, name);
+      typed = true;
+    }
+    if (t.dim() == 2) {
+      check(t, name, dev, {heads, dim}, wt);
+      stride = heads > 1 ? t.stride(0) : 0;
+    } else {
+      check(t, name, dev, {dim}, wt);
+    }
+    to = t.data_ptr();
+  };
+  weight(q_weight, "q_weight", q_heads, n.q_weight, n.q_weight_stride);
+  weight(k_weight, "k_weight", k_heads, n.k_weight, n.k_weight_stride);
+  return n;
+}
+
 // k, v, k_cache, v_cache, slots, positions, cos_sin, interleaved, q, q_out,
-// k_scale, v_scale, hadamard
+// k_scale, v_scale, hadamard, norm, q_weight, k_weight, eps
 PyObject* kv_append(PyObject* const* v) {
   const at::Tensor& k = tensor(v[0], "k", 3);
   const int dev = k.get_device();
@@ -343,9 +374,67 @@ PyObject* kv_append(PyObject* const* v) {
   } else if (v[9] != Py_None) {
     refuse("q_out needs q");
   }
-  launch("orbit_kv_append", dev, [&](hipStream_t s) { return orbit_kv_append(&a, s); });
+  const orbit_head_norm norm = head_norm(v[13], v[14], v[15], v[16], dev, a.q_heads, heads, dim);
+  if (v[14] != Py_None && !a.q) refuse("q_weight needs q");
+  launch("orbit_kv_append", dev, [&](hipStream_t s) {
+    return norm.norm == ORBIT_NORM_NONE ? orbit_kv_append(&a, s) : orbit_kv_append_normed(&a, &norm, s);
+  });
   if (!q_out.defined()) Py_RETURN_NONE;
   return wrap(q_out);
+}
+
+// q, k, norm, q_weight, k_weight, eps, positions, cos_sin, interleaved,
+// hadamard, q_out, k_out
+PyObject* qk_norm(PyObject* const* v) {
+  const at::Tensor& q = tensor(v[0], "q", 3);
+  const int dev = q.get_device();
+  const at::ScalarType t = q.scalar_type();
+  orbit_qk_norm_args a = {};
+  a.dtype = dtype(t, "q");
+  const int64_t T = q.size(0), H = q.size(1), D = q.size(2);
+  check(q, "q", dev, {T, H, D}, t);
+  a.tokens = T;
+  a.q_heads = H;
+  a.head_dim = D;
+  a.q = q.data_ptr();
+  a.q_token_stride = q.stride(0);
+  a.q_head_stride = q.stride(1);
+  const at::Tensor q_out = v[10] == Py_None ? fresh(q, {T, H, D}, t) : checked(v[10], "q_out", dev, {T, H, D}, t);
+  a.q_out = q_out.data_ptr();
+  a.q_out_token_stride = q_out.stride(0);
+  a.q_out_head_stride = q_out.stride(1);
+  at::Tensor k_out;
+  if (v[1] != Py_None) {
+    const at::Tensor& k = tensor(v[1], "k", 3);
+    a.k_heads = k.size(1);
+    check(k, "k", dev, {T, a.k_heads, D}, t);
+    a.k = k.data_ptr();
+    a.k_token_stride = k.stride(0);
+    a.k_head_stride = k.stride(1);
+    k_out = v[11] == Py_None ? fresh(k, {T, a.k_heads, D}, t) : checked(v[11], "k_out", dev, {T, a.k_heads, D}, t);
+    a.k_out = k_out.data_ptr();
+    a.k_out_token_stride = k_out.stride(0);
+    a.k_out_head_stride = k_out.stride(1);
+  } else if (v[4] != Py_None || v[11] != Py_None) {
+    refuse("k_weight and k_out need k");
+  }
+  a.norm = head_norm(v[2], v[3], v[4], v[5], dev, H, a.k_heads, D);
+  if (v[7] != Py_None) {
+    const at::Tensor& table = tensor(v[7], "cos_sin", 2);
+    if (table.size(0) < 1) refuse("cos_sin must have a row");
+    check(table, "cos_sin", dev, {table.size(0), table.size(1)}, at::kFloat);
+    dense(table, "cos_sin");
+    if (v[6] == Py_None) refuse("cos_sin needs positions");
+    if (table.size(1) > D) refuse("cos_sin turns %lld coordinates, the heads have %lld", (long long)table.size(1), (long long)D);
+    a.positions = (const int64_t*)checked(v[6], "positions", dev, {T}, at::kLong).data_ptr();
+    a.cos_sin = (const float*)table.data_ptr();
+    a.table_len = table.size(0);
+    a.rot_dim = (int32_t)table.size(1);
+  }
+  a.interleaved = truth(v[8]);
+  a.hadamard = truth(v[9]);
+  launch("orbit_qk_norm", dev, [&](hipStream_t s) { return orbit_qk_norm(&a, s); });
+  return k_out.defined() ? pair(q_out, k_out) : wrap(q_out);
 }
 
 // k_cache, v_cache, slots, k_scale, v_scale, dtype
@@ -565,7 +654,8 @@ PyMethodDef g_methods[] = {
     {"start", (PyCFunction)(void (*)(void))start, METH_FASTCALL, nullptr},
     ENTRY(block_norm, 15),
     ENTRY(adapter_add, 8),
-    ENTRY(kv_append, 13),
+    ENTRY(kv_append, 17),
+    ENTRY(qk_norm, 12),
     ENTRY(kv_read, 6),
     ENTRY(paged_attention, 11),
     ENTRY(tree_attention, 14),

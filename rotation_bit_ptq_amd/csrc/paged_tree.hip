@@ -9,8 +9,8 @@ using namespace orbit::block;
 
 namespace orbit {
 namespace block {
-hipError_t launch_tree_f16(const TreeArgs& a, int rb, dim3 grid, hipStream_t stream) {
-  return launch_tree<ORBIT_KV_F16, ORBIT_KV_F16>(a, rb, grid, stream);
+hipError_t launch_tree_f16(const TreeArgs& a, bool few, dim3 grid, hipStream_t stream) {
+  return launch_tree<ORBIT_KV_F16, ORBIT_KV_F16>(a, few, grid, stream);
 }
 }  // namespace block
 }  // namespace orbit
@@ -28,29 +28,33 @@ bool sizes_ok(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, 
 }
 
 struct Split {
-  int rb, wr, rows;    // blocks of 16 rows per wave, waves on rows, rows of a workgroup
+  bool few;          // one block of 16 rows per wave, and weights in pairs
+  int rows, target;  // of a workgroup; workgroups
   int64_t slots, pieces;
 };
 
-// Rows per workgroup: those of a request of average size, up to 256 (128 at
-// head dimensions above 128, whose sums take the registers).  Pieces: so many
+// Rows per workgroup: two blocks of 16 per wave from 33 rows of a request of
+// average size on (one at head dimensions above 128, whose sums take the
+// registers), so up to 256 or 128.  Pieces, of 256 tokens at least: so many
 // that the workgroups fill the chip twice over (four times where two are
-// resident in a unit), each of two tiles at least.
+// resident in a unit).
 Split split_of(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t cap, int64_t window,
                int64_t sinks, bool single) {
   Split s = {};
   const int dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-  const int64_t group = q_heads / kv_heads, n = batch > 0 ? (tokens + batch - 1) / batch : 0, rows = n * group;
-  s.rb = rows > 32 && dp < 256 ? 2 : 1;
-  s.wr = 1;
-  while (s.wr < kTreeWaves && s.wr * 16 * s.rb < rows) s.wr *= 2;
-  s.rows = s.wr * 16 * s.rb;
+  const int64_t group = q_heads / kv_heads, n = batch > 0 ? (tokens + batch - 1) / batch : 0;
+  s.few = n * group <= 32;
+  s.rows = kTreeWaves * 16 * (s.few || dp == 256 ? 1 : 2);
   s.slots = single ? batch * ((group + s.rows - 1) / s.rows) : tokens * group / s.rows + batch;
+  s.target = kUnits * (s.few && dp == 64 ? 4 : 2);
   int64_t span = cap;
   if (window > 0 && window + sinks + n < span) span = window + sinks + n;
-  const int64_t most = (span + 2 * tree_tile(dp) - 1) / (2 * tree_tile(dp));
-  const int64_t work = (single ? s.slots : tokens * group / s.rows + (batch + 1) / 2) * kv_heads;
-  s.pieces = work > 0 ? (kUnits * (s.rb == 1 && dp == 64 ? 4 : 2) + work - 1) / work : 1;
+  const int64_t most = (span + 255) / 256;
+  // a batch's longest request is taken to be up to four times its average
+  int64_t least = (batch + 3) / 4;
+  if (tokens * group / s.rows > least) least = tokens * group / s.rows;
+  if (least < 1) least = 1;
+  s.pieces = (s.target + least * kv_heads - 1) / (least * kv_heads);
   if (s.pieces > most) s.pieces = most;
   if (s.pieces < 1) s.pieces = 1;
   return s;
@@ -120,7 +124,7 @@ extern "C" orbit_status orbit_tree_attention(const orbit_tree_attention_args* p,
   a.group = (int)(p->q_heads / c.kv_heads);
   a.words = p->tree ? (int)p->tree_words : 0;
   a.rows = s.rows;
-  a.wr = s.wr;
+  a.target = s.target;
   a.pieces = (int)s.pieces;
   a.slots = (int)s.slots;
   a.cap = c.pages > 0 ? (int)(p->table_width * c.page_size) : 0;  // no page: nothing to see
@@ -130,9 +134,9 @@ extern "C" orbit_status orbit_tree_attention(const orbit_tree_attention_args* p,
   const dim3 grid((unsigned)(s.slots * c.kv_heads), (unsigned)s.pieces);
   hipError_t e;
   switch (c.format) {
-    case ORBIT_KV_BF16: e = launch_tree_bf16(a, s.rb, grid, stream); break;
-    case ORBIT_KV_F16: e = launch_tree_f16(a, s.rb, grid, stream); break;
-    default: e = launch_tree_int8(a, p->q_dtype, s.rb, grid, stream);
+    case ORBIT_KV_BF16: e = launch_tree_bf16(a, s.few, grid, stream); break;
+    case ORBIT_KV_F16: e = launch_tree_f16(a, s.few, grid, stream); break;
+    default: e = launch_tree_int8(a, p->q_dtype, s.few, grid, stream);
   }
   if (e == hipSuccess && s.pieces > 1) {
     const int at_once = 64 / (c.head_dim / 4);

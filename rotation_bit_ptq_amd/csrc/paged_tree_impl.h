@@ -8,11 +8,13 @@
 // Rows.  The new tokens of a request and the query heads of one key head are
 // the rows r = token * group + head of one product with its keys.  A workgroup
 // of eight waves takes 16 RB WR rows and a piece of the context: WR waves side
-// by side on the rows (16 RB each), WT on the tokens.  Tiles of TILE tokens
-// are loaded by all waves: into registers while the tile before is multiplied,
-// then, converted to 16 bits where the cache holds codes, to LDS, from where
-// every wave reads what it needs.  So a tile is read from memory once for all
-// its rows, and a tile is in flight all the time.
+// by side on the rows (16 RB each), WT on the tokens.  Tiles of 64 tokens (32
+// at head dimensions above 128) go from memory straight to an LDS ring of four
+// stages, eight (four) rows by each wave, and every wave reads what it needs:
+// a tile is read from memory once for all its rows, three are in flight while
+// one is multiplied, and one barrier stands between two.  Codes of an int8
+// cache go through a ring that is the wave's own and become fp16 on their way
+// to one of two tiles in LDS, once for all rows.
 //
 // Products as in the single-token kernel (paged_attention_impl.h): S^T = K Q^T
 // with the keys as A operand; O^T = V^T P^T with the probabilities in the
@@ -47,8 +49,9 @@ struct TreeArgs {
   long long part_ml, part_n;  // floats before the second and the third
   int tokens, batch, q_heads, group;
   int words;      // of a token's mask; 0: a run
-  int rows, wr;   // rows of a workgroup, waves on them
+  int rows;       // of a workgroup, at most
   int pieces, slots;
+  int target;     // workgroups that the pieces should make
   int cap, window, sinks;
   float scale_log2e;
 };
@@ -88,9 +91,9 @@ __device__ __forceinline__ int request_at(const TreeArgs& a, int slot, int lane)
 __device__ __forceinline__ Request request_of(const TreeArgs& a, int b) {
   Request r;
   r.b = b;
-  r.begin = start_of(a, b);
-  r.n = max(start_of(a, b + 1) - r.begin, 0);
-  const int len = a.lengths[b];
+  r.begin = __builtin_amdgcn_readfirstlane(start_of(a, b));
+  r.n = max(__builtin_amdgcn_readfirstlane(start_of(a, b + 1)) - r.begin, 0);
+  const int len = __builtin_amdgcn_readfirstlane(a.lengths[b]);
   r.len = len < 0 ? 0 : len < a.cap ? len : a.cap;
   r.base = r.len - r.n;
   return r;
@@ -109,34 +112,57 @@ __device__ __forceinline__ uint32_t bits32(const uint64_t* mask, int words, int 
   return (uint32_t)(sh ? (lo >> sh) | (hi << (64 - sh)) : lo);
 }
 
-constexpr int kTreeWaves = 8;
-constexpr int tree_tile(int dp) { return dp == 256 ? 64 : 128; }
-constexpr int tree_lds(int dp) { return 2 * tree_tile(dp) * dp * 2 + tree_tile(dp) * 12 + 16; }
+constexpr int kTreeWaves = 8, kTreeStages = 4;
+constexpr int tree_tile(int dp) { return dp == 256 ? 32 : 64; }
+constexpr int tree_rows(int dp) { return tree_tile(dp) / kTreeWaves; }  // of a tile, by each wave
+// LDS: the 16-bit tiles (keys, then values), the codes' and scales' ring, and
+// for each stage a word (bits: rows whose page lies outside the cache), and
+// whether a wave saw such a page.
+constexpr int tree_tiles_lds(int dp, bool coded) { return (coded ? 2 : kTreeStages) * 2 * tree_tile(dp) * dp * 2; }
+constexpr int tree_raw_stage(int dp) { return 2 * tree_rows(dp) * dp + 4 * tree_rows(dp); }  // of a wave
+constexpr int tree_lds(int dp, bool coded) {
+  return tree_tiles_lds(dp, coded) + (coded ? kTreeStages * kTreeWaves * tree_raw_stage(dp) : 0) + kTreeStages * 8 + kTreeWaves * 4;
+}
+alignas(16) static __device__ const uint32_t kTreeZeros[4] = {0, 0, 0, 0};  // what is read in the place of tokens that are not there
+
+// 16 (4) bytes a lane from memory to LDS at `to`, in lane order.  Inline, with
+// explicit waits: the compiler would wait for all of them before each LDS read.
+__device__ __forceinline__ void tree_load16(uint32_t to, const char* from) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+}
+__device__ __forceinline__ void load_lds16(uint32_t to, uint32_t offset, const char* base) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void tree_load4(uint32_t to, const char* from) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tree_wait() {  // until at most N of this wave's loads are in flight, and no LDS access
+  static_assert(N >= 0 && N < 64);
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
 
 // Q: the queries' format; F: the cache's; DP: head_dim rounded up to 64, 128
-// or 256; RB: blocks of 16 rows per wave.
-template <int Q, int F, int DP, int RB>
+// or 256; RB: blocks of 16 rows per wave; PAIR: weights as two 16-bit numbers.
+template <int Q, int F, int DP, int RB, bool PAIR>
 __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void tree_kernel(TreeArgs a) {
   constexpr bool kCoded = F == ORBIT_KV_INT8;
   typedef Mma<F> M;
   typedef typename M::T T;
   typedef typename M::V8 V8;
   typedef typename Mma<Q>::T QT;
-  constexpr int kThreads = 64 * kTreeWaves, kTokens = tree_tile(DP), kSubs = kTokens / 32;
+  constexpr int kTokens = tree_tile(DP), kSubs = kTokens / 32, kRows = tree_rows(DP), S = kTreeStages;
   constexpr int kSteps = DP / 32, kBlocks = DP / 16;
   constexpr int kElem = kCoded ? 1 : 2;
-  constexpr int kRowLanes = DP * kElem / 16, kRowsAtOnce = kThreads / kRowLanes, kLoads = kTokens / kRowsAtOnce;
-  static_assert(kLoads >= 1 && kTokens % kRowsAtOnce == 0, "whole rows per load");
+  constexpr int kRowLanes = DP * kElem / 16, kAtOnce = 64 / kRowLanes;  // lanes on a row, rows of a load
+  constexpr int kLoads = (kRows + kAtOnce - 1) / kAtOnce;               // of each tensor and tile; INT8: and one of scales
+  constexpr int kInFlight = 2 * kLoads + (kCoded ? 1 : 0);
   constexpr float kLift = lift_of(F);
   typedef Stage<DP * 2> St;
-  constexpr int kStageBytes = kTokens * DP * 2;
+  constexpr int kTileBytes = kTokens * DP * 2, kRaw = tree_raw_stage(DP);
   extern __shared__ __align__(1024) char lds[];
-  char* const kstage = lds;
-  char* const vstage = lds + kStageBytes;
-  float* const kscale = (float*)(lds + 2 * kStageBytes);  // INT8: of each token
-  float* const vscale = kscale + kTokens;
-  uint32_t* const gone = (uint32_t*)(vscale + kTokens);  // tokens whose page is outside the cache: 1
-  uint32_t* const any_gone = gone + kTokens;             // [2]: whether the tile has such tokens, by the tile's parity
+  constexpr uint32_t kRawAt = tree_tiles_lds(DP, kCoded), kGoneAt = kRawAt + (kCoded ? S * kTreeWaves * kRaw : 0);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, lg = lane >> 4;
@@ -148,7 +174,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   const int b = request_at(a, slot, lane);
   if (b >= a.batch) return;
   const Request rq = request_of(a, b);
-  const int row0 = (slot - first_slot(a, b)) * a.rows, all_rows = rq.n * a.group;
+  const int row0 = __builtin_amdgcn_readfirstlane(slot - first_slot(a, b)) * a.rows, all_rows = rq.n * a.group;
   if (row0 < 0 || row0 >= all_rows) return;
   const int rows_here = min(a.rows, all_rows - row0);
 
@@ -162,17 +188,37 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   const int sink_tiles = a.window ? min((min(a.sinks, hi_all) + kTokens - 1) / kTokens, end_tile) : 0;
   const int first_tile = max(sink_tiles, lo_all / kTokens);
   const int tiles = sink_tiles + max(end_tile - first_tile, 0);
-  const int per = max((tiles + a.pieces - 1) / a.pieces, 1), used = (tiles + per - 1) / per;
+  // Pieces of one size for all requests, so that together they are about
+  // a.target workgroups (only the first 4096 requests are counted: the size is
+  // a matter of balance alone), and a request has at most a.pieces of them.
+  int per = max((tiles + a.pieces - 1) / a.pieces, 1);
+  if (a.pieces > 1) {
+    const int most = a.window ? (a.window + a.sinks) / kTokens + 2 : 0x7fffffff;
+    uint32_t all = 0;
+    for (int x = lane; x < min(a.batch, 4096); x += 64) {
+      const int n = a.starts ? max(start_of(a, x + 1) - start_of(a, x), 0) : 1;
+      const int t = min((min(max(a.lengths[x], 0), a.cap) + kTokens - 1) / kTokens, most);
+      all += (uint32_t)min((long long)t * ((n * a.group + a.rows - 1) / a.rows), 1LL << 18);
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) all += (uint32_t)__shfl_xor((int)all, x);
+    per = max(per, __builtin_amdgcn_readfirstlane((int)min((long long)all * a.c.kv_heads / a.target, 1LL << 24)));
+  }
+  const int used = (tiles + per - 1) / per;
   const int k0 = (int)blockIdx.y * per, k1 = min(tiles, k0 + per);
   const bool last = used <= 1;  // nothing to join
   if (k0 >= k1 && blockIdx.y > 0) return;
 
-  const int wt_all = kTreeWaves / a.wr < kSubs ? kTreeWaves / a.wr : kSubs;  // waves on the tokens
-  const int wr = wave % a.wr, wt = wave / a.wr;
+  // Waves on the rows, so many as these need, and on the tokens; where four
+  // are on the tokens a step takes two tiles, otherwise one.
+  int wrs = 1;
+  while (wrs * 16 * RB < rows_here) wrs *= 2;
+  const int wt_all = min(kTreeWaves / wrs, 2 * kSubs), step = wt_all > kSubs ? 2 : 1;
+  const int wr = wave & (wrs - 1), wt = wave / wrs;
   const bool works = wt < wt_all && wr * 16 * RB < rows_here;
 
   // this lane's rows
-  int lo[RB], hi[RB], token[RB], qhead[RB];
+  int lo[RB], hi[RB], token[RB];
   int lo_max = 0, hi_min = 0x7fffffff;
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
@@ -180,7 +226,6 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
     const bool in = (wr * RB + rb) * 16 + r16 < rows_here;
     const int i = (in ? r : row0) / a.group;
     token[rb] = in ? rq.begin + i : -1;
-    qhead[rb] = head * a.group + (in ? r : row0) - i * a.group;
     int p = rq.base + i;
     hi[rb] = p + 1;
     if (a.words) {
@@ -209,6 +254,10 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   lo_max = __builtin_amdgcn_readfirstlane(lo_max);
   hi_min = __builtin_amdgcn_readfirstlane(hi_min);
 
+  auto head_of = [&](int rb) {
+    return token[rb] < 0 ? 0 : head * a.group + row0 + (wr * RB + rb) * 16 + r16 - (token[rb] - rq.begin) * a.group;
+  };
+
   // the bits of the tokens among 32 from t0 on that this lane's row rb sees
   auto seen32 = [&](int rb, int t0) {
     uint32_t m = range32(lo[rb], hi[rb], t0);
@@ -223,7 +272,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   float zscale[RB];
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
-    const QT* const qrow = (const QT*)a.q + (long long)max(token[rb], 0) * a.qts + qhead[rb] * a.qhs;
+    const QT* const qrow = (const QT*)a.q + (long long)max(token[rb], 0) * a.qts + head_of(rb) * a.qhs;
     float f[kSteps][8], m = 0.0f;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
@@ -233,11 +282,12 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       if (in) v = *(const Vec8<QT>*)(qrow + d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        f[s][j] = in ? (float)v.e[j] : 0.0f;
+        // the scale's sign goes to the query, so that the largest product is the largest score
+        f[s][j] = in ? (a.scale_log2e < 0.0f ? -(float)v.e[j] : (float)v.e[j]) : 0.0f;
         if (kCoded) m = fmaxf(m, fabsf(f[s][j]));
       }
     }
-    zscale[rb] = a.scale_log2e;
+    zscale[rb] = fmaxf(fabsf(a.scale_log2e), 1.17549435e-38f);  // not 0: a hidden score is minus infinity
     if (kCoded) {  // into fp16's range by a power of two per row
       m = max_rows32(max_rows16(m));
       const int e = m > 0.0f && m < __builtin_inff() ? __builtin_amdgcn_frexp_expf(m) : 0;
@@ -249,85 +299,125 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
         for (int j = 0; j < 8; ++j) f[s][j] = f[s][j] * down * down2;
     }
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
+    for (int s = 0; s < kSteps; ++s) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) qf[rb][s][j] = (T)f[s][j];
+      asm volatile("" : "+v"(qf[rb][s]));  // or the unrounded values are kept too, for the sums below
+    }
   }
 
-  // Loading.  This thread's rows of a tile are lrow + i * kRowsAtOnce, 16
-  // bytes at unit lcol of each.  Tokens from hi_all on, and those whose page
-  // lies outside the cache, are zeros.
-  const int lrow = tid / kRowLanes, lcol = tid & (kRowLanes - 1);
+  // Loading.  This wave's rows of a tile are kRows wave .. + kRows - 1, load i
+  // takes those from i * kAtOnce on, a lane 16 bytes: rows on one page, all of
+  // them seen by some row and without padding, at constant places from a
+  // scalar address.  Otherwise each lane has an address of its own, and tokens
+  // from hi_all on, those whose page lies outside the cache, and coordinates
+  // past head_dim are read as zeros.
   const int row_bytes = dim * kElem;
-  const bool col_in = lcol * 16 < row_bytes;
+  const int lrow = lane / kRowLanes, lplace = lane & (kRowLanes - 1);
+  typedef const __attribute__((address_space(4))) int32_t* const_ptr;  // by scalar loads, which no vector load waits for
   const int32_t* const table = a.table + b * a.table_stride;
   auto tile_at = [&](int k) { return (k < sink_tiles ? k : first_tile + k - sink_tiles) * kTokens; };
-  u32x4 kr[kLoads], vr[kLoads];
-  _Float16 ksr[kLoads], vsr[kLoads];
-  uint32_t page[kLoads];  // of the next tile's rows; 0xffffffff: nothing to read
+  const bool plain = (int)a.c.page_mask + 1 >= kRows && dim == DP;
+  uint32_t lane_at[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = i * kAtOnce + lrow;
+    // unit of the row that belongs in this lane's place (keys of rows 16 apart are the same)
+    lane_at[i] = (uint32_t)(r * row_bytes + (kCoded ? lplace : lplace ^ St::key((wave * kRows + r) & 15)) * 16);
+  }
+  constexpr int kPairs = kRows / 2;
+  const uint32_t scale_at = 4 * ((uint32_t)lane % kPairs);  // INT8: two tokens a lane, keys' scales, then values'
+  uint32_t page = 0xffffffffu;  // of the next tile's first row
   auto look_up = [&](int k) {
-    const int t0 = tile_at(k) + lrow;
+    const int t = tile_at(k) + wave * kRows;
+    page = k < k1 && t < hi_all ? (uint32_t)((const_ptr)(uintptr_t)table)[t >> a.c.page_shift] : 0xffffffffu;
+  };
+  auto issue = [&](int k) {
+    const int t0 = tile_at(k) + wave * kRows, stage = k % S;
+    const uint32_t to = kCoded ? kRawAt + (uint32_t)(stage * kTreeWaves + wave) * kRaw
+                               : (uint32_t)stage * 2 * kTileBytes + (uint32_t)wave * kRows * DP * 2;
+    constexpr uint32_t kValues = kCoded ? kRows * DP : kTileBytes;
+    uint32_t gone = 0;  // of this wave's rows
+    if (plain && page < a.c.pages && t0 + kRows <= hi_all) {
+      const long long row = cache_row(a.c, page, head, (uint32_t)t0 & a.c.page_mask);
+      const char *const kb = a.c.k + row * row_bytes, *const vb = a.c.v + row * row_bytes;
+      if constexpr (kCoded) {
+        if (lane < 2 * kPairs) tree_load4(to + 2 * kRows * DP, (const char*)((lane < kPairs ? a.c.ks : a.c.vs) + row) + scale_at);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        if (kRows < kAtOnce && lrow >= kRows) break;
+        load_lds16(to + i * 1024, lane_at[i], kb);
+        load_lds16(to + kValues + i * 1024, lane_at[i], vb);
+      }
+    } else {
+      auto page_of = [&](int t) { return t < hi_all ? (uint32_t)table[t >> a.c.page_shift] : 0xffffffffu; };
+      const char* from_k[kLoads];
+      const char* from_v[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = i * kAtOnce + lrow, t = t0 + r;
+        const uint32_t pg = page_of(t);
+        const bool there = pg < a.c.pages;
+        const int byte = (int)(lane_at[i] - (uint32_t)(r * row_bytes));
+        const bool in = there && byte < row_bytes;
+        const long long at = cache_row(a.c, there ? pg : 0, head, (uint32_t)t & a.c.page_mask) * row_bytes + byte;
+        from_k[i] = in ? a.c.k + at : (const char*)kTreeZeros;
+        from_v[i] = in ? a.c.v + at : (const char*)kTreeZeros;
+        const uint64_t lost = __ballot(!there && t < hi_all && r < kRows);
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) gone |= (uint32_t)((lost >> (j * kRowLanes)) & 1u) << (i * kAtOnce + j);
+      }
+      if constexpr (kCoded) {  // the two tokens lie on one page, as pages are even
+        const int t = t0 + 2 * (lane % kPairs);
+        const uint32_t pg = page_of(t);
+        const long long at = cache_row(a.c, pg < a.c.pages ? pg : 0, head, (uint32_t)t & a.c.page_mask);
+        const char* const from_s = pg < a.c.pages ? (const char*)((lane < kPairs ? a.c.ks : a.c.vs) + at) : (const char*)kTreeZeros;
+        if (lane < 2 * kPairs) tree_load4(to + 2 * kRows * DP, from_s);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        if (kRows < kAtOnce && lrow >= kRows) break;
+        tree_load16(to + i * 1024, from_k[i]);
+        tree_load16(to + kValues + i * 1024, from_v[i]);
+      }
+    }
+    if (lane == 0) ((uint8_t*)(lds + kGoneAt))[stage * 8 + wave] = (uint8_t)gone;
+  };
+  // INT8: this wave's rows of tile k become fp16 in tile k % 2
+  auto convert = [&](int k) {
+    const char* const raw = lds + kRawAt + (uint32_t)((k % S) * kTreeWaves + wave) * kRaw;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int t = t0 + i * kRowsAtOnce;
-      page[i] = k < k1 && t < hi_all ? (uint32_t)table[t >> a.c.page_shift] : 0xffffffffu;
+      if (kRows < kAtOnce && lrow >= kRows) break;
+      const int r = wave * kRows + i * kAtOnce + lrow;
+      const u32x4 k4 = *(const u32x4*)(raw + i * 1024 + lane * 16), v4 = *(const u32x4*)(raw + kRows * DP + i * 1024 + lane * 16);
+      char* const to = lds + (k & 1) * 2 * kTileBytes + r * DP * 2;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int at = ((lplace * 2 + c) ^ St::key(r & 15)) << 4;
+        const u32x2 x = codes_to_f16(k4[2 * c]), y = codes_to_f16(k4[2 * c + 1]);
+        const u32x2 z = codes_to_f16(v4[2 * c]), w = codes_to_f16(v4[2 * c + 1]);
+        *(u32x4*)(to + at) = u32x4{x.x, x.y, y.x, y.y};
+        *(u32x4*)(to + kTileBytes + at) = u32x4{z.x, z.y, w.x, w.y};
+      }
     }
   };
-  uint32_t absent;  // bit i: row i was not read
-  auto load = [&](int k) {
-    const int t0 = tile_at(k) + lrow;
-    absent = 0;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int t = t0 + i * kRowsAtOnce;
-      const bool there = page[i] < a.c.pages;
-      absent |= (uint32_t)!there << i;
-      const long long row = there ? cache_row(a.c, page[i], head, (uint32_t)t & a.c.page_mask) : 0;
-      const long long at = row * row_bytes + (col_in ? lcol * 16 : 0);
-      kr[i] = *(const u32x4*)(a.c.k + at);
-      vr[i] = *(const u32x4*)(a.c.v + at);
-      if constexpr (kCoded) {
-        ksr[i] = a.c.ks[row];
-        vsr[i] = a.c.vs[row];
-      }
-    }
+  // this wave's loads have landed
+  auto landed = [&](int later) {  // but for those of the `later` last tiles
+    if (later == 2) tree_wait<2 * kInFlight>();
+    else if (later == 1) tree_wait<kInFlight>();
+    else tree_wait<0>();
   };
-  auto store = [&](int k) {
-    const int t0 = tile_at(k) + lrow;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int r = lrow + i * kRowsAtOnce;
-      const bool keep = !((absent >> i) & 1u) && col_in;
-      const u32x4 zero = {0u, 0u, 0u, 0u};
-      const u32x4 k4 = keep ? kr[i] : zero, v4 = keep ? vr[i] : zero;
-      const int key = St::key(r & 15);
-      if constexpr (kCoded) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const u32x2 x = codes_to_f16(k4[2 * c]), y = codes_to_f16(k4[2 * c + 1]);
-          const u32x2 z = codes_to_f16(v4[2 * c]), w = codes_to_f16(v4[2 * c + 1]);
-          const int at = r * DP * 2 + (((lcol * 2 + c) ^ key) << 4);
-          *(u32x4*)(kstage + at) = u32x4{x.x, x.y, y.x, y.y};
-          *(u32x4*)(vstage + at) = u32x4{z.x, z.y, w.x, w.y};
-        }
-      } else {
-        const int at = r * DP * 2 + ((lcol ^ key) << 4);
-        *(u32x4*)(kstage + at) = k4;
-        *(u32x4*)(vstage + at) = v4;
-      }
-      if (lcol == 0) {
-        const bool out = (absent >> i) & 1u;
-        if constexpr (kCoded) {
-          kscale[r] = out ? 0.0f : (float)ksr[i];
-          vscale[r] = out ? 0.0f : (float)vsr[i];
-        }
-        gone[r] = out;
-        if (out && t0 + i * kRowsAtOnce < hi_all) any_gone[k & 1] = 1;
-      }
-    }
+
+  auto meet = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   };
 
   f32x4 o[RB][kBlocks];
+  constexpr float kSlack = F == ORBIT_KV_BF16 ? 8.0f : 0.0f;
   float m_run[RB], l_run[RB];  // l: this lane's tokens alone
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
@@ -336,80 +426,216 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
 #pragma unroll
     for (int d = 0; d < kBlocks; ++d) o[rb][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const int kread = r16 * DP * 2 + ((lg ^ St::key(r16)) << 4);
+  int kread = r16 * DP * 2 + ((lg ^ St::key(r16)) << 4);
   const int trow = lg * 4 + (r16 >> 2);
-  const int vread = trow * DP * 2 + ((((r16 & 3) >> 1) ^ St::key(trow)) << 4) + (r16 & 1) * 8;
+  int vread = trow * DP * 2 + ((((r16 & 3) >> 1) ^ St::key(trow)) << 4) + (r16 & 1) * 8;
 
-  if (tid < 2) any_gone[tid] = 0;
-  if (k0 < k1) {
-    look_up(k0);
-    load(k0);
-    look_up(k0 + 1);
+  // With two blocks of rows (kPipe) the scores of 32 tokens are computed beside
+  // the weights of the 32 before them, whose products come next, so that a
+  // wave's matrix and vector instructions overlap; also over a step's end
+  // (kCross): those values are read behind the next barrier, so the stage after
+  // next is filled and not the next.
+  constexpr bool kPipe = RB == 2, kCross = kPipe && !kCoded;
+  f32x4 s[RB][2];
+  float vt[8];  // INT8: the values' scales
+  const char* pend = nullptr;
+  bool pend_masked = false;
+  uint32_t pend_seen[RB];
+
+  V8 ph[RB], pl[PAIR ? RB : 1];
+  // Scores of 32 tokens (SCORES), and weights of the pending ones (WEIGHTS), a
+  // part of both at a time: the weights' instructions stand between the keys'
+  // reads and their products.
+  auto advance = [&](f32x4 (&z)[RB][2], const char* ks, auto with_scores, auto with_weights) {
+    constexpr bool SCORES = decltype(with_scores)::value, WEIGHTS = decltype(with_weights)::value;
+    constexpr int kPart = 8 / kSteps < 1 ? 1 : 8 / kSteps;  // weights of a row in a part
+    float m_use[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) m_use[rb] = m_run[rb] == -__builtin_inff() ? 0.0f : m_run[rb] - kLift;
+    if constexpr (SCORES) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) z[rb][half] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      V8 kv[2];
+      if constexpr (SCORES) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          kv[half] = __builtin_bit_cast(V8, *(const u32x4*)(ks + half * 16 * DP * 2 + (kread ^ (i << 6))));
+      }
+      if constexpr (WEIGHTS) {
+        if (i * kPart < 8) {
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int j0 = 0; j0 < (kPart < 2 ? (i & 1 ? 0 : 2) : kPart); j0 += 2) {
+              const int j = i * kPart + j0;
+              float p[2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) p[x] = __builtin_amdgcn_exp2f(fmaf(s[rb][j >> 2][(j & 3) + x], zscale[rb], -m_use[rb]));
+              l_run[rb] += p[0] + p[1];
+              if constexpr (kCoded) {  // a hidden token's scale may be infinite or NaN
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  p[x] = !pend_masked || (pend_seen[rb] >> ((j >> 2) * 16 + lg * 4 + (j & 3) + x)) & 1u ? p[x] * vt[j + x] : 0.0f;
+              }
+              if constexpr (PAIR) {
+                split2(p[0], p[1], ph[rb], pl[rb], j);
+              } else {
+                ph[rb][j] = (T)p[0];
+                ph[rb][j + 1] = (T)p[1];
+              }
+            }
+        }
+      }
+      if constexpr (SCORES) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) z[rb][half] = M::run(kv[half], qf[rb][i], z[rb][half]);
+      }
+      if constexpr (kPipe) __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // The pending tokens' weights with their values; two blocks of coordinates
+  // are read ahead.
+  auto products = [&] {
+    typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+    union Block {
+      s16x4 h[2];
+      V8 v;
+    } u[2][2];
+    auto read = [&](int d) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const char* const at = pend + (vread ^ ((d + x) << 5));
+        u[(d >> 1) & 1][x].h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)at);
+        u[(d >> 1) & 1][x].h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 16 * DP * 2));
+      }
+    };
+    read(0);
+#pragma unroll
+    for (int d = 0; d < kBlocks; d += 2) {
+      if (d + 2 < kBlocks) read(d + 2);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+          o[rb][d + x] = M::run(u[(d >> 1) & 1][x].v, ph[rb], o[rb][d + x]);
+          if constexpr (PAIR) o[rb][d + x] = M::run(u[(d >> 1) & 1][x].v, pl[rb], o[rb][d + x]);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // A step of one tile has three in flight beside it (two: kCross), one of two
+  // tiles two.
+  const int ahead = step == 2 || kCross ? 2 : S - 1;
+  look_up(k0);
+#pragma unroll 1
+  for (int x = k0; x < min(k0 + ahead, k1); ++x) {
+    issue(x);
+    look_up(x + 1);
   }
-  for (int k = k0; k < k1; ++k) {
-    __syncthreads();  // the tile before has been read
-    store(k);
-    __syncthreads();
-    if (tid == 0) any_gone[(k + 1) & 1] = 0;
-    if (k + 1 < k1) {
-      load(k + 1);
-      look_up(k + 2);
+  // whether any page of the piece lies outside the cache
+  bool bad = false;
+  if (k0 < k1)
+    for (int x = (tile_at(k0) >> a.c.page_shift) + tid; x <= (min(tile_at(k1 - 1) + kTokens, hi_all) - 1) >> a.c.page_shift; x += 64 * kTreeWaves)
+      bad |= (uint32_t)table[x] >= a.c.pages;
+  if (lane == 0) ((uint32_t*)(lds + kGoneAt + S * 8))[wave] = 0;
+  if (__any(bad)) ((uint32_t*)(lds + kGoneAt + S * 8))[wave] = 1;
+  tree_wait<62>();
+  meet();
+  const u32x4 bad0 = *(const u32x4*)(lds + kGoneAt + S * 8), bad1 = *(const u32x4*)(lds + kGoneAt + S * 8 + 16);
+  const bool holes = __builtin_amdgcn_readfirstlane(bad0.x | bad0.y | bad0.z | bad0.w | bad1.x | bad1.y | bad1.z | bad1.w) != 0;
+#pragma unroll 1
+  for (int k = k0; k < k1; k += step) {
+    const int here = min(step, k1 - k);  // tiles of this step
+    landed(min(k1, k + ahead) - k - here);
+    if constexpr (kCoded) {
+      // two tiles take both places in LDS: those of the step before must have been read
+      if (step == 2) meet();
+      convert(k);
+      if (here == 2) convert(k + 1);
+      tree_wait<62>();
+    }
+    meet();  // the tiles are there, and those of the step before (kCross: the one before that) have been read
+#pragma unroll 1
+    for (int x = k + ahead; x < min(k + ahead + step, k1); ++x) {  // into their stages
+      issue(x);
+      look_up(x + 1);
     }
     if (!works) continue;
-    const int t0 = tile_at(k);
-    const bool holes = any_gone[k & 1] != 0;
 #pragma unroll 1
-    for (int sub = wt; sub < kSubs; sub += wt_all) {
-      const int ts = t0 + sub * 32;
+    for (int n = wt; n < here * kSubs; n += wt_all) {
+      const int at = k + n / kSubs, sub = n % kSubs;
+      const int ts = tile_at(at) + sub * 32;
       if (ts >= hi_all) break;
-      const char* const ks = kstage + sub * 32 * DP * 2;
-      const char* const vs = vstage + sub * 32 * DP * 2;
-      f32x4 s[RB][2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) s[rb][half] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          const V8 kv = __builtin_bit_cast(V8, *(const u32x4*)(ks + half * 16 * DP * 2 + (kread ^ (i << 6))));
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) s[rb][half] = M::run(kv, qf[rb][i], s[rb][half]);
-        }
+      const char* const ks = lds + (kCoded ? at & 1 : at % S) * 2 * kTileBytes + sub * 32 * DP * 2;
+      asm volatile("" : "+v"(kread), "+v"(vread));  // the places made of them are not kept in registers
+      f32x4 z[RB][2];
+      if (kPipe && pend) {
+        advance(z, ks, std::true_type{}, std::true_type{});
+        products();
+      } else {
+        advance(z, ks, std::true_type{}, std::false_type{});
       }
-      float kt[8], vt[8];
+      pend = ks + kTileBytes;
+      float lv[8];
       if constexpr (kCoded) {
+        const char* const scales = lds + kRawAt + (uint32_t)(at % S) * kTreeWaves * kRaw + 2 * kRows * DP;  // of the first wave's rows
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          *(f32x4*)(kt + half * 4) = *(const f32x4*)(kscale + sub * 32 + half * 16 + lg * 4);
-          *(f32x4*)(vt + half * 4) = *(const f32x4*)(vscale + sub * 32 + half * 16 + lg * 4);
+          typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+          const int t = sub * 32 + half * 16 + lg * 4;
+          const char* const from = scales + t / kRows * kRaw + t % kRows * 2;
+          const h4 x = *(const h4*)from, y = *(const h4*)(from + 2 * kRows);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            vt[half * 4 + i] = (float)y[i];
+            lv[half * 4 + i] = __builtin_amdgcn_logf(fmaxf((float)y[i], 5.9604645e-8f));
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) z[rb][half][i] *= (float)x[i];
+          }
         }
       }
-      const bool masked = holes || !((ts >= lo_max || ts + 32 <= a.sinks) && ts + 32 <= hi_min);
-      uint32_t there = 0xffffffffu;
-      if (holes) there = (uint32_t)__ballot(gone[sub * 32 + (lane & 31)] == 0);
-      V8 ph[RB], pl[RB];
+      pend_masked = holes || !((ts >= lo_max || ts + 32 <= a.sinks) && ts + 32 <= hi_min);
+      if (pend_masked) {
+        uint32_t there = 0xffffffffu;
+        if (holes) {  // a wave's rows are a byte, or half of one
+          const uint64_t gone = *(const uint64_t*)(lds + kGoneAt + (at % S) * 8);
+          uint64_t rows = gone;
+          if (kRows == 4) {
+            rows = 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) rows |= ((gone >> (8 * w)) & 15u) << (4 * w);
+          }
+          there = ~(uint32_t)(rows >> (sub * 32));
+        }
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+          const uint32_t seen = seen32(rb, ts) & there;
+          if constexpr (kCoded) pend_seen[rb] = seen;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[rb][j >> 2][j & 3] = (seen >> ((j >> 2) * 16 + lg * 4 + (j & 3))) & 1u ? z[rb][j >> 2][j & 3] : -__builtin_inff();
+        }
+      }
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
-        float z[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          z[j] = s[rb][j >> 2][j & 3] * zscale[rb];
-          if constexpr (kCoded) z[j] *= kt[j];
-        }
-        uint32_t seen = 0xffffffffu;
-        if (masked) {
-          seen = seen32(rb, ts) & there;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) z[j] = (seen >> ((j >> 2) * 16 + lg * 4 + (j & 3))) & 1u ? z[j] : -__builtin_inff();
-        }
         float mt = -__builtin_inff();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if constexpr (kCoded) mt = fmaxf(mt, z[j] + __builtin_amdgcn_logf(fmaxf(vt[j], 5.9604645e-8f)));
-          else mt = fmaxf(mt, z[j]);
+          if constexpr (kCoded) mt = fmaxf(mt, fmaf(z[rb][j >> 2][j & 3], zscale[rb], lv[j]));
+          else mt = fmaxf(mt, z[rb][j >> 2][j & 3]);
         }
+        if constexpr (!kCoded) mt *= zscale[rb];
         mt = max_rows32(max_rows16(mt));
-        if (__any(mt > m_run[rb])) {
+        // with float32's range for the weights (bfloat16) a larger score by
+        // less than 2^8 may stay: the sums are relative to m_run either way
+        if (__any(mt > m_run[rb] + kSlack)) {
           const float m_new = fmaxf(m_run[rb], mt);
           const float alpha = factor(m_run[rb] - (m_new == -__builtin_inff() ? 0.0f : m_new));
           m_run[rb] = m_new;
@@ -417,37 +643,21 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
 #pragma unroll
           for (int d = 0; d < kBlocks; ++d) o[rb][d] *= alpha;
         }
-        const float m_use = m_run[rb] == -__builtin_inff() ? 0.0f : m_run[rb] - kLift;
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          float p0 = __builtin_amdgcn_exp2f(z[j] - m_use), p1 = __builtin_amdgcn_exp2f(z[j + 1] - m_use);
-          l_run[rb] += p0 + p1;
-          if constexpr (kCoded) {  // a hidden token's scale may be infinite or NaN
-            p0 = !masked || (seen >> ((j >> 2) * 16 + lg * 4 + (j & 3))) & 1u ? p0 * vt[j] : 0.0f;
-            p1 = !masked || (seen >> ((j >> 2) * 16 + lg * 4 + (j & 3) + 1)) & 1u ? p1 * vt[j + 1] : 0.0f;
-          }
-          split2(p0, p1, ph[rb], pl[rb], j);
-        }
+        for (int half = 0; half < 2; ++half) s[rb][half] = z[rb][half];
       }
-      typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-#pragma unroll
-      for (int d = 0; d < kBlocks; ++d) {
-        union {
-          s16x4 h[2];
-          V8 v;
-        } u;
-        const char* const at = vs + (vread ^ (d << 5));
-        u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)at);
-        u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 16 * DP * 2));
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          o[rb][d] = M::run(u.v, ph[rb], o[rb][d]);
-          o[rb][d] = M::run(u.v, pl[rb], o[rb][d]);
-        }
+      if constexpr (!kPipe) {
+        advance(z, ks, std::false_type{}, std::true_type{});
+        products();
       }
     }
+    if (kPipe && pend && (!kCross || step == 2 || k + step >= k1)) {
+      f32x4 none[RB][2];
+      advance(none, nullptr, std::false_type{}, std::true_type{});
+      products();
+      pend = nullptr;
+    }
   }
-
   if constexpr (!kCoded) {
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
@@ -466,12 +676,12 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
           }
         const float m_use = m_run[rb] == -__builtin_inff() ? 0.0f : m_run[rb];
 #pragma unroll 1
-        for (int k = k0; k < k1; ++k)
+        for (int k = k0; k < k1; k += step)
 #pragma unroll 1
-          for (int sub = wt; sub < kSubs; sub += wt_all)
+          for (int n = wt; n < min(step, k1 - k) * kSubs; n += wt_all)
 #pragma unroll 1
             for (int x = 0; x < 32; ++x) {
-              const int t = tile_at(k) + sub * 32 + x;
+              const int t = tile_at(k + n / kSubs) + n % kSubs * 32 + x;
               if (t >= hi_all) break;
               const uint32_t pg = (uint32_t)table[t >> a.c.page_shift];
               if (pg >= a.c.pages) continue;
@@ -507,8 +717,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   // The sums of the waves on the same rows meet in LDS, one block of rows
   // after the other; from here on the maximum stands for the lifted one.
   float* const so = (float*)lds;  // [wave with wt > 0][16][DP], then its maxima and sums
-  float* const sm = so + (wt_all - 1) * a.wr * 16 * DP;
-  const int mine = (wt - 1) * a.wr + wr;
+  float* const sm = so + (wt_all - 1) * wrs * 16 * DP;
+  const int mine = (wt - 1) * wrs + wr;
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
     l_run[rb] = add_rows32(add_rows16(l_run[rb]));
@@ -526,14 +736,14 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       __syncthreads();
       if (wt == 0) {
         float m = m_run[rb];
-        for (int w = 1; w < wt_all; ++w) m = fmaxf(m, sm[(((w - 1) * a.wr + wr) * 16 + r16) * 2]);
+        for (int w = 1; w < wt_all; ++w) m = fmaxf(m, sm[(((w - 1) * wrs + wr) * 16 + r16) * 2]);
         const float m_use = m == -__builtin_inff() ? 0.0f : m;
         const float e0 = factor(m_run[rb] - m_use);
         float l = l_run[rb] * e0;
 #pragma unroll
         for (int d = 0; d < kBlocks; ++d) o[rb][d] *= e0;
         for (int w = 1; w < wt_all; ++w) {
-          const int from = ((w - 1) * a.wr + wr) * 16 + r16;
+          const int from = ((w - 1) * wrs + wr) * 16 + r16;
           const float e = factor(sm[from * 2] - m_use);
           l = fmaf(e, sm[from * 2 + 1], l);
 #pragma unroll
@@ -548,7 +758,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       }
     }
     if (wt != 0 || token[rb] < 0) continue;
-    const long long row = (long long)token[rb] * a.q_heads + qhead[rb];
+    const long long row = (long long)token[rb] * a.q_heads + head_of(rb);
     const float l = l_run[rb];
     if (last) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -619,27 +829,34 @@ __global__ __launch_bounds__(64) void tree_join_kernel(TreeArgs a) {
 
 // The unit files instantiate these (one file per pair of formats).
 template <int Q, int F>
-hipError_t launch_tree(const TreeArgs& a, int rb, dim3 grid, hipStream_t stream) {
+hipError_t launch_tree(const TreeArgs& a, bool few, dim3 grid, hipStream_t stream) {
   const int dim = a.c.head_dim;
-  auto go = [&](auto dp, auto blocks) {
-    constexpr int DP = decltype(dp)::value;
-    auto kern = tree_kernel<Q, F, DP, decltype(blocks)::value>;
+  auto go = [&](auto dp, auto blocks, auto pair) {
+    constexpr int DP = decltype(dp)::value, kLds = tree_lds(DP, F == ORBIT_KV_INT8);
+    auto kern = tree_kernel<Q, F, DP, decltype(blocks)::value, decltype(pair)::value>;
     static LaunchCache cache;
-    const hipError_t e = prepare_launch(cache, (const void*)kern, 64 * kTreeWaves, tree_lds(DP), nullptr);
+    const hipError_t e = prepare_launch(cache, (const void*)kern, 64 * kTreeWaves, kLds, nullptr);
     if (e != hipSuccess) return e;
-    kern<<<grid, dim3(64 * kTreeWaves), tree_lds(DP), stream>>>(a);
+    kern<<<grid, dim3(64 * kTreeWaves), kLds, stream>>>(a);
     return hipGetLastError();
   };
   typedef std::integral_constant<int, 1> One;
   typedef std::integral_constant<int, 2> Two;
-  if (dim <= 64) return rb == 1 ? go(std::integral_constant<int, 64>{}, One{}) : go(std::integral_constant<int, 64>{}, Two{});
-  if (dim <= 128) return rb == 1 ? go(std::integral_constant<int, 128>{}, One{}) : go(std::integral_constant<int, 128>{}, Two{});
-  return go(std::integral_constant<int, 256>{}, One{});
+  if (dim <= 64) {
+    const std::integral_constant<int, 64> dp;
+    return few ? go(dp, One{}, std::true_type{}) : go(dp, Two{}, std::false_type{});
+  }
+  if (dim <= 128) {
+    const std::integral_constant<int, 128> dp;
+    return few ? go(dp, One{}, std::true_type{}) : go(dp, Two{}, std::false_type{});
+  }
+  const std::integral_constant<int, 256> dp;
+  return few ? go(dp, One{}, std::true_type{}) : go(dp, One{}, std::false_type{});
 }
 
-hipError_t launch_tree_bf16(const TreeArgs& a, int rb, dim3 grid, hipStream_t stream);
-hipError_t launch_tree_f16(const TreeArgs& a, int rb, dim3 grid, hipStream_t stream);
-hipError_t launch_tree_int8(const TreeArgs& a, int q_dtype, int rb, dim3 grid, hipStream_t stream);
+hipError_t launch_tree_bf16(const TreeArgs& a, bool few, dim3 grid, hipStream_t stream);
+hipError_t launch_tree_f16(const TreeArgs& a, bool few, dim3 grid, hipStream_t stream);
+hipError_t launch_tree_int8(const TreeArgs& a, int q_dtype, bool few, dim3 grid, hipStream_t stream);
 
 }  // namespace block
 }  // namespace orbit

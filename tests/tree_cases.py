@@ -1,9 +1,11 @@
 """Attention of several new tokens over the paged cache in 64 bits, and inputs for it.
 
 Bounds as for single tokens: a score is a sum of D <= 256 products (depth D / 32 + 32 on the matrix cores) and two scalings,
-dz bounds its error; probabilities are within a relative 2 dz + 2^-20 of their values, as pairs of 16-bit operands within
-2^-15 (bfloat16) or 2^-19 (float16, of the largest); sums over L tokens add (L / 128 + 60) E.  The output's error is that
-times sum p |v| / sum p.
+dz bounds its error; probabilities are within a relative 2 dz + 2^-20 of their values; sums over L tokens add (L / 128 +
+60) E.  Above the products' denominator, which stays float32, a probability is a pair of 16-bit operands, within 2^-15
+(bfloat16) or 2^-19 (float16, of the largest), where a request has at most 32 rows (tokens times the group) on average,
+and one number, within half a step, where it has more: 2^-8 or 2^-11, in float16 and beside an int8 cache of the largest
+at least 2^-39 steps down, inside the same 2^-11.  The output's error is the sum of these times sum p |v| / sum p.
 """
 import numpy as np
 import torch
@@ -11,6 +13,7 @@ import torch
 from block_cases import DTYPES, E, check, draw, f64
 
 PAIR = {"bf16": 2.0 ** -15, "f16": 2.0 ** -19, "int8": 2.0 ** -19}
+ONE = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11 + 2.0 ** -19, "int8": 2.0 ** -11 + 2.0 ** -19}
 
 
 def seen_by(length, n, window, sinks, mask=None):
@@ -81,6 +84,8 @@ class Case:
         pages, KV, page, D = k.shape
         T, H, _ = self.q64.shape
         G, room = H // KV, self.table64.shape[1] * page
+        few = -(-T // max(1, len(self.requests))) * G <= 32
+        weight = (PAIR if few else ONE)[self.fmt]
         out, lse = np.full((T, H, D), np.nan), np.full((T, H), np.nan)
         omag, lmag = np.zeros((T, H, D)), np.zeros((T, H))
         for b, (length, n) in enumerate(self.requests):
@@ -105,9 +110,9 @@ class Case:
                         o = o + np.where((seen[:, t_] & (z[:, t_] > -np.inf))[:, None] & ~np.isfinite(vv[t_]), vv[t_], 0)
                     out[rows, h], lse[rows, h] = o, top + np.log(total)
                 dz = (D / 32 + 36) * E * abs(self.scale) * np.abs(self.q64[rows, h]).sum(-1) * np.abs(np.where(np.isfinite(kk), kk, 0)).max(initial=0)
-                rel = 2 * dz + PAIR[self.fmt] + (length / 128 + 60) * E
-                omag[rows, h] = rel[:, None] * (p @ np.abs(fine)) / np.where(total > 0, total, 1)[:, None]
-                lmag[rows, h] = rel + 4 * E * np.abs(np.where(np.isfinite(lse[rows, h]), lse[rows, h], 0))
+                rel = 2 * dz + (length / 128 + 60) * E
+                omag[rows, h] = (rel + weight)[:, None] * (p @ np.abs(fine)) / np.where(total > 0, total, 1)[:, None]
+                lmag[rows, h] = rel + 2.0 ** -20 + 4 * E * np.abs(np.where(np.isfinite(lse[rows, h]), lse[rows, h], 0))
         return out, lse, omag, lmag
 
     def check(self, rbp):

@@ -30,14 +30,14 @@ bool sizes_ok(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, 
 struct Split {
   bool few;          // one block of 16 rows per wave, and weights in pairs
   int rows, target;  // of a workgroup; workgroups
-  int64_t slots, pieces;
+  int64_t slots, pieces, groups;  // groups: workgroups of a key head
 };
 
 // Rows per workgroup: two blocks of 16 per wave from 33 rows of a request of
 // average size on (one at head dimensions above 128, whose sums take the
-// registers), so up to 256 or 128.  Pieces, of 256 tokens at least: so many
-// that the workgroups fill the chip twice over (four times where two are
-// resident in a unit).
+// registers), so up to 256 or 128.  Pieces: so many that the workgroups fill the chip
+// twice over (four times where two are resident in a unit), but two tiles at
+// least (item_of).
 Split split_of(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t cap, int64_t window,
                int64_t sinks, bool single) {
   Split s = {};
@@ -49,14 +49,16 @@ Split split_of(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads,
   s.target = kUnits * (s.few && dp == 64 ? 4 : 2);
   int64_t span = cap;
   if (window > 0 && window + sinks + n < span) span = window + sinks + n;
-  const int64_t most = (span + 255) / 256;
+  const int64_t most = (span + 127) / 128;
   // a batch's longest request is taken to be up to four times its average
   int64_t least = (batch + 3) / 4;
   if (tokens * group / s.rows > least) least = tokens * group / s.rows;
   if (least < 1) least = 1;
   s.pieces = (s.target + least * kv_heads - 1) / (least * kv_heads);
   if (s.pieces > most) s.pieces = most;
-  if (s.pieces < 1) s.pieces = 1;
+  // every workgroup counts the requests: not too many
+  if (s.pieces < 1 || batch > 512) s.pieces = 1;
+  s.groups = s.slots + (s.pieces > 1 ? s.target / kv_heads + 2 : 0);
   return s;
 }
 
@@ -102,7 +104,7 @@ extern "C" orbit_status orbit_tree_attention(const orbit_tree_attention_args* p,
                            single);
   const int64_t need = bytes_of(s, p->tokens, p->q_heads, c.head_dim);
   if (need > 0 && (!p->workspace || !aligned_to(p->workspace, 16) || p->workspace_bytes < need)) return ORBIT_E_ARG;
-  if (s.slots * c.kv_heads >= (1LL << 31) || s.pieces > 65535) return ORBIT_E_SHAPE;
+  if (s.groups * c.kv_heads >= (1LL << 31)) return ORBIT_E_SHAPE;
   TreeArgs a = {};
   a.c = cache_of(c);
   a.q = (const char*)p->q;
@@ -131,7 +133,7 @@ extern "C" orbit_status orbit_tree_attention(const orbit_tree_attention_args* p,
   a.window = (int)p->window;
   a.sinks = (int)p->sinks;
   a.scale_log2e = p->sm_scale * 1.44269504089f;
-  const dim3 grid((unsigned)(s.slots * c.kv_heads), (unsigned)s.pieces);
+  const dim3 grid((unsigned)(s.groups * c.kv_heads));
   hipError_t e;
   switch (c.format) {
     case ORBIT_KV_BF16: e = launch_tree_bf16(a, s.few, grid, stream); break;

@@ -50,7 +50,8 @@ struct TreeArgs {
   int tokens, batch, q_heads, group;
   int words;      // of a token's mask; 0: a run
   int rows;       // of a workgroup, at most
-  int pieces, slots;
+  int pieces;     // of a row's context, at most
+  int slots;      // where there are no pieces: of row tiles
   int target;     // workgroups that the pieces should make
   int cap, window, sinks;
   float scale_log2e;
@@ -99,6 +100,67 @@ __device__ __forceinline__ Request request_of(const TreeArgs& a, int b) {
   return r;
 }
 
+// What a workgroup takes, where contexts are cut in pieces: a row tile of a
+// request, and a piece of `per` tiles of its context; b < 0: nothing.  Every
+// workgroup counts the requests' row tiles and tiles, from which the size of a
+// piece (one for all, so that together they are about a.target workgroups)
+// and whose item this is follow.
+struct Item {
+  int b, row_tile, piece, per;
+};
+__device__ __forceinline__ Item item_of(const TreeArgs& a, int item, int tile, int lane) {
+  auto count = [&](int x, int& row_tiles, int& tiles) {
+    row_tiles = tiles = 0;
+    if (x >= a.batch) return;
+    const int n = a.starts ? max(start_of(a, x + 1) - start_of(a, x), 0) : 1;
+    row_tiles = (n * a.group + a.rows - 1) / a.rows;
+    tiles = (min(max(a.lengths[x], 0), a.cap) + tile - 1) / tile;
+    if (a.window) tiles = min(tiles, (a.window + n) / tile + a.sinks / tile + 3);  // at most, for any of its rows
+  };
+  int row_tiles, tiles, most = 0, rows = 0;
+  float all = 0.0f;
+  for (int x = 0; x < a.batch; x += 64) {
+    count(x + lane, row_tiles, tiles);
+    most = max(most, row_tiles ? tiles : 0);
+    rows += row_tiles;
+    all += (float)row_tiles * (float)tiles;
+  }
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) {
+    most = max(most, __shfl_xor(most, x));
+    rows += __shfl_xor(rows, x);
+    all += __shfl_xor(all, x);
+  }
+  const float left = fmaxf((float)a.target - (float)rows * (float)a.c.kv_heads, 0.25f * (float)a.target);
+  Item it;
+  it.per = max(max((int)(all * (float)a.c.kv_heads / left) + 1, (most + a.pieces - 1) / a.pieces), 2);
+  it.per = __builtin_amdgcn_readfirstlane(it.per);
+  it.b = -1;
+  it.row_tile = it.piece = 0;
+  for (int x = 0; x < a.batch; x += 64) {
+    if (a.batch > 64) count(x + lane, row_tiles, tiles);
+    const int mine = row_tiles * max((tiles + it.per - 1) / it.per, 1);  // a request with nothing to see has zeros to write
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_up(upto, d);
+      upto += lane >= d ? o : 0;
+    }
+    const int total = __builtin_amdgcn_readlane(upto, 63);
+    if (item < total) {
+      const int who = __builtin_ctzll(__ballot(upto > item));
+      const int local = item - (__builtin_amdgcn_readlane(upto, who) - __builtin_amdgcn_readlane(mine, who));
+      const int r = __builtin_amdgcn_readlane(row_tiles, who);
+      it.b = x + who;
+      it.piece = local / r;
+      it.row_tile = r - 1 - (local - it.piece * r);
+      break;
+    }
+    item -= total;
+  }
+  return it;
+}
+
 // The bits of tokens [from, to) among 32 from `tile` on.
 __device__ __forceinline__ uint32_t range32(int from, int to, int tile) {
   const int x = min(max(from - tile, 0), 32), y = min(max(to - tile, 0), 32);
@@ -115,13 +177,18 @@ __device__ __forceinline__ uint32_t bits32(const uint64_t* mask, int words, int 
 constexpr int kTreeWaves = 8, kTreeStages = 4;
 constexpr int tree_tile(int dp) { return dp == 256 ? 32 : 64; }
 constexpr int tree_rows(int dp) { return tree_tile(dp) / kTreeWaves; }  // of a tile, by each wave
-// LDS: the 16-bit tiles (keys, then values), the codes' and scales' ring, and
+// LDS: the 16-bit tiles (keys, then values), the codes' ring and the scales' of
+// twice the stages (a wave's codes have been read when they are converted, its
+// scales are read by all waves later), and of as many
 // for each stage a word (bits: rows whose page lies outside the cache), and
 // whether a wave saw such a page.
 constexpr int tree_tiles_lds(int dp, bool coded) { return (coded ? 2 : kTreeStages) * 2 * tree_tile(dp) * dp * 2; }
-constexpr int tree_raw_stage(int dp) { return 2 * tree_rows(dp) * dp + 4 * tree_rows(dp); }  // of a wave
+constexpr int tree_raw_stage(int dp) { return 2 * tree_rows(dp) * dp; }    // of a wave
+constexpr int tree_scale_stage(int dp) { return 4 * tree_rows(dp); }
 constexpr int tree_lds(int dp, bool coded) {
-  return tree_tiles_lds(dp, coded) + (coded ? kTreeStages * kTreeWaves * tree_raw_stage(dp) : 0) + kTreeStages * 8 + kTreeWaves * 4;
+  return tree_tiles_lds(dp, coded) +
+         (coded ? kTreeWaves * (kTreeStages * tree_raw_stage(dp) + 2 * kTreeStages * tree_scale_stage(dp)) : 0) + 2 * kTreeStages * 8 +
+         kTreeWaves * 4;
 }
 alignas(16) static __device__ const uint32_t kTreeZeros[4] = {0, 0, 0, 0};  // what is read in the place of tokens that are not there
 
@@ -162,19 +229,30 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   typedef Stage<DP * 2> St;
   constexpr int kTileBytes = kTokens * DP * 2, kRaw = tree_raw_stage(DP);
   extern __shared__ __align__(1024) char lds[];
-  constexpr uint32_t kRawAt = tree_tiles_lds(DP, kCoded), kGoneAt = kRawAt + (kCoded ? S * kTreeWaves * kRaw : 0);
+  constexpr int kScale = tree_scale_stage(DP);
+  constexpr uint32_t kRawAt = tree_tiles_lds(DP, kCoded), kScaleAt = kRawAt + (kCoded ? S * kTreeWaves * kRaw : 0),
+                     kGoneAt = kScaleAt + (kCoded ? 2 * S * kTreeWaves * kScale : 0);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, lg = lane >> 4;
   const int dim = a.c.head_dim;
-  // neighbouring workgroups take the key heads of one slot; the last slots
-  // come first, as in a prompt they have the longest contexts
-  const int order = (int)blockIdx.x / a.c.kv_heads, head = (int)blockIdx.x - order * a.c.kv_heads;
-  const int slot = a.slots - 1 - order;
-  const int b = request_at(a, slot, lane);
-  if (b >= a.batch) return;
+  // neighbouring workgroups take the key heads of one item
+  const int item = (int)blockIdx.x / a.c.kv_heads, head = (int)blockIdx.x - item * a.c.kv_heads;
+  Item it;
+  if (a.pieces > 1) {
+    it = item_of(a, item, kTokens, lane);
+  } else {
+    // the last slots first: in a prompt they have the longest contexts
+    const int slot = a.slots - 1 - item;
+    it.b = request_at(a, slot, lane);
+    it.row_tile = __builtin_amdgcn_readfirstlane(slot - first_slot(a, it.b));
+    it.piece = 0;
+    it.per = 1 << 30;
+  }
+  const int b = it.b;
+  if (b < 0 || b >= a.batch) return;
   const Request rq = request_of(a, b);
-  const int row0 = __builtin_amdgcn_readfirstlane(slot - first_slot(a, b)) * a.rows, all_rows = rq.n * a.group;
+  const int row0 = it.row_tile * a.rows, all_rows = rq.n * a.group;
   if (row0 < 0 || row0 >= all_rows) return;
   const int rows_here = min(a.rows, all_rows - row0);
 
@@ -188,26 +266,10 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   const int sink_tiles = a.window ? min((min(a.sinks, hi_all) + kTokens - 1) / kTokens, end_tile) : 0;
   const int first_tile = max(sink_tiles, lo_all / kTokens);
   const int tiles = sink_tiles + max(end_tile - first_tile, 0);
-  // Pieces of one size for all requests, so that together they are about
-  // a.target workgroups (only the first 4096 requests are counted: the size is
-  // a matter of balance alone), and a request has at most a.pieces of them.
-  int per = max((tiles + a.pieces - 1) / a.pieces, 1);
-  if (a.pieces > 1) {
-    const int most = a.window ? (a.window + a.sinks) / kTokens + 2 : 0x7fffffff;
-    uint32_t all = 0;
-    for (int x = lane; x < min(a.batch, 4096); x += 64) {
-      const int n = a.starts ? max(start_of(a, x + 1) - start_of(a, x), 0) : 1;
-      const int t = min((min(max(a.lengths[x], 0), a.cap) + kTokens - 1) / kTokens, most);
-      all += (uint32_t)min((long long)t * ((n * a.group + a.rows - 1) / a.rows), 1LL << 18);
-    }
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) all += (uint32_t)__shfl_xor((int)all, x);
-    per = max(per, __builtin_amdgcn_readfirstlane((int)min((long long)all * a.c.kv_heads / a.target, 1LL << 24)));
-  }
-  const int used = (tiles + per - 1) / per;
-  const int k0 = (int)blockIdx.y * per, k1 = min(tiles, k0 + per);
+  const int per = it.per, used = (tiles + per - 1) / per;
+  const int k0 = min(it.piece * per, tiles), k1 = min(tiles, k0 + per);
   const bool last = used <= 1;  // nothing to join
-  if (k0 >= k1 && blockIdx.y > 0) return;
+  if (k0 >= k1 && it.piece > 0) return;
 
   // Waves on the rows, so many as these need, and on the tokens; where four
   // are on the tokens a step takes two tiles, otherwise one.
@@ -337,12 +399,13 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
     const uint32_t to = kCoded ? kRawAt + (uint32_t)(stage * kTreeWaves + wave) * kRaw
                                : (uint32_t)stage * 2 * kTileBytes + (uint32_t)wave * kRows * DP * 2;
     constexpr uint32_t kValues = kCoded ? kRows * DP : kTileBytes;
+    const uint32_t to_scales = kScaleAt + (uint32_t)(k % (2 * S) * kTreeWaves + wave) * kScale;
     uint32_t gone = 0;  // of this wave's rows
     if (plain && page < a.c.pages && t0 + kRows <= hi_all) {
       const long long row = cache_row(a.c, page, head, (uint32_t)t0 & a.c.page_mask);
       const char *const kb = a.c.k + row * row_bytes, *const vb = a.c.v + row * row_bytes;
       if constexpr (kCoded) {
-        if (lane < 2 * kPairs) tree_load4(to + 2 * kRows * DP, (const char*)((lane < kPairs ? a.c.ks : a.c.vs) + row) + scale_at);
+        if (lane < 2 * kPairs) tree_load4(to_scales, (const char*)((lane < kPairs ? a.c.ks : a.c.vs) + row) + scale_at);
       }
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -373,7 +436,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
         const uint32_t pg = page_of(t);
         const long long at = cache_row(a.c, pg < a.c.pages ? pg : 0, head, (uint32_t)t & a.c.page_mask);
         const char* const from_s = pg < a.c.pages ? (const char*)((lane < kPairs ? a.c.ks : a.c.vs) + at) : (const char*)kTreeZeros;
-        if (lane < 2 * kPairs) tree_load4(to + 2 * kRows * DP, from_s);
+        if (lane < 2 * kPairs) tree_load4(to_scales, from_s);
       }
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -382,7 +445,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
         tree_load16(to + kValues + i * 1024, from_v[i]);
       }
     }
-    if (lane == 0) ((uint8_t*)(lds + kGoneAt))[stage * 8 + wave] = (uint8_t)gone;
+    if (lane == 0) ((uint8_t*)(lds + kGoneAt))[k % (2 * S) * 8 + wave] = (uint8_t)gone;
   };
   // INT8: this wave's rows of tile k become fp16 in tile k % 2
   auto convert = [&](int k) {
@@ -405,11 +468,11 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   };
   // this wave's loads have landed
   auto landed = [&](int later) {  // but for those of the `later` last tiles
-    if (later == 2) tree_wait<2 * kInFlight>();
+    if (later >= 3) tree_wait<3 * kInFlight>();
+    else if (later == 2) tree_wait<2 * kInFlight>();
     else if (later == 1) tree_wait<kInFlight>();
     else tree_wait<0>();
   };
-
   auto meet = [] {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -531,9 +594,9 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
     }
   };
 
-  // A step of one tile has three in flight beside it (two: kCross), one of two
-  // tiles two.
-  const int ahead = step == 2 || kCross ? 2 : S - 1;
+  // Tiles in flight beside a step's: codes' places are free once converted;
+  // others' when the next barrier says so (kCross: the next but one).
+  const int ahead = kCoded ? S : step == 2 || kCross ? 2 : S - 1;
   look_up(k0);
 #pragma unroll 1
   for (int x = k0; x < min(k0 + ahead, k1); ++x) {
@@ -545,11 +608,11 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   if (k0 < k1)
     for (int x = (tile_at(k0) >> a.c.page_shift) + tid; x <= (min(tile_at(k1 - 1) + kTokens, hi_all) - 1) >> a.c.page_shift; x += 64 * kTreeWaves)
       bad |= (uint32_t)table[x] >= a.c.pages;
-  if (lane == 0) ((uint32_t*)(lds + kGoneAt + S * 8))[wave] = 0;
-  if (__any(bad)) ((uint32_t*)(lds + kGoneAt + S * 8))[wave] = 1;
+  if (lane == 0) ((uint32_t*)(lds + kGoneAt + 2 * S * 8))[wave] = 0;
+  if (__any(bad)) ((uint32_t*)(lds + kGoneAt + 2 * S * 8))[wave] = 1;
   tree_wait<62>();
   meet();
-  const u32x4 bad0 = *(const u32x4*)(lds + kGoneAt + S * 8), bad1 = *(const u32x4*)(lds + kGoneAt + S * 8 + 16);
+  const u32x4 bad0 = *(const u32x4*)(lds + kGoneAt + 2 * S * 8), bad1 = *(const u32x4*)(lds + kGoneAt + 2 * S * 8 + 16);
   const bool holes = __builtin_amdgcn_readfirstlane(bad0.x | bad0.y | bad0.z | bad0.w | bad1.x | bad1.y | bad1.z | bad1.w) != 0;
 #pragma unroll 1
   for (int k = k0; k < k1; k += step) {
@@ -586,12 +649,12 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       pend = ks + kTileBytes;
       float lv[8];
       if constexpr (kCoded) {
-        const char* const scales = lds + kRawAt + (uint32_t)(at % S) * kTreeWaves * kRaw + 2 * kRows * DP;  // of the first wave's rows
+        const char* const scales = lds + kScaleAt + (uint32_t)(at % (2 * S)) * kTreeWaves * kScale;  // of the first wave's rows
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           typedef _Float16 h4 __attribute__((ext_vector_type(4)));
           const int t = sub * 32 + half * 16 + lg * 4;
-          const char* const from = scales + t / kRows * kRaw + t % kRows * 2;
+          const char* const from = scales + t / kRows * kScale + t % kRows * 2;
           const h4 x = *(const h4*)from, y = *(const h4*)(from + 2 * kRows);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -606,7 +669,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       if (pend_masked) {
         uint32_t there = 0xffffffffu;
         if (holes) {  // a wave's rows are a byte, or half of one
-          const uint64_t gone = *(const uint64_t*)(lds + kGoneAt + (at % S) * 8);
+          const uint64_t gone = *(const uint64_t*)(lds + kGoneAt + at % (2 * S) * 8);
           uint64_t rows = gone;
           if (kRows == 4) {
             rows = 0;
@@ -777,13 +840,13 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
         if (a.pieces > 1) ((int*)(a.part + a.part_n))[row] = 0;
       }
     } else {
-      const long long at = row * a.pieces + blockIdx.y;
+      const long long at = row * a.pieces + it.piece;
 #pragma unroll
       for (int d = 0; d < kBlocks; ++d)
         if (d * 16 + lg * 4 < dim) *(f32x4*)(a.part + at * dim + d * 16 + lg * 4) = o[rb][d];
       if (lg == 0) {
         *(float2*)(a.part + a.part_ml + at * 2) = make_float2(m_run[rb], l);
-        if (blockIdx.y == 0) ((int*)(a.part + a.part_n))[row] = used;
+        if (it.piece == 0) ((int*)(a.part + a.part_n))[row] = used;
       }
     }
   }
@@ -804,12 +867,13 @@ __global__ __launch_bounds__(64) void tree_join_kernel(TreeArgs a) {
   if (n <= 1 || n > a.pieces) return;
   const float2* const ml = (const float2*)(a.part + a.part_ml) + row * a.pieces;
   float m = -__builtin_inff();
+#pragma unroll 8
   for (int c = 0; c < n; ++c) m = fmaxf(m, ml[c].x);
   const float m_use = m == -__builtin_inff() ? 0.0f : m;
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
   float l = 0.0f;
   const f32x4* const part = (const f32x4*)(a.part + row * a.pieces * dim) + t;
-#pragma unroll 4
+#pragma unroll 8
   for (int c = 0; c < n; ++c) {
     const float e = factor(ml[c].x - m_use);
     const f32x4 v = part[(long long)c * lanes];

@@ -14,7 +14,7 @@
 // a tile is read from memory once for all its rows, three are in flight while
 // one is multiplied, and one barrier stands between two.  Codes of an int8
 // cache go through a ring that is the wave's own and become fp16 on their way
-// to one of two tiles in LDS, once for all rows.
+// to one of three tiles in LDS, once for all rows.
 //
 // Products as in the single-token kernel (paged_attention_impl.h): S^T = K Q^T
 // with the keys as A operand; O^T = V^T P^T with the probabilities in the
@@ -174,20 +174,22 @@ __device__ __forceinline__ uint32_t bits32(const uint64_t* mask, int words, int 
   return (uint32_t)(sh ? (lo >> sh) | (hi << (64 - sh)) : lo);
 }
 
-constexpr int kTreeWaves = 8, kTreeStages = 4;
+constexpr int kTreeWaves = 8;
+constexpr int kTreeWords = 8;  // stages of the scales and the words
+constexpr int tree_stages(bool coded) { return coded ? 3 : 4; }
 constexpr int tree_tile(int dp) { return dp == 256 ? 32 : 64; }
 constexpr int tree_rows(int dp) { return tree_tile(dp) / kTreeWaves; }  // of a tile, by each wave
 // LDS: the 16-bit tiles (keys, then values), the codes' ring and the scales' of
-// twice the stages (a wave's codes have been read when they are converted, its
+// more stages (a wave's codes have been read when they are converted, its
 // scales are read by all waves later), and of as many
 // for each stage a word (bits: rows whose page lies outside the cache), and
 // whether a wave saw such a page.
-constexpr int tree_tiles_lds(int dp, bool coded) { return (coded ? 2 : kTreeStages) * 2 * tree_tile(dp) * dp * 2; }
+constexpr int tree_tiles_lds(int dp, bool coded) { return tree_stages(coded) * 2 * tree_tile(dp) * dp * 2; }
 constexpr int tree_raw_stage(int dp) { return 2 * tree_rows(dp) * dp; }    // of a wave
 constexpr int tree_scale_stage(int dp) { return 4 * tree_rows(dp); }
 constexpr int tree_lds(int dp, bool coded) {
   return tree_tiles_lds(dp, coded) +
-         (coded ? kTreeWaves * (kTreeStages * tree_raw_stage(dp) + 2 * kTreeStages * tree_scale_stage(dp)) : 0) + 2 * kTreeStages * 8 +
+         (coded ? kTreeWaves * (tree_stages(true) * tree_raw_stage(dp) + kTreeWords * tree_scale_stage(dp)) : 0) + kTreeWords * 8 +
          kTreeWaves * 4;
 }
 alignas(16) static __device__ const uint32_t kTreeZeros[4] = {0, 0, 0, 0};  // what is read in the place of tokens that are not there
@@ -219,7 +221,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   typedef typename M::T T;
   typedef typename M::V8 V8;
   typedef typename Mma<Q>::T QT;
-  constexpr int kTokens = tree_tile(DP), kSubs = kTokens / 32, kRows = tree_rows(DP), S = kTreeStages;
+  constexpr int kTokens = tree_tile(DP), kSubs = kTokens / 32, kRows = tree_rows(DP), S = tree_stages(kCoded);
   constexpr int kSteps = DP / 32, kBlocks = DP / 16;
   constexpr int kElem = kCoded ? 1 : 2;
   constexpr int kRowLanes = DP * kElem / 16, kAtOnce = 64 / kRowLanes;  // lanes on a row, rows of a load
@@ -231,7 +233,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   extern __shared__ __align__(1024) char lds[];
   constexpr int kScale = tree_scale_stage(DP);
   constexpr uint32_t kRawAt = tree_tiles_lds(DP, kCoded), kScaleAt = kRawAt + (kCoded ? S * kTreeWaves * kRaw : 0),
-                     kGoneAt = kScaleAt + (kCoded ? 2 * S * kTreeWaves * kScale : 0);
+                     kGoneAt = kScaleAt + (kCoded ? kTreeWords * kTreeWaves * kScale : 0);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, lg = lane >> 4;
@@ -399,7 +401,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
     const uint32_t to = kCoded ? kRawAt + (uint32_t)(stage * kTreeWaves + wave) * kRaw
                                : (uint32_t)stage * 2 * kTileBytes + (uint32_t)wave * kRows * DP * 2;
     constexpr uint32_t kValues = kCoded ? kRows * DP : kTileBytes;
-    const uint32_t to_scales = kScaleAt + (uint32_t)(k % (2 * S) * kTreeWaves + wave) * kScale;
+    const uint32_t to_scales = kScaleAt + (uint32_t)(k % kTreeWords * kTreeWaves + wave) * kScale;
     uint32_t gone = 0;  // of this wave's rows
     if (plain && page < a.c.pages && t0 + kRows <= hi_all) {
       const long long row = cache_row(a.c, page, head, (uint32_t)t0 & a.c.page_mask);
@@ -445,9 +447,9 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
         tree_load16(to + kValues + i * 1024, from_v[i]);
       }
     }
-    if (lane == 0) ((uint8_t*)(lds + kGoneAt))[k % (2 * S) * 8 + wave] = (uint8_t)gone;
+    if (lane == 0) ((uint8_t*)(lds + kGoneAt))[k % kTreeWords * 8 + wave] = (uint8_t)gone;
   };
-  // INT8: this wave's rows of tile k become fp16 in tile k % 2
+  // INT8: this wave's rows of tile k become fp16 in tile k % S
   auto convert = [&](int k) {
     const char* const raw = lds + kRawAt + (uint32_t)((k % S) * kTreeWaves + wave) * kRaw;
 #pragma unroll
@@ -455,7 +457,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       if (kRows < kAtOnce && lrow >= kRows) break;
       const int r = wave * kRows + i * kAtOnce + lrow;
       const u32x4 k4 = *(const u32x4*)(raw + i * 1024 + lane * 16), v4 = *(const u32x4*)(raw + kRows * DP + i * 1024 + lane * 16);
-      char* const to = lds + (k & 1) * 2 * kTileBytes + r * DP * 2;
+      char* const to = lds + k % S * 2 * kTileBytes + r * DP * 2;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int at = ((lplace * 2 + c) ^ St::key(r & 15)) << 4;
@@ -495,22 +497,23 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
 
   // With two blocks of rows (kPipe) the scores of 32 tokens are computed beside
   // the weights of the 32 before them, whose products come next, so that a
-  // wave's matrix and vector instructions overlap; also over a step's end
-  // (kCross): those values are read behind the next barrier, so the stage after
-  // next is filled and not the next.
-  constexpr bool kPipe = RB == 2, kCross = kPipe && !kCoded;
+  // wave's matrix and vector instructions overlap; also over a step's
+  // end where it has one tile: those values are read behind the next barrier, so the stage
+  // after next is filled and not the next.
+  constexpr bool kPipe = RB == 2;
   f32x4 s[RB][2];
   float vt[8];  // INT8: the values' scales
   const char* pend = nullptr;
-  bool pend_masked = false;
-  uint32_t pend_seen[RB];
+  bool pend_odd = false;  // INT8: some of the values' scales are infinite or NaN
+  uint32_t pend_seen[kCoded ? RB : 1];
 
   V8 ph[RB], pl[PAIR ? RB : 1];
   // Scores of 32 tokens (SCORES), and weights of the pending ones (WEIGHTS), a
   // part of both at a time: the weights' instructions stand between the keys'
   // reads and their products.
-  auto advance = [&](f32x4 (&z)[RB][2], const char* ks, auto with_scores, auto with_weights) {
-    constexpr bool SCORES = decltype(with_scores)::value, WEIGHTS = decltype(with_weights)::value;
+  // CHECKED: values' scales of hidden tokens may be infinite or NaN.
+  auto advance_as = [&](f32x4 (&z)[RB][2], const char* ks, auto with_scores, auto with_weights, auto checked) {
+    constexpr bool SCORES = decltype(with_scores)::value, WEIGHTS = decltype(with_weights)::value, CHECKED = decltype(checked)::value;
     constexpr int kPart = 8 / kSteps < 1 ? 1 : 8 / kSteps;  // weights of a row in a part
     float m_use[RB];
 #pragma unroll
@@ -540,10 +543,10 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
 #pragma unroll
               for (int x = 0; x < 2; ++x) p[x] = __builtin_amdgcn_exp2f(fmaf(s[rb][j >> 2][(j & 3) + x], zscale[rb], -m_use[rb]));
               l_run[rb] += p[0] + p[1];
-              if constexpr (kCoded) {  // a hidden token's scale may be infinite or NaN
+              if constexpr (kCoded) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                  p[x] = !pend_masked || (pend_seen[rb] >> ((j >> 2) * 16 + lg * 4 + (j & 3) + x)) & 1u ? p[x] * vt[j + x] : 0.0f;
+                  p[x] = !CHECKED || (pend_seen[rb] >> ((j >> 2) * 16 + lg * 4 + (j & 3) + x)) & 1u ? p[x] * vt[j + x] : 0.0f;
               }
               if constexpr (PAIR) {
                 split2(p[0], p[1], ph[rb], pl[rb], j);
@@ -562,6 +565,10 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       }
       if constexpr (kPipe) __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  auto advance = [&](f32x4 (&z)[RB][2], const char* ks, auto with_scores, auto with_weights) {
+    if (kCoded && decltype(with_weights)::value && pend_odd) advance_as(z, ks, with_scores, with_weights, std::true_type{});
+    else advance_as(z, ks, with_scores, with_weights, std::false_type{});
   };
   // The pending tokens' weights with their values; two blocks of coordinates
   // are read ahead.
@@ -595,8 +602,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   };
 
   // Tiles in flight beside a step's: codes' places are free once converted;
-  // others' when the next barrier says so (kCross: the next but one).
-  const int ahead = kCoded ? S : step == 2 || kCross ? 2 : S - 1;
+  // others' when the next barrier says so (kPipe: the next but one).
+  const int ahead = kCoded ? S : step == 2 || kPipe ? 2 : S - 1;
   look_up(k0);
 #pragma unroll 1
   for (int x = k0; x < min(k0 + ahead, k1); ++x) {
@@ -608,24 +615,24 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   if (k0 < k1)
     for (int x = (tile_at(k0) >> a.c.page_shift) + tid; x <= (min(tile_at(k1 - 1) + kTokens, hi_all) - 1) >> a.c.page_shift; x += 64 * kTreeWaves)
       bad |= (uint32_t)table[x] >= a.c.pages;
-  if (lane == 0) ((uint32_t*)(lds + kGoneAt + 2 * S * 8))[wave] = 0;
-  if (__any(bad)) ((uint32_t*)(lds + kGoneAt + 2 * S * 8))[wave] = 1;
+  if (lane == 0) ((uint32_t*)(lds + kGoneAt + kTreeWords * 8))[wave] = 0;
+  if (__any(bad)) ((uint32_t*)(lds + kGoneAt + kTreeWords * 8))[wave] = 1;
   tree_wait<62>();
   meet();
-  const u32x4 bad0 = *(const u32x4*)(lds + kGoneAt + 2 * S * 8), bad1 = *(const u32x4*)(lds + kGoneAt + 2 * S * 8 + 16);
+  const u32x4 bad0 = *(const u32x4*)(lds + kGoneAt + kTreeWords * 8), bad1 = *(const u32x4*)(lds + kGoneAt + kTreeWords * 8 + 16);
   const bool holes = __builtin_amdgcn_readfirstlane(bad0.x | bad0.y | bad0.z | bad0.w | bad1.x | bad1.y | bad1.z | bad1.w) != 0;
 #pragma unroll 1
   for (int k = k0; k < k1; k += step) {
     const int here = min(step, k1 - k);  // tiles of this step
     landed(min(k1, k + ahead) - k - here);
     if constexpr (kCoded) {
-      // two tiles take both places in LDS: those of the step before must have been read
+      // two tiles take a place that the step before had: it must have been read
       if (step == 2) meet();
       convert(k);
       if (here == 2) convert(k + 1);
       tree_wait<62>();
     }
-    meet();  // the tiles are there, and those of the step before (kCross: the one before that) have been read
+    meet();  // the tiles are there, and those of the step before (kPipe: the one before that) have been read
 #pragma unroll 1
     for (int x = k + ahead; x < min(k + ahead + step, k1); ++x) {  // into their stages
       issue(x);
@@ -637,7 +644,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       const int at = k + n / kSubs, sub = n % kSubs;
       const int ts = tile_at(at) + sub * 32;
       if (ts >= hi_all) break;
-      const char* const ks = lds + (kCoded ? at & 1 : at % S) * 2 * kTileBytes + sub * 32 * DP * 2;
+      const char* const ks = lds + at % S * 2 * kTileBytes + sub * 32 * DP * 2;
       asm volatile("" : "+v"(kread), "+v"(vread));  // the places made of them are not kept in registers
       f32x4 z[RB][2];
       if (kPipe && pend) {
@@ -649,7 +656,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       pend = ks + kTileBytes;
       float lv[8];
       if constexpr (kCoded) {
-        const char* const scales = lds + kScaleAt + (uint32_t)(at % (2 * S)) * kTreeWaves * kScale;  // of the first wave's rows
+        const char* const scales = lds + kScaleAt + (uint32_t)(at % kTreeWords) * kTreeWaves * kScale;  // of the first wave's rows
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           typedef _Float16 h4 __attribute__((ext_vector_type(4)));
@@ -664,12 +671,18 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
             for (int rb = 0; rb < RB; ++rb) z[rb][half][i] *= (float)x[i];
           }
         }
+        float odd = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) odd = fmaf(vt[j], 0.0f, odd);
+        pend_odd = __any(odd != odd);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) pend_seen[rb] = 0xffffffffu;
       }
-      pend_masked = holes || !((ts >= lo_max || ts + 32 <= a.sinks) && ts + 32 <= hi_min);
-      if (pend_masked) {
+      const bool masked = holes || !((ts >= lo_max || ts + 32 <= a.sinks) && ts + 32 <= hi_min);
+      if (masked) {
         uint32_t there = 0xffffffffu;
         if (holes) {  // a wave's rows are a byte, or half of one
-          const uint64_t gone = *(const uint64_t*)(lds + kGoneAt + at % (2 * S) * 8);
+          const uint64_t gone = *(const uint64_t*)(lds + kGoneAt + at % kTreeWords * 8);
           uint64_t rows = gone;
           if (kRows == 4) {
             rows = 0;
@@ -714,7 +727,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
         products();
       }
     }
-    if (kPipe && pend && (!kCross || step == 2 || k + step >= k1)) {
+    if (kPipe && pend && (step == 2 || k + step >= k1)) {
       f32x4 none[RB][2];
       advance(none, nullptr, std::false_type{}, std::true_type{});
       products();

@@ -14,7 +14,7 @@
 // a tile is read from memory once for all its rows, three are in flight while
 // one is multiplied, and one barrier stands between two.  Codes of an int8
 // cache go through a ring that is the wave's own and become fp16 on their way
-// to one of three tiles in LDS, once for all rows.
+// to tiles in LDS, once for all rows.
 //
 // Products as in the single-token kernel (paged_attention_impl.h): S^T = K Q^T
 // with the keys as A operand; O^T = V^T P^T with the probabilities in the
@@ -176,7 +176,9 @@ __device__ __forceinline__ uint32_t bits32(const uint64_t* mask, int words, int 
 
 constexpr int kTreeWaves = 8;
 constexpr int kTreeWords = 8;  // stages of the scales and the words
-constexpr int tree_stages(bool coded) { return coded ? 3 : 4; }
+constexpr int kTreeStages = 4;
+constexpr int tree_key_tiles(bool coded) { return coded ? 2 : kTreeStages; }
+constexpr int tree_value_tiles(bool coded) { return coded ? 3 : kTreeStages; }  // values are read a step later
 constexpr int tree_tile(int dp) { return dp == 256 ? 32 : 64; }
 constexpr int tree_rows(int dp) { return tree_tile(dp) / kTreeWaves; }  // of a tile, by each wave
 // LDS: the 16-bit tiles (keys, then values), the codes' ring and the scales' of
@@ -184,12 +186,12 @@ constexpr int tree_rows(int dp) { return tree_tile(dp) / kTreeWaves; }  // of a 
 // scales are read by all waves later), and of as many
 // for each stage a word (bits: rows whose page lies outside the cache), and
 // whether a wave saw such a page.
-constexpr int tree_tiles_lds(int dp, bool coded) { return tree_stages(coded) * 2 * tree_tile(dp) * dp * 2; }
+constexpr int tree_tiles_lds(int dp, bool coded) { return (tree_key_tiles(coded) + tree_value_tiles(coded)) * tree_tile(dp) * dp * 2; }
 constexpr int tree_raw_stage(int dp) { return 2 * tree_rows(dp) * dp; }    // of a wave
 constexpr int tree_scale_stage(int dp) { return 4 * tree_rows(dp); }
 constexpr int tree_lds(int dp, bool coded) {
   return tree_tiles_lds(dp, coded) +
-         (coded ? kTreeWaves * (tree_stages(true) * tree_raw_stage(dp) + kTreeWords * tree_scale_stage(dp)) : 0) + kTreeWords * 8 +
+         (coded ? kTreeWaves * (kTreeStages * tree_raw_stage(dp) + kTreeWords * tree_scale_stage(dp)) : 0) + kTreeWords * 8 +
          kTreeWaves * 4;
 }
 alignas(16) static __device__ const uint32_t kTreeZeros[4] = {0, 0, 0, 0};  // what is read in the place of tokens that are not there
@@ -221,7 +223,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   typedef typename M::T T;
   typedef typename M::V8 V8;
   typedef typename Mma<Q>::T QT;
-  constexpr int kTokens = tree_tile(DP), kSubs = kTokens / 32, kRows = tree_rows(DP), S = tree_stages(kCoded);
+  constexpr int kTokens = tree_tile(DP), kSubs = kTokens / 32, kRows = tree_rows(DP), S = kTreeStages;
   constexpr int kSteps = DP / 32, kBlocks = DP / 16;
   constexpr int kElem = kCoded ? 1 : 2;
   constexpr int kRowLanes = DP * kElem / 16, kAtOnce = 64 / kRowLanes;  // lanes on a row, rows of a load
@@ -229,7 +231,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   constexpr int kInFlight = 2 * kLoads + (kCoded ? 1 : 0);
   constexpr float kLift = lift_of(F);
   typedef Stage<DP * 2> St;
-  constexpr int kTileBytes = kTokens * DP * 2, kRaw = tree_raw_stage(DP);
+  constexpr int kKeyTiles = tree_key_tiles(kCoded), kValueTiles = tree_value_tiles(kCoded);
+  constexpr int kTileBytes = kTokens * DP * 2, kValuesAt = kKeyTiles * kTileBytes, kRaw = tree_raw_stage(DP);
   extern __shared__ __align__(1024) char lds[];
   constexpr int kScale = tree_scale_stage(DP);
   constexpr uint32_t kRawAt = tree_tiles_lds(DP, kCoded), kScaleAt = kRawAt + (kCoded ? S * kTreeWaves * kRaw : 0),
@@ -399,8 +402,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   auto issue = [&](int k) {
     const int t0 = tile_at(k) + wave * kRows, stage = k % S;
     const uint32_t to = kCoded ? kRawAt + (uint32_t)(stage * kTreeWaves + wave) * kRaw
-                               : (uint32_t)stage * 2 * kTileBytes + (uint32_t)wave * kRows * DP * 2;
-    constexpr uint32_t kValues = kCoded ? kRows * DP : kTileBytes;
+                               : (uint32_t)stage * kTileBytes + (uint32_t)wave * kRows * DP * 2;
+    constexpr uint32_t kValues = kCoded ? kRows * DP : kValuesAt;
     const uint32_t to_scales = kScaleAt + (uint32_t)(k % kTreeWords * kTreeWaves + wave) * kScale;
     uint32_t gone = 0;  // of this wave's rows
     if (plain && page < a.c.pages && t0 + kRows <= hi_all) {
@@ -449,7 +452,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
     }
     if (lane == 0) ((uint8_t*)(lds + kGoneAt))[k % kTreeWords * 8 + wave] = (uint8_t)gone;
   };
-  // INT8: this wave's rows of tile k become fp16 in tile k % S
+  // INT8: this wave's rows of tile k become fp16
   auto convert = [&](int k) {
     const char* const raw = lds + kRawAt + (uint32_t)((k % S) * kTreeWaves + wave) * kRaw;
 #pragma unroll
@@ -457,14 +460,15 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       if (kRows < kAtOnce && lrow >= kRows) break;
       const int r = wave * kRows + i * kAtOnce + lrow;
       const u32x4 k4 = *(const u32x4*)(raw + i * 1024 + lane * 16), v4 = *(const u32x4*)(raw + kRows * DP + i * 1024 + lane * 16);
-      char* const to = lds + k % S * 2 * kTileBytes + r * DP * 2;
+      char* const to = lds + k % kKeyTiles * kTileBytes + r * DP * 2;
+      char* const to_v = lds + kValuesAt + k % kValueTiles * kTileBytes + r * DP * 2;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int at = ((lplace * 2 + c) ^ St::key(r & 15)) << 4;
         const u32x2 x = codes_to_f16(k4[2 * c]), y = codes_to_f16(k4[2 * c + 1]);
         const u32x2 z = codes_to_f16(v4[2 * c]), w = codes_to_f16(v4[2 * c + 1]);
         *(u32x4*)(to + at) = u32x4{x.x, x.y, y.x, y.y};
-        *(u32x4*)(to + kTileBytes + at) = u32x4{z.x, z.y, w.x, w.y};
+        *(u32x4*)(to_v + at) = u32x4{z.x, z.y, w.x, w.y};
       }
     }
   };
@@ -563,7 +567,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
 #pragma unroll
           for (int rb = 0; rb < RB; ++rb) z[rb][half] = M::run(kv[half], qf[rb][i], z[rb][half]);
       }
-      if constexpr (kPipe) __builtin_amdgcn_sched_barrier(0);
+      if constexpr (SCORES && WEIGHTS) __builtin_amdgcn_sched_barrier(0);
     }
   };
   auto advance = [&](f32x4 (&z)[RB][2], const char* ks, auto with_scores, auto with_weights) {
@@ -644,7 +648,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       const int at = k + n / kSubs, sub = n % kSubs;
       const int ts = tile_at(at) + sub * 32;
       if (ts >= hi_all) break;
-      const char* const ks = lds + at % S * 2 * kTileBytes + sub * 32 * DP * 2;
+      const char* const ks = lds + at % kKeyTiles * kTileBytes + sub * 32 * DP * 2;
       asm volatile("" : "+v"(kread), "+v"(vread));  // the places made of them are not kept in registers
       f32x4 z[RB][2];
       if (kPipe && pend) {
@@ -653,7 +657,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       } else {
         advance(z, ks, std::true_type{}, std::false_type{});
       }
-      pend = ks + kTileBytes;
+      pend = lds + kValuesAt + at % kValueTiles * kTileBytes + sub * 32 * DP * 2;
       float lv[8];
       if constexpr (kCoded) {
         const char* const scales = lds + kScaleAt + (uint32_t)(at % kTreeWords) * kTreeWaves * kScale;  // of the first wave's rows

@@ -184,15 +184,15 @@ constexpr int tree_rows(int dp) { return tree_tile(dp) / kTreeWaves; }  // of a 
 // LDS: the 16-bit tiles (keys, then values), the codes' ring and the scales' of
 // more stages (a wave's codes have been read when they are converted, its
 // scales are read by all waves later), and of as many
-// for each stage a word (bits: rows whose page lies outside the cache), and
-// whether a wave saw such a page.
+// for each stage a word (bits: rows whose page lies outside the cache),
+// whether a wave saw such a page, and 32 rows of zeros.
 constexpr int tree_tiles_lds(int dp, bool coded) { return (tree_key_tiles(coded) + tree_value_tiles(coded)) * tree_tile(dp) * dp * 2; }
 constexpr int tree_raw_stage(int dp) { return 2 * tree_rows(dp) * dp; }    // of a wave
 constexpr int tree_scale_stage(int dp) { return 4 * tree_rows(dp); }
 constexpr int tree_lds(int dp, bool coded) {
   return tree_tiles_lds(dp, coded) +
          (coded ? kTreeWaves * (kTreeStages * tree_raw_stage(dp) + kTreeWords * tree_scale_stage(dp)) : 0) + kTreeWords * 8 +
-         kTreeWaves * 4;
+         kTreeWaves * 4 + (dp <= 128 ? 32 * dp * 2 : 0);
 }
 alignas(16) static __device__ const uint32_t kTreeZeros[4] = {0, 0, 0, 0};  // what is read in the place of tokens that are not there
 
@@ -214,17 +214,34 @@ __device__ __forceinline__ void tree_wait() {  // until at most N of this wave's
   asm volatile("" ::: "memory");
 }
 
+// One product: 16x16x32 or 32x32x16, by the accumulator.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ f32x4 tree_mma(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f32x4 tree_mma(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f32x16 tree_mma(bf16x8 a, bf16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f32x16 tree_mma(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+
 // Q: the queries' format; F: the cache's; DP: head_dim rounded up to 64, 128
-// or 256; RB: blocks of 16 rows per wave; PAIR: weights as two 16-bit numbers.
-template <int Q, int F, int DP, int RB, bool PAIR>
-__global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void tree_kernel(TreeArgs a) {
-  constexpr bool kCoded = F == ORBIT_KV_INT8;
+// or 256; R: rows of a wave, 16 or 32; PAIR: weights as two 16-bit numbers.
+//
+// The lanes.  G = 64 / R lanes hold a row; lane l is number g = l / R of row l
+// % R and holds, of 32 tokens' scores, tokens 4 G q + 4 g + i (i < 4), and of a
+// row's sums coordinates 4 G c + 4 g + i: what a 16x16x32 (R = 16, both halves
+// of the tokens) or a 32x32x16 product (R = 32) leaves.  32 rows to a wave take
+// half the instructions around a score that 16 do (two blocks of 16 rows in a
+// wave: 555 us for 4096 new of 8192 tokens).
+template <int Q, int F, int DP, int R, bool PAIR>
+__global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void tree_kernel(TreeArgs a) {
+  constexpr bool kCoded = F == ORBIT_KV_INT8, kWide = R == 32;
   typedef Mma<F> M;
   typedef typename M::T T;
   typedef typename M::V8 V8;
   typedef typename Mma<Q>::T QT;
+  constexpr int G = 64 / R, kStride = 4 * G;   // lanes of a row; tokens or coordinates between a lane's fours
+  constexpr int kQuads = 32 / kStride;         // fours of scores of a lane
   constexpr int kTokens = tree_tile(DP), kSubs = kTokens / 32, kRows = tree_rows(DP), S = kTreeStages;
-  constexpr int kSteps = DP / 32, kBlocks = DP / 16;
+  constexpr int kSteps = DP / (8 * G);         // coordinates of a product: 8 G
+  constexpr int kBlocks = DP / R;              // of a row's coordinates
   constexpr int kElem = kCoded ? 1 : 2;
   constexpr int kRowLanes = DP * kElem / 16, kAtOnce = 64 / kRowLanes;  // lanes on a row, rows of a load
   constexpr int kLoads = (kRows + kAtOnce - 1) / kAtOnce;               // of each tensor and tile; INT8: and one of scales
@@ -233,13 +250,14 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   typedef Stage<DP * 2> St;
   constexpr int kKeyTiles = tree_key_tiles(kCoded), kValueTiles = tree_value_tiles(kCoded);
   constexpr int kTileBytes = kTokens * DP * 2, kValuesAt = kKeyTiles * kTileBytes, kRaw = tree_raw_stage(DP);
-  extern __shared__ __align__(1024) char lds[];
   constexpr int kScale = tree_scale_stage(DP);
   constexpr uint32_t kRawAt = tree_tiles_lds(DP, kCoded), kScaleAt = kRawAt + (kCoded ? S * kTreeWaves * kRaw : 0),
-                     kGoneAt = kScaleAt + (kCoded ? kTreeWords * kTreeWaves * kScale : 0);
+                     kGoneAt = kScaleAt + (kCoded ? kTreeWords * kTreeWaves * kScale : 0),
+                     kZerosAt = kGoneAt + kTreeWords * 8 + kTreeWaves * 4;
+  extern __shared__ __align__(1024) char lds[];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r16 = lane & 15, lg = lane >> 4;
+  const int rl = lane & (R - 1), g = lane / R, r16 = lane & 15;
   const int dim = a.c.head_dim;
   // neighbouring workgroups take the key heads of one item
   const int item = (int)blockIdx.x / a.c.kv_heads, head = (int)blockIdx.x - item * a.c.kv_heads;
@@ -261,8 +279,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   if (row0 < 0 || row0 >= all_rows) return;
   const int rows_here = min(a.rows, all_rows - row0);
 
-  // the tiles of TILE tokens that any of the rows sees part of: those of the
-  // sinks, then those from the earliest window's first token on
+  // the tiles that any of the rows sees part of: those of the sinks, then
+  // those from the earliest window's first token on
   const int i_first = row0 / a.group, i_last = (row0 + rows_here - 1) / a.group;
   const int hi_all = a.words ? rq.len : max(rq.base + i_last + 1, 0);
   const int p_least = a.words ? rq.base - 1 : rq.base + i_first;
@@ -279,72 +297,63 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   // Waves on the rows, so many as these need, and on the tokens; where four
   // are on the tokens a step takes two tiles, otherwise one.
   int wrs = 1;
-  while (wrs * 16 * RB < rows_here) wrs *= 2;
+  while (wrs * R < rows_here) wrs *= 2;
   const int wt_all = min(kTreeWaves / wrs, 2 * kSubs), step = wt_all > kSubs ? 2 : 1;
   const int wr = wave & (wrs - 1), wt = wave / wrs;
-  const bool works = wt < wt_all && wr * 16 * RB < rows_here;
+  const bool works = wt < wt_all && wr * R < rows_here;
 
-  // this lane's rows
-  int lo[RB], hi[RB], token[RB];
-  int lo_max = 0, hi_min = 0x7fffffff;
-#pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    const int r = row0 + (wr * RB + rb) * 16 + r16;
-    const bool in = (wr * RB + rb) * 16 + r16 < rows_here;
-    const int i = (in ? r : row0) / a.group;
-    token[rb] = in ? rq.begin + i : -1;
-    int p = rq.base + i;
-    hi[rb] = p + 1;
+  // this lane's row: its token, its query head, the prefix tokens [lo, hi)
+  const bool row_in = wr * R + rl < rows_here;
+  const int row_at = row_in ? row0 + wr * R + rl : row0;
+  const int row_i = row_at / a.group;
+  const int token = rq.begin + row_i, qhead = head * a.group + row_at - row_i * a.group;
+  int lo = 0, hi = a.words ? rq.base : rq.base + row_i + 1;
+  if (a.window) {
+    int p = rq.base + row_i;
     if (a.words) {
-      hi[rb] = rq.base;
-      if (a.window) {
-        int seen = 0;
-        const uint64_t* const mask = a.tree + (long long)(rq.begin + i) * a.words;
-        for (int w = 0; w < a.words && w * 64 < rq.n; ++w) {
-          const int left = rq.n - w * 64;
-          seen += __popcll(left >= 64 ? mask[w] : mask[w] & ((1ull << left) - 1));
-        }
-        p = rq.base + seen - 1;
+      int seen = 0;
+      const uint64_t* const mask = a.tree + (long long)token * a.words;
+      for (int w = 0; w < a.words && w * 64 < rq.n; ++w) {
+        const int left = rq.n - w * 64;
+        seen += __popcll(left >= 64 ? mask[w] : mask[w] & ((1ull << left) - 1));
       }
+      p = rq.base + seen - 1;
     }
-    lo[rb] = a.window ? max(p - a.window + 1, 0) : 0;
-    if (in) {
-      lo_max = max(lo_max, lo[rb]);
-      hi_min = min(hi_min, hi[rb]);
-    }
+    lo = max(p - a.window + 1, 0);
   }
+  // all of the wave's rows see the tokens [lo_max, hi_min)
+  int lo_max = row_in ? lo : 0, hi_min = row_in ? hi : 0x7fffffff;
 #pragma unroll
-  for (int s = 1; s < 16; s *= 2) {
+  for (int s = 1; s < R; s *= 2) {
     lo_max = max(lo_max, __shfl_xor(lo_max, s));
     hi_min = min(hi_min, __shfl_xor(hi_min, s));
   }
   lo_max = __builtin_amdgcn_readfirstlane(lo_max);
   hi_min = __builtin_amdgcn_readfirstlane(hi_min);
 
-  auto head_of = [&](int rb) {
-    return token[rb] < 0 ? 0 : head * a.group + row0 + (wr * RB + rb) * 16 + r16 - (token[rb] - rq.begin) * a.group;
-  };
-
-  // the bits of the tokens among 32 from t0 on that this lane's row rb sees
-  auto seen32 = [&](int rb, int t0) {
-    uint32_t m = range32(lo[rb], hi[rb], t0);
-    if (a.window) m |= range32(0, min(a.sinks, hi[rb]), t0);
-    if (a.words && t0 + 32 > rq.base && token[rb] >= 0)
-      m |= bits32(a.tree + (long long)token[rb] * a.words, a.words, t0 - rq.base) & range32(max(rq.base, 0), rq.len, t0);
+  // the bits of the tokens among 32 from t0 on that this lane's row sees
+  auto seen32 = [&](int t0) {
+    uint32_t m = range32(lo, hi, t0);
+    if (a.window) m |= range32(0, min(a.sinks, hi), t0);
+    if (a.words && t0 + 32 > rq.base && row_in)
+      m |= bits32(a.tree + (long long)token * a.words, a.words, t0 - rq.base) & range32(max(rq.base, 0), rq.len, t0);
     return m;
   };
+  auto bit_of = [&](int j) { return j / 4 * kStride + g * 4 + j % 4; };  // of score j among the 32 tokens
+  // over the lanes of a row
+  auto row_max = [&](float v) { return max_rows32(kWide ? v : max_rows16(v)); };
+  auto row_add = [&](float v) { return add_rows32(kWide ? v : add_rows16(v)); };
 
   // queries as the B operand
-  V8 qf[RB][kSteps];
-  float zscale[RB];
-#pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    const QT* const qrow = (const QT*)a.q + (long long)max(token[rb], 0) * a.qts + head_of(rb) * a.qhs;
+  V8 qf[kSteps];
+  float zscale = fmaxf(fabsf(a.scale_log2e), 1.17549435e-38f);  // not 0: a hidden score is minus infinity
+  {
+    const QT* const qrow = (const QT*)a.q + (long long)token * a.qts + qhead * a.qhs;
     float f[kSteps][8], m = 0.0f;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const int d = s * 32 + lg * 8;
-      const bool in = token[rb] >= 0 && d < dim;
+      const int d = (s * G + g) * 8;
+      const bool in = row_in && d < dim;
       Vec8<QT> v;
       if (in) v = *(const Vec8<QT>*)(qrow + d);
 #pragma unroll
@@ -354,12 +363,11 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
         if (kCoded) m = fmaxf(m, fabsf(f[s][j]));
       }
     }
-    zscale[rb] = fmaxf(fabsf(a.scale_log2e), 1.17549435e-38f);  // not 0: a hidden score is minus infinity
     if (kCoded) {  // into fp16's range by a power of two per row
-      m = max_rows32(max_rows16(m));
+      m = row_max(m);
       const int e = m > 0.0f && m < __builtin_inff() ? __builtin_amdgcn_frexp_expf(m) : 0;
       const float down = ldexpf(1.0f, -e / 2), down2 = ldexpf(1.0f, -e - (-e / 2));
-      zscale[rb] = ldexpf(zscale[rb], e);
+      zscale = ldexpf(zscale, e);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
 #pragma unroll
@@ -368,8 +376,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) qf[rb][s][j] = (T)f[s][j];
-      asm volatile("" : "+v"(qf[rb][s]));  // or the unrounded values are kept too, for the sums below
+      for (int j = 0; j < 8; ++j) qf[s][j] = (T)f[s][j];
+      asm volatile("" : "+v"(qf[s]));  // or the unrounded values are kept too, for the sums below
     }
   }
 
@@ -485,134 +493,141 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
     asm volatile("" ::: "memory");
   };
 
-  f32x4 o[RB][kBlocks];
+  // The sums: o[c], coordinates kStride c + 4 g + i; relative to m_run.
+  typedef float f32xR __attribute__((ext_vector_type(kWide ? 16 : 4)));
   constexpr float kSlack = F == ORBIT_KV_BF16 ? 8.0f : 0.0f;
-  float m_run[RB], l_run[RB];  // l: this lane's tokens alone
+  f32xR o[kBlocks];
+  float m_run = -__builtin_inff(), l_run = 0.0f;  // l: this lane's tokens alone
+  constexpr int kOf = kWide ? 16 : 4;  // sums of a block in a lane
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    m_run[rb] = -__builtin_inff();
-    l_run[rb] = 0.0f;
+  for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
-    for (int d = 0; d < kBlocks; ++d) o[rb][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-  int kread = r16 * DP * 2 + ((lg ^ St::key(r16)) << 4);
-  const int trow = lg * 4 + (r16 >> 2);
-  int vread = trow * DP * 2 + ((((r16 & 3) >> 1) ^ St::key(trow)) << 4) + (r16 & 1) * 8;
+    for (int i = 0; i < kOf; ++i) o[d][i] = 0.0f;
+  // where this lane reads its first operands
+  int kread = rl * DP * 2 + ((g ^ St::key(rl & 15)) << 4);
+  const int trow = g * 4 + (r16 >> 2), tunit = (kWide ? ((lane >> 4) & 1) * 2 : 0) + ((r16 & 3) >> 1);
+  int vread = trow * DP * 2 + ((tunit ^ St::key(trow)) << 4) + (r16 & 1) * 8;
 
-  // With two blocks of rows (kPipe) the scores of 32 tokens are computed beside
-  // the weights of the 32 before them, whose products come next, so that a
-  // wave's matrix and vector instructions overlap; also over a step's
-  // end where it has one tile: those values are read behind the next barrier, so the stage
-  // after next is filled and not the next.
-  constexpr bool kPipe = RB == 2;
-  f32x4 s[RB][2];
-  float vt[8];  // INT8: the values' scales
-  const char* pend = nullptr;
+  // With 32 rows (kWide) the scores of 32 tokens are computed beside the
+  // weights of the 32 before them, whose products come next, so that a wave's
+  // matrix and vector instructions overlap; also over a step's end where it has
+  // one tile: those values are read behind the next barrier, so the stage after
+  // next is filled and not the next.
+  constexpr int kScores = 4 * kQuads;  // of a lane
+  float s[kScores];
+  float vt[kCoded ? kScores : 1];  // INT8: the values' scales
+  const char* pend;  // their values
   bool pend_odd = false;  // INT8: some of the values' scales are infinite or NaN
-  uint32_t pend_seen[kCoded ? RB : 1];
+  uint32_t pend_seen = 0;
 
-  V8 ph[RB], pl[PAIR ? RB : 1];
+  V8 ph[kScores / 8], pl[PAIR ? kScores / 8 : 1];
   // Scores of 32 tokens (SCORES), and weights of the pending ones (WEIGHTS), a
   // part of both at a time: the weights' instructions stand between the keys'
   // reads and their products.
   // CHECKED: values' scales of hidden tokens may be infinite or NaN.
-  auto advance_as = [&](f32x4 (&z)[RB][2], const char* ks, auto with_scores, auto with_weights, auto checked) {
+  auto advance_as = [&](float (&z)[kScores], const char* ks, auto with_scores, auto with_weights, auto checked) {
     constexpr bool SCORES = decltype(with_scores)::value, WEIGHTS = decltype(with_weights)::value, CHECKED = decltype(checked)::value;
-    constexpr int kPart = 8 / kSteps < 1 ? 1 : 8 / kSteps;  // weights of a row in a part
-    float m_use[RB];
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) m_use[rb] = m_run[rb] == -__builtin_inff() ? 0.0f : m_run[rb] - kLift;
+    constexpr int kPairs2 = kScores / 2;  // weights, two by two
+    const float m_use = m_run == -__builtin_inff() ? 0.0f : m_run - kLift;
+    f32xR acc[kWide ? 1 : 2];
     if constexpr (SCORES) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+      for (int h = 0; h < (kWide ? 1 : 2); ++h)
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) z[rb][half] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < kOf; ++i) acc[h][i] = 0.0f;
+    }
+    constexpr int kAheadK = kWide ? 3 : 1;  // keys are read so many parts ahead
+    V8 kv[kAheadK + 1][kWide ? 1 : 2];
+    auto read_keys = [&](int i) {
+#pragma unroll
+      for (int h = 0; h < (kWide ? 1 : 2); ++h)
+        kv[i % (kAheadK + 1)][h] = __builtin_bit_cast(V8, *(const u32x4*)(ks + h * 16 * DP * 2 + (kread ^ (i * G << 4))));
+    };
+    if constexpr (SCORES) {
+#pragma unroll
+      for (int i = 0; i < kAheadK && i < kSteps; ++i) read_keys(i);
     }
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      V8 kv[2];
       if constexpr (SCORES) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-          kv[half] = __builtin_bit_cast(V8, *(const u32x4*)(ks + half * 16 * DP * 2 + (kread ^ (i << 6))));
+        if (i + kAheadK < kSteps) read_keys(i + kAheadK);
       }
       if constexpr (WEIGHTS) {
-        if (i * kPart < 8) {
 #pragma unroll
-          for (int rb = 0; rb < RB; ++rb)
+        for (int x = kPairs2 * i / kSteps; x < kPairs2 * (i + 1) / kSteps; ++x) {
+          const int j = 2 * x;
+          float p[2];
 #pragma unroll
-            for (int j0 = 0; j0 < (kPart < 2 ? (i & 1 ? 0 : 2) : kPart); j0 += 2) {
-              const int j = i * kPart + j0;
-              float p[2];
+          for (int y = 0; y < 2; ++y) p[y] = __builtin_amdgcn_exp2f(fmaf(s[j + y], zscale, -m_use));
+          l_run += p[0] + p[1];
+          if constexpr (kCoded) {
 #pragma unroll
-              for (int x = 0; x < 2; ++x) p[x] = __builtin_amdgcn_exp2f(fmaf(s[rb][j >> 2][(j & 3) + x], zscale[rb], -m_use[rb]));
-              l_run[rb] += p[0] + p[1];
-              if constexpr (kCoded) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                  p[x] = !CHECKED || (pend_seen[rb] >> ((j >> 2) * 16 + lg * 4 + (j & 3) + x)) & 1u ? p[x] * vt[j + x] : 0.0f;
-              }
-              if constexpr (PAIR) {
-                split2(p[0], p[1], ph[rb], pl[rb], j);
-              } else {
-                ph[rb][j] = (T)p[0];
-                ph[rb][j + 1] = (T)p[1];
-              }
-            }
+            for (int y = 0; y < 2; ++y) p[y] = !CHECKED || (pend_seen >> bit_of(j + y)) & 1u ? p[y] * vt[j + y] : 0.0f;
+          }
+          if constexpr (PAIR) {
+            split2(p[0], p[1], ph[j / 8], pl[j / 8], j % 8);
+          } else {
+            ph[j / 8][j % 8] = (T)p[0];
+            ph[j / 8][j % 8 + 1] = (T)p[1];
+          }
         }
       }
       if constexpr (SCORES) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) z[rb][half] = M::run(kv[half], qf[rb][i], z[rb][half]);
+        for (int h = 0; h < (kWide ? 1 : 2); ++h) acc[h] = tree_mma(kv[i % (kAheadK + 1)][h], qf[i], acc[h]);
       }
       if constexpr (SCORES && WEIGHTS) __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (SCORES) {
+#pragma unroll
+      for (int j = 0; j < kScores; ++j) z[j] = acc[kWide ? 0 : j / 4][kWide ? j : j % 4];
+    }
   };
-  auto advance = [&](f32x4 (&z)[RB][2], const char* ks, auto with_scores, auto with_weights) {
+  auto advance = [&](float (&z)[kScores], const char* ks, auto with_scores, auto with_weights) {
     if (kCoded && decltype(with_weights)::value && pend_odd) advance_as(z, ks, with_scores, with_weights, std::true_type{});
     else advance_as(z, ks, with_scores, with_weights, std::false_type{});
   };
-  // The pending tokens' weights with their values; two blocks of coordinates
-  // are read ahead.
+  // The pending tokens' weights with their values, by blocks of R coordinates
+  // (and 16 tokens: kWide); some products' operands are read ahead.
   auto products = [&] {
     typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+    constexpr int kAll = kBlocks * (kWide ? 2 : 1);
+    // rows 8 (kWide) or 16 further: this far, with the units' places exchanged
+    constexpr int kFar = kWide ? 8 : 16, kOther = kWide ? (DP == 64 ? 4 : 8) : 0;
+    constexpr int kAheadV = kWide ? 4 : 2;
     union Block {
       s16x4 h[2];
       V8 v;
-    } u[2][2];
-    auto read = [&](int d) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const char* const at = pend + (vread ^ ((d + x) << 5));
-        u[(d >> 1) & 1][x].h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)at);
-        u[(d >> 1) & 1][x].h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 16 * DP * 2));
-      }
+    } u[kAheadV + 1];
+    auto read = [&](int n) {
+      const int d = kWide ? n >> 1 : n, m = kWide ? n & 1 : 0;
+      const int at = vread ^ (d * (R / 8) << 4);
+      u[n % (kAheadV + 1)].h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(pend + m * 16 * DP * 2 + at));
+      u[n % (kAheadV + 1)].h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(pend + (m * 16 + kFar) * DP * 2 + (at ^ (kOther << 4))));
     };
-    read(0);
 #pragma unroll
-    for (int d = 0; d < kBlocks; d += 2) {
-      if (d + 2 < kBlocks) read(d + 2);
+    for (int n = 0; n < kAheadV && n < kAll; ++n) read(n);
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          o[rb][d + x] = M::run(u[(d >> 1) & 1][x].v, ph[rb], o[rb][d + x]);
-          if constexpr (PAIR) o[rb][d + x] = M::run(u[(d >> 1) & 1][x].v, pl[rb], o[rb][d + x]);
-        }
-      __builtin_amdgcn_sched_barrier(0);
+    for (int n = 0; n < kAll; ++n) {
+      if (n + kAheadV < kAll) read(n + kAheadV);
+      const int d = kWide ? n >> 1 : n, m = kWide ? n & 1 : 0;
+      o[d] = tree_mma(u[n % (kAheadV + 1)].v, ph[m], o[d]);
+      if constexpr (PAIR) o[d] = tree_mma(u[n % (kAheadV + 1)].v, pl[m], o[d]);
+      if (kWide || n % 2) __builtin_amdgcn_sched_barrier(0);
     }
   };
 
   // Tiles in flight beside a step's: codes' places are free once converted;
-  // others' when the next barrier says so (kPipe: the next but one).
-  const int ahead = kCoded ? S : step == 2 || kPipe ? 2 : S - 1;
+  // others' when the next barrier says so (kWide: the next but one).
+  const int ahead = kCoded ? S : step == 2 || kWide ? 2 : S - 1;
   look_up(k0);
 #pragma unroll 1
   for (int x = k0; x < min(k0 + ahead, k1); ++x) {
     issue(x);
     look_up(x + 1);
+  }
+  if constexpr (kWide) {
+    for (int x = tid; x < 32 * DP * 2 / 16; x += 64 * kTreeWaves) *(u32x4*)(lds + kZerosAt + x * 16) = u32x4{0u, 0u, 0u, 0u};
   }
   // whether any page of the piece lies outside the cache
   bool bad = false;
@@ -625,9 +640,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
   meet();
   const u32x4 bad0 = *(const u32x4*)(lds + kGoneAt + kTreeWords * 8), bad1 = *(const u32x4*)(lds + kGoneAt + kTreeWords * 8 + 16);
   const bool holes = __builtin_amdgcn_readfirstlane(bad0.x | bad0.y | bad0.z | bad0.w | bad1.x | bad1.y | bad1.z | bad1.w) != 0;
-#pragma unroll 1
-  for (int k = k0; k < k1; k += step) {
-    const int here = min(step, k1 - k);  // tiles of this step
+  // A step's tiles, there and ready to be read by all waves.
+  auto begin_step = [&](int k, int here) {
     landed(min(k1, k + ahead) - k - here);
     if constexpr (kCoded) {
       // two tiles take a place that the step before had: it must have been read
@@ -636,236 +650,252 @@ __global__ __launch_bounds__(64 * kTreeWaves, RB == 1 && DP == 64 ? 4 : 2) void 
       if (here == 2) convert(k + 1);
       tree_wait<62>();
     }
-    meet();  // the tiles are there, and those of the step before (kPipe: the one before that) have been read
+    meet();  // the tiles are there, and those of the step before (kWide: the one before that) have been read
 #pragma unroll 1
     for (int x = k + ahead; x < min(k + ahead + step, k1); ++x) {  // into their stages
       issue(x);
       look_up(x + 1);
     }
-    if (!works) continue;
+    asm volatile("" : "+v"(kread), "+v"(vread));  // the places made of them are not kept in registers
+  };
+  // Scores z of the 32 tokens from ts on (part `sub` of tile `at`) become s:
+  // scaled, masked, the maximum carried on.
+  auto take = [&](float (&z)[kScores], int at, int sub, int ts) {
+    float lv[kCoded ? kScores : 1];
+    if constexpr (kCoded) {
+      const char* const scales = lds + kScaleAt + (uint32_t)(at % kTreeWords) * kTreeWaves * kScale;  // of the first wave's rows
+      float odd = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) {
+        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+        const int t = sub * 32 + q * kStride + g * 4;
+        const char* const from = scales + t / kRows * kScale + t % kRows * 2;
+        const h4 x = *(const h4*)from, y = *(const h4*)(from + 2 * kRows);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vt[q * 4 + i] = (float)y[i];
+          lv[q * 4 + i] = __builtin_amdgcn_logf(fmaxf((float)y[i], 5.9604645e-8f));
+          z[q * 4 + i] *= (float)x[i];
+          odd = fmaf((float)y[i], 0.0f, odd);
+        }
+      }
+      pend_odd = __any(odd != odd);
+      pend_seen = 0xffffffffu;
+    }
+    if (holes || !((ts >= lo_max || ts + 32 <= a.sinks) && ts + 32 <= hi_min)) {
+      uint32_t seen = seen32(ts);
+      if (holes) {  // a wave's rows are a byte, or half of one
+        uint64_t rows = *(const uint64_t*)(lds + kGoneAt + at % kTreeWords * 8);
+        if (kRows == 4) {
+          const uint64_t gone = rows;
+          rows = 0;
+#pragma unroll
+          for (int w = 0; w < 8; ++w) rows |= ((gone >> (8 * w)) & 15u) << (4 * w);
+        }
+        seen &= ~(uint32_t)(rows >> (sub * 32));
+      }
+      pend_seen = seen;
+#pragma unroll
+      for (int j = 0; j < kScores; ++j) z[j] = (seen >> bit_of(j)) & 1u ? z[j] : -__builtin_inff();
+    }
+    float mt = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < kScores; ++j) {
+      if constexpr (kCoded) mt = fmaxf(mt, fmaf(z[j], zscale, lv[j]));
+      else mt = fmaxf(mt, z[j]);
+    }
+    if constexpr (!kCoded) mt *= zscale;
+    mt = row_max(mt);
+    // with float32's range for the weights (bfloat16) a larger score by less
+    // than 2^8 may stay: the sums are relative to m_run either way
+    if (__any(mt > m_run + kSlack)) {
+      const float m_new = fmaxf(m_run, mt);
+      const float alpha = factor(m_run - (m_new == -__builtin_inff() ? 0.0f : m_new));
+      m_run = m_new;
+      l_run *= alpha;
+#pragma unroll
+      for (int d = 0; d < kBlocks; ++d) o[d] *= alpha;
+    }
+#pragma unroll
+    for (int j = 0; j < kScores; ++j) s[j] = z[j];
+  };
+  auto keys_of = [&](int at, int sub) { return lds + at % kKeyTiles * kTileBytes + sub * 32 * DP * 2; };
+  auto values_of = [&](int at, int sub) { return lds + kValuesAt + at % kValueTiles * kTileBytes + sub * 32 * DP * 2; };
+  if (kWide && step == 1) {
+    // nothing is pending: zeros
+#pragma unroll
+    for (int j = 0; j < kScores; ++j) {
+      s[j] = -__builtin_inff();
+      if constexpr (kCoded) vt[j] = 0.0f;
+    }
+    pend = lds + kZerosAt;
 #pragma unroll 1
-    for (int n = wt; n < here * kSubs; n += wt_all) {
-      const int at = k + n / kSubs, sub = n % kSubs;
-      const int ts = tile_at(at) + sub * 32;
-      if (ts >= hi_all) break;
-      const char* const ks = lds + at % kKeyTiles * kTileBytes + sub * 32 * DP * 2;
-      asm volatile("" : "+v"(kread), "+v"(vread));  // the places made of them are not kept in registers
-      f32x4 z[RB][2];
-      if (kPipe && pend) {
-        advance(z, ks, std::true_type{}, std::true_type{});
+    for (int k = k0; k < k1; ++k) {
+      begin_step(k, 1);
+      const int n1 = works ? kSubs : 0;
+#pragma unroll 1
+      for (int sub = wt; sub < n1; sub += wt_all) {
+        const int ts = tile_at(k) + sub * 32;
+        if (ts >= hi_all) break;
+        float z[kScores];
+        advance(z, keys_of(k, sub), std::true_type{}, std::true_type{});
         products();
-      } else {
-        advance(z, ks, std::true_type{}, std::false_type{});
-      }
-      pend = lds + kValuesAt + at % kValueTiles * kTileBytes + sub * 32 * DP * 2;
-      float lv[8];
-      if constexpr (kCoded) {
-        const char* const scales = lds + kScaleAt + (uint32_t)(at % kTreeWords) * kTreeWaves * kScale;  // of the first wave's rows
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-          const int t = sub * 32 + half * 16 + lg * 4;
-          const char* const from = scales + t / kRows * kScale + t % kRows * 2;
-          const h4 x = *(const h4*)from, y = *(const h4*)(from + 2 * kRows);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            vt[half * 4 + i] = (float)y[i];
-            lv[half * 4 + i] = __builtin_amdgcn_logf(fmaxf((float)y[i], 5.9604645e-8f));
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) z[rb][half][i] *= (float)x[i];
-          }
-        }
-        float odd = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) odd = fmaf(vt[j], 0.0f, odd);
-        pend_odd = __any(odd != odd);
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) pend_seen[rb] = 0xffffffffu;
-      }
-      const bool masked = holes || !((ts >= lo_max || ts + 32 <= a.sinks) && ts + 32 <= hi_min);
-      if (masked) {
-        uint32_t there = 0xffffffffu;
-        if (holes) {  // a wave's rows are a byte, or half of one
-          const uint64_t gone = *(const uint64_t*)(lds + kGoneAt + at % kTreeWords * 8);
-          uint64_t rows = gone;
-          if (kRows == 4) {
-            rows = 0;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) rows |= ((gone >> (8 * w)) & 15u) << (4 * w);
-          }
-          there = ~(uint32_t)(rows >> (sub * 32));
-        }
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          const uint32_t seen = seen32(rb, ts) & there;
-          if constexpr (kCoded) pend_seen[rb] = seen;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) z[rb][j >> 2][j & 3] = (seen >> ((j >> 2) * 16 + lg * 4 + (j & 3))) & 1u ? z[rb][j >> 2][j & 3] : -__builtin_inff();
-        }
-      }
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        float mt = -__builtin_inff();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if constexpr (kCoded) mt = fmaxf(mt, fmaf(z[rb][j >> 2][j & 3], zscale[rb], lv[j]));
-          else mt = fmaxf(mt, z[rb][j >> 2][j & 3]);
-        }
-        if constexpr (!kCoded) mt *= zscale[rb];
-        mt = max_rows32(max_rows16(mt));
-        // with float32's range for the weights (bfloat16) a larger score by
-        // less than 2^8 may stay: the sums are relative to m_run either way
-        if (__any(mt > m_run[rb] + kSlack)) {
-          const float m_new = fmaxf(m_run[rb], mt);
-          const float alpha = factor(m_run[rb] - (m_new == -__builtin_inff() ? 0.0f : m_new));
-          m_run[rb] = m_new;
-          l_run[rb] *= alpha;
-#pragma unroll
-          for (int d = 0; d < kBlocks; ++d) o[rb][d] *= alpha;
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) s[rb][half] = z[rb][half];
-      }
-      if constexpr (!kPipe) {
-        advance(z, ks, std::false_type{}, std::true_type{});
-        products();
+        pend = values_of(k, sub);
+        take(z, k, sub, ts);
       }
     }
-    if (kPipe && pend && (step == 2 || k + step >= k1)) {
-      f32x4 none[RB][2];
+    if (works) {
+      float none[kScores];
       advance(none, nullptr, std::false_type{}, std::true_type{});
       products();
-      pend = nullptr;
     }
-  }
-  if constexpr (!kCoded) {
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      f32x4 all = o[rb][0];
-#pragma unroll
-      for (int d = 1; d < kBlocks; ++d) all += o[rb][d];
-      const float one = (all[0] + all[1]) + (all[2] + all[3]);
-      if (works && __any(one != one)) {  // a NaN, or infinities of both signs
-        uint64_t lost = 0;               // bit 4 d + i: sum i of block d is NaN
-#pragma unroll
-        for (int d = 0; d < kBlocks; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            lost |= (uint64_t)(o[rb][d][i] != o[rb][d][i]) << (4 * d + i);
-            o[rb][d][i] = o[rb][d][i] != o[rb][d][i] ? 0.0f : o[rb][d][i];
-          }
-        const float m_use = m_run[rb] == -__builtin_inff() ? 0.0f : m_run[rb];
+  } else {
 #pragma unroll 1
-        for (int k = k0; k < k1; k += step)
+    for (int k = k0; k < k1; k += step) {
+      const int here = min(step, k1 - k);  // tiles of this step
+      begin_step(k, here);
+      const int n1 = works ? here * kSubs : 0;
 #pragma unroll 1
-          for (int n = wt; n < min(step, k1 - k) * kSubs; n += wt_all)
-#pragma unroll 1
-            for (int x = 0; x < 32; ++x) {
-              const int t = tile_at(k + n / kSubs) + n % kSubs * 32 + x;
-              if (t >= hi_all) break;
-              const uint32_t pg = (uint32_t)table[t >> a.c.page_shift];
-              if (pg >= a.c.pages) continue;
-              const long long at = cache_row(a.c, pg, head, (uint32_t)t & a.c.page_mask) * dim;
-              float z = 0.0f;
-#pragma unroll
-              for (int s = 0; s < kSteps; ++s) {
-                if (s * 32 + lg * 8 >= dim) continue;
-                const Vec8<T> kv = *(const Vec8<T>*)((const T*)a.c.k + at + s * 32 + lg * 8);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z = fmaf((float)qf[rb][s][j], (float)kv.e[j], z);
-              }
-              z = add_rows32(add_rows16(z)) * zscale[rb];
-              const bool seen = (seen32(rb, t & ~31) >> (t & 31)) & 1u;
-              if (!seen || z == -__builtin_inff()) continue;
-              const float p = __builtin_amdgcn_exp2f(z - m_use + kLift), w = p < 1.17549435e-38f ? 1.17549435e-38f : p;
-#pragma unroll
-              for (int d = 0; d < kBlocks; ++d) {
-                if (d * 16 + lg * 4 >= dim) continue;
-                T v[4];
-                __builtin_memcpy(v, (const T*)a.c.v + at + d * 16 + lg * 4, sizeof v);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float f = (float)v[i];
-                  o[rb][d][i] = (lost >> (4 * d + i)) & 1u ? fmaf(fabsf(f) < __builtin_inff() ? p : w, f, o[rb][d][i]) : o[rb][d][i];
-                }
-              }
-            }
+      for (int n = wt; n < n1; n += wt_all) {
+        const int at = k + n / kSubs, sub = n % kSubs, ts = tile_at(at) + sub * 32;
+        if (ts >= hi_all) break;
+        float z[kScores];
+        advance(z, keys_of(at, sub), std::true_type{}, std::false_type{});
+        take(z, at, sub, ts);
+        pend = values_of(at, sub);
+        advance(z, nullptr, std::false_type{}, std::true_type{});
+        products();
       }
     }
   }
 
-  // The sums of the waves on the same rows meet in LDS, one block of rows
-  // after the other; from here on the maximum stands for the lifted one.
-  float* const so = (float*)lds;  // [wave with wt > 0][16][DP], then its maxima and sums
-  float* const sm = so + (wt_all - 1) * wrs * 16 * DP;
-  const int mine = (wt - 1) * wrs + wr;
+  if constexpr (!kCoded) {
+    float one = 0.0f;
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    l_run[rb] = add_rows32(add_rows16(l_run[rb]));
-    m_run[rb] -= kLift;
-    if (wt_all > 1) {
-      __syncthreads();
-      if (wt > 0 && wt < wt_all) {
+    for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
-        for (int d = 0; d < kBlocks; ++d) *(f32x4*)(so + (mine * 16 + r16) * DP + d * 16 + lg * 4) = o[rb][d];
-        if (lg == 0) {
-          sm[(mine * 16 + r16) * 2] = m_run[rb];
-          sm[(mine * 16 + r16) * 2 + 1] = l_run[rb];
-        }
-      }
-      __syncthreads();
-      if (wt == 0) {
-        float m = m_run[rb];
-        for (int w = 1; w < wt_all; ++w) m = fmaxf(m, sm[(((w - 1) * wrs + wr) * 16 + r16) * 2]);
-        const float m_use = m == -__builtin_inff() ? 0.0f : m;
-        const float e0 = factor(m_run[rb] - m_use);
-        float l = l_run[rb] * e0;
-#pragma unroll
-        for (int d = 0; d < kBlocks; ++d) o[rb][d] *= e0;
-        for (int w = 1; w < wt_all; ++w) {
-          const int from = ((w - 1) * wrs + wr) * 16 + r16;
-          const float e = factor(sm[from * 2] - m_use);
-          l = fmaf(e, sm[from * 2 + 1], l);
-#pragma unroll
-          for (int d = 0; d < kBlocks; ++d) {
-            const f32x4 x = *(const f32x4*)(so + from * DP + d * 16 + lg * 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[rb][d][i] = fmaf(e, x[i], o[rb][d][i]);
-          }
-        }
-        m_run[rb] = m;
-        l_run[rb] = l;
-      }
-    }
-    if (wt != 0 || token[rb] < 0) continue;
-    const long long row = (long long)token[rb] * a.q_heads + head_of(rb);
-    const float l = l_run[rb];
-    if (last) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-      for (int d = 0; d < kBlocks; ++d) {
-        if (d * 16 + lg * 4 >= dim) continue;
-        struct alignas(8) {
-          QT e[4];
-        } v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v.e[i] = (QT)(l == 0.0f ? 0.0f : o[rb][d][i] * inv);
-        *(decltype(v)*)((QT*)a.out + row * dim + d * 16 + lg * 4) = v;
-      }
-      if (lg == 0) {
-        if (a.lse) a.lse[row] = (m_run[rb] + __builtin_amdgcn_logf(l)) * 0.69314718056f;
-        if (a.pieces > 1) ((int*)(a.part + a.part_n))[row] = 0;
-      }
-    } else {
-      const long long at = row * a.pieces + it.piece;
+      for (int i = 0; i < kOf; ++i) one += o[d][i];
+    if (works && __any(one != one)) {  // a NaN, or infinities of both signs
+      uint64_t lost = 0;               // bit kOf d + i: that sum is NaN
 #pragma unroll
       for (int d = 0; d < kBlocks; ++d)
-        if (d * 16 + lg * 4 < dim) *(f32x4*)(a.part + at * dim + d * 16 + lg * 4) = o[rb][d];
-      if (lg == 0) {
-        *(float2*)(a.part + a.part_ml + at * 2) = make_float2(m_run[rb], l);
-        if (it.piece == 0) ((int*)(a.part + a.part_n))[row] = used;
+#pragma unroll
+        for (int i = 0; i < kOf; ++i) {
+          lost |= (uint64_t)(o[d][i] != o[d][i]) << (kOf * d + i);
+          o[d][i] = o[d][i] != o[d][i] ? 0.0f : o[d][i];
+        }
+      const float m_use = m_run == -__builtin_inff() ? 0.0f : m_run;
+#pragma unroll 1
+      for (int k = k0; k < k1; k += step)
+#pragma unroll 1
+        for (int n = wt; n < min(step, k1 - k) * kSubs; n += wt_all)
+#pragma unroll 1
+          for (int x = 0; x < 32; ++x) {
+            const int t = tile_at(k + n / kSubs) + n % kSubs * 32 + x;
+            if (t >= hi_all) break;
+            const uint32_t pg = (uint32_t)table[t >> a.c.page_shift];
+            if (pg >= a.c.pages) continue;
+            const long long at = cache_row(a.c, pg, head, (uint32_t)t & a.c.page_mask) * dim;
+            float z = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+              const int e = (s * G + g) * 8;
+              if (e >= dim) continue;
+              const Vec8<T> kv = *(const Vec8<T>*)((const T*)a.c.k + at + e);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) z = fmaf((float)qf[s][j], (float)kv.e[j], z);
+            }
+            z = row_add(z) * zscale;
+            const bool seen = (seen32(t & ~31) >> (t & 31)) & 1u;
+            if (!seen || z == -__builtin_inff()) continue;
+            const float p = __builtin_amdgcn_exp2f(z - m_use + kLift), w = p < 1.17549435e-38f ? 1.17549435e-38f : p;
+#pragma unroll
+            for (int c = 0; c < DP / kStride; ++c) {
+              const int e = c * kStride + g * 4;
+              if (e >= dim) continue;
+              T v[4];
+              __builtin_memcpy(v, (const T*)a.c.v + at + e, sizeof v);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float f = (float)v[i];
+                const int d = c * 4 / kOf, y = c * 4 % kOf + i;
+                o[d][y] = (lost >> (kOf * d + y)) & 1u ? fmaf(fabsf(f) < __builtin_inff() ? p : w, f, o[d][y]) : o[d][y];
+              }
+            }
+          }
+    }
+  }
+
+  // The sums of the waves on the same rows meet in LDS; from here on the
+  // maximum stands for the lifted one.
+  float* const so = (float*)lds;  // [wave with wt > 0][R][DP], then its maxima and sums
+  float* const sm = so + (wt_all - 1) * wrs * R * DP;
+  l_run = row_add(l_run);
+  m_run -= kLift;
+  if (wt_all > 1) {
+    __syncthreads();
+    const int mine = ((wt - 1) * wrs + wr) * R + rl;
+    if (wt > 0 && wt < wt_all) {
+#pragma unroll
+      for (int c = 0; c < DP / kStride; ++c) {
+        const int d = c * 4 / kOf, y = c * 4 % kOf;
+        *(f32x4*)(so + mine * DP + c * kStride + g * 4) = f32x4{o[d][y], o[d][y + 1], o[d][y + 2], o[d][y + 3]};
+      }
+      if (g == 0) {
+        sm[mine * 2] = m_run;
+        sm[mine * 2 + 1] = l_run;
       }
     }
+    __syncthreads();
+    if (wt == 0) {
+      float m = m_run;
+      for (int w = 1; w < wt_all; ++w) m = fmaxf(m, sm[(((w - 1) * wrs + wr) * R + rl) * 2]);
+      const float m_use = m == -__builtin_inff() ? 0.0f : m;
+      const float e0 = factor(m_run - m_use);
+      l_run *= e0;
+#pragma unroll
+      for (int d = 0; d < kBlocks; ++d) o[d] *= e0;
+      for (int w = 1; w < wt_all; ++w) {
+        const int from = ((w - 1) * wrs + wr) * R + rl;
+        const float e = factor(sm[from * 2] - m_use);
+        l_run = fmaf(e, sm[from * 2 + 1], l_run);
+#pragma unroll
+        for (int c = 0; c < DP / kStride; ++c) {
+          const f32x4 x = *(const f32x4*)(so + from * DP + c * kStride + g * 4);
+          const int d = c * 4 / kOf, y = c * 4 % kOf;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[d][y + i] = fmaf(e, x[i], o[d][y + i]);
+        }
+      }
+      m_run = m;
+    }
+  }
+  if (wt != 0 || !row_in) return;
+  const long long row = (long long)token * a.q_heads + qhead;
+  const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+  const long long part = row * a.pieces + it.piece;
+#pragma unroll
+  for (int c = 0; c < DP / kStride; ++c) {
+    const int e = c * kStride + g * 4, d = c * 4 / kOf, y = c * 4 % kOf;
+    if (e >= dim) continue;
+    if (last) {
+      struct alignas(8) {
+        QT e[4];
+      } v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v.e[i] = (QT)(l_run == 0.0f ? 0.0f : o[d][y + i] * inv);
+      *(decltype(v)*)((QT*)a.out + row * dim + e) = v;
+    } else {
+      *(f32x4*)(a.part + part * dim + e) = f32x4{o[d][y], o[d][y + 1], o[d][y + 2], o[d][y + 3]};
+    }
+  }
+  if (g == 0) {
+    if (last) {
+      if (a.lse) a.lse[row] = (m_run + __builtin_amdgcn_logf(l_run)) * 0.69314718056f;
+    } else {
+      *(float2*)(a.part + a.part_ml + part * 2) = make_float2(m_run, l_run);
+    }
+    if (a.pieces > 1 && it.piece == 0) ((int*)(a.part + a.part_n))[row] = last ? 0 : used;
   }
 }
 
@@ -912,27 +942,27 @@ __global__ __launch_bounds__(64) void tree_join_kernel(TreeArgs a) {
 template <int Q, int F>
 hipError_t launch_tree(const TreeArgs& a, bool few, dim3 grid, hipStream_t stream) {
   const int dim = a.c.head_dim;
-  auto go = [&](auto dp, auto blocks, auto pair) {
+  auto go = [&](auto dp, auto rows, auto pair) {
     constexpr int DP = decltype(dp)::value, kLds = tree_lds(DP, F == ORBIT_KV_INT8);
-    auto kern = tree_kernel<Q, F, DP, decltype(blocks)::value, decltype(pair)::value>;
+    auto kern = tree_kernel<Q, F, DP, decltype(rows)::value, decltype(pair)::value>;
     static LaunchCache cache;
     const hipError_t e = prepare_launch(cache, (const void*)kern, 64 * kTreeWaves, kLds, nullptr);
     if (e != hipSuccess) return e;
     kern<<<grid, dim3(64 * kTreeWaves), kLds, stream>>>(a);
     return hipGetLastError();
   };
-  typedef std::integral_constant<int, 1> One;
-  typedef std::integral_constant<int, 2> Two;
+  typedef std::integral_constant<int, 16> Narrow;
+  typedef std::integral_constant<int, 32> Wide;
   if (dim <= 64) {
     const std::integral_constant<int, 64> dp;
-    return few ? go(dp, One{}, std::true_type{}) : go(dp, Two{}, std::false_type{});
+    return few ? go(dp, Narrow{}, std::true_type{}) : go(dp, Wide{}, std::false_type{});
   }
   if (dim <= 128) {
     const std::integral_constant<int, 128> dp;
-    return few ? go(dp, One{}, std::true_type{}) : go(dp, Two{}, std::false_type{});
+    return few ? go(dp, Narrow{}, std::true_type{}) : go(dp, Wide{}, std::false_type{});
   }
   const std::integral_constant<int, 256> dp;
-  return few ? go(dp, One{}, std::true_type{}) : go(dp, One{}, std::false_type{});
+  return few ? go(dp, Narrow{}, std::true_type{}) : go(dp, Narrow{}, std::false_type{});
 }
 
 hipError_t launch_tree_bf16(const TreeArgs& a, bool few, dim3 grid, hipStream_t stream);

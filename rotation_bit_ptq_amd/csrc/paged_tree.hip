@@ -141,10 +141,11 @@ extern "C" orbit_status orbit_tree_attention(const orbit_tree_attention_args* p,
     default: e = launch_tree_int8(a, p->q_dtype, s.few, grid, stream);
   }
   if (e == hipSuccess && s.pieces > 1) {
-    const int at_once = 64 / (c.head_dim / 4);
-    const dim3 g((unsigned)((p->tokens * p->q_heads + at_once - 1) / at_once));
-    if (p->q_dtype == ORBIT_BF16) tree_join_kernel<__bf16><<<g, dim3(64), 0, stream>>>(a);
-    else tree_join_kernel<_Float16><<<g, dim3(64), 0, stream>>>(a);
+    const int64_t rows = p->tokens * p->q_heads;
+    // many rows fill the chip with a wave each
+    const dim3 g((unsigned)rows), threads(rows <= 16 * kUnits ? kJoinMost : 64);
+    if (p->q_dtype == ORBIT_BF16) tree_join_kernel<__bf16><<<g, threads, 0, stream>>>(a);
+    else tree_join_kernel<_Float16><<<g, threads, 0, stream>>>(a);
     e = hipGetLastError();
   }
   return hip_status(e);

@@ -104,7 +104,8 @@ __device__ __forceinline__ Request request_of(const TreeArgs& a, int b) {
 // request, and a piece of `per` tiles of its context; b < 0: nothing.  Every
 // workgroup counts the requests' row tiles and tiles, from which the size of a
 // piece (one for all, so that together they are about a.target workgroups)
-// and whose item this is follow.
+// and whose item this is follow.  Whole pieces come first and the contexts'
+// rests last, where they fill what the others leave.
 struct Item {
   int b, row_tile, piece, per;
 };
@@ -131,32 +132,37 @@ __device__ __forceinline__ Item item_of(const TreeArgs& a, int item, int tile, i
     rows += __shfl_xor(rows, x);
     all += __shfl_xor(all, x);
   }
-  const float left = fmaxf((float)a.target - (float)rows * (float)a.c.kv_heads, 0.25f * (float)a.target);
+  // as many whole pieces as leave a workgroup to each rest
+  const float left = fmaxf((float)a.target - 0.5f * (float)rows * (float)a.c.kv_heads, 0.25f * (float)a.target);
   Item it;
   it.per = max(max((int)(all * (float)a.c.kv_heads / left) + 1, (most + a.pieces - 1) / a.pieces), 2);
   it.per = __builtin_amdgcn_readfirstlane(it.per);
   it.b = -1;
   it.row_tile = it.piece = 0;
-  for (int x = 0; x < a.batch; x += 64) {
-    if (a.batch > 64) count(x + lane, row_tiles, tiles);
-    const int mine = row_tiles * max((tiles + it.per - 1) / it.per, 1);  // a request with nothing to see has zeros to write
-    int upto = mine;
+  for (int rest = 0; rest < 2; ++rest) {
+    for (int x = 0; x < a.batch; x += 64) {
+      if (a.batch > 64) count(x + lane, row_tiles, tiles);
+      const int whole = tiles / it.per;
+      // a request with nothing to see has zeros to write
+      const int mine = row_tiles * (!rest ? whole : tiles > whole * it.per || tiles == 0);
+      int upto = mine;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int o = __shfl_up(upto, d);
-      upto += lane >= d ? o : 0;
+      for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(upto, d);
+        upto += lane >= d ? o : 0;
+      }
+      const int total = __builtin_amdgcn_readlane(upto, 63);
+      if (item < total) {
+        const int who = __builtin_ctzll(__ballot(upto > item));
+        const int local = item - (__builtin_amdgcn_readlane(upto, who) - __builtin_amdgcn_readlane(mine, who));
+        const int r = __builtin_amdgcn_readlane(row_tiles, who);
+        it.b = x + who;
+        it.piece = rest ? __builtin_amdgcn_readlane(whole, who) : local / r;
+        it.row_tile = r - 1 - (rest ? local : local - it.piece * r);
+        return it;
+      }
+      item -= total;
     }
-    const int total = __builtin_amdgcn_readlane(upto, 63);
-    if (item < total) {
-      const int who = __builtin_ctzll(__ballot(upto > item));
-      const int local = item - (__builtin_amdgcn_readlane(upto, who) - __builtin_amdgcn_readlane(mine, who));
-      const int r = __builtin_amdgcn_readlane(row_tiles, who);
-      it.b = x + who;
-      it.piece = local / r;
-      it.row_tile = r - 1 - (local - it.piece * r);
-      break;
-    }
-    item -= total;
   }
   return it;
 }
@@ -177,6 +183,7 @@ __device__ __forceinline__ uint32_t bits32(const uint64_t* mask, int words, int 
 constexpr int kTreeWaves = 8;
 constexpr int kTreeWords = 8;  // stages of the scales and the words
 constexpr int kTreeStages = 4;
+constexpr int kJoinMost = 256;  // threads of a workgroup that joins
 constexpr int tree_key_tiles(bool coded) { return coded ? 2 : kTreeStages; }
 constexpr int tree_value_tiles(bool coded) { return coded ? 3 : kTreeStages; }  // values are read a step later
 constexpr int tree_tile(int dp) { return dp == 256 ? 32 : 64; }
@@ -899,42 +906,73 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   }
 }
 
-// Joins the pieces of one row: a workgroup of 64 threads for up to four rows
-// (dim / 4 lanes each) in a fixed order.
+// Joins the pieces of a row, a workgroup to each: groups of dim / 4 lanes take
+// every so many-th piece, and the first group adds their sums, in a fixed
+// order.  A group's first piece is read before it is known whether there is one.
 template <class QT>
-__global__ __launch_bounds__(64) void tree_join_kernel(TreeArgs a) {
+__global__ __launch_bounds__(kJoinMost) void tree_join_kernel(TreeArgs a) {
+  __shared__ __align__(16) float so[kJoinMost * 4], sm[kJoinMost * 2];
   const int dim = a.c.head_dim, lanes = dim >> 2;
-  const int at_once = 64 / lanes, g = threadIdx.x / lanes, t = threadIdx.x - g * lanes;
-  const long long row = (long long)blockIdx.x * at_once + g;
-  // rows that no request has (behind the last one's) hold no count
-  if (g >= at_once || row >= (long long)a.tokens * a.q_heads) return;
-  const int tok = (int)(row / a.q_heads);
-  if (tok < start_of(a, 0) || tok >= start_of(a, a.batch)) return;
-  const int n = ((const int*)(a.part + a.part_n))[row];
-  if (n <= 1 || n > a.pieces) return;
+  const int parts = (int)blockDim.x / lanes, g = (int)threadIdx.x / lanes, t = (int)threadIdx.x - g * lanes;
+  const long long row = blockIdx.x;
   const float2* const ml = (const float2*)(a.part + a.part_ml) + row * a.pieces;
-  float m = -__builtin_inff();
-#pragma unroll 8
-  for (int c = 0; c < n; ++c) m = fmaxf(m, ml[c].x);
-  const float m_use = m == -__builtin_inff() ? 0.0f : m;
-  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-  float l = 0.0f;
   const f32x4* const part = (const f32x4*)(a.part + row * a.pieces * dim) + t;
-#pragma unroll 8
-  for (int c = 0; c < n; ++c) {
-    const float e = factor(ml[c].x - m_use);
-    const f32x4 v = part[(long long)c * lanes];
-    l = fmaf(e, ml[c].y, l);
+  const int n = ((const int*)(a.part + a.part_n))[row];
+  const int from = min(g, a.pieces - 1);
+  float2 w = ml[from];
+  f32x4 v = part[(long long)from * lanes];
+  const int tok = (int)(row / a.q_heads);
+  // rows that no request has (behind the last one's) hold no count
+  if (tok < start_of(a, 0) || tok >= start_of(a, a.batch)) return;
+  if (n <= 1 || n > a.pieces) return;
+  float m = -__builtin_inff(), l = 0.0f;
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (g < parts && g < n) {
+    m = w.x;
+#pragma unroll 4
+    for (int c = g + parts; c < n; c += parts) m = fmaxf(m, ml[c].x);
+    const float m_use = m == -__builtin_inff() ? 0.0f : m;
+    auto add = [&] {
+      const float e = factor(w.x - m_use);
+      l = fmaf(e, w.y, l);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = fmaf(e, v[j], o[j]);
+      for (int j = 0; j < 4; ++j) o[j] = fmaf(e, v[j], o[j]);
+    };
+    add();
+#pragma unroll 4
+    for (int c = g + parts; c < n; c += parts) {
+      w = ml[c];
+      v = part[(long long)c * lanes];
+      add();
+    }
+    *(f32x4*)(so + (g * lanes + t) * 4) = o;
+    if (t == 0) {
+      sm[2 * g] = m;
+      sm[2 * g + 1] = l;
+    }
+  }
+  __syncthreads();
+  if (g != 0) return;
+  const int used = min(n, parts);
+  for (int c = 1; c < used; ++c) m = fmaxf(m, sm[2 * c]);
+  const float m_use = m == -__builtin_inff() ? 0.0f : m;
+  l = 0.0f;
+  o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int c = 0; c < used; ++c) {
+    const float e = factor(sm[2 * c] - m_use);
+    const f32x4 x = *(const f32x4*)(so + (c * lanes + t) * 4);
+    l = fmaf(e, sm[2 * c + 1], l);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = fmaf(e, x[j], o[j]);
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   struct alignas(8) {
     QT e[4];
-  } v;
+  } y;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v.e[j] = (QT)(l == 0.0f ? 0.0f : o[j] * inv);
-  *(decltype(v)*)((QT*)a.out + row * dim + t * 4) = v;
+  for (int j = 0; j < 4; ++j) y.e[j] = (QT)(l == 0.0f ? 0.0f : o[j] * inv);
+  *(decltype(y)*)((QT*)a.out + row * dim + t * 4) = y;
   if (a.lse && t == 0) a.lse[row] = (m + __builtin_amdgcn_logf(l)) * 0.69314718056f;
 }
 

@@ -180,6 +180,21 @@ __device__ __forceinline__ uint32_t bits32(const uint64_t* mask, int words, int 
   return (uint32_t)(sh ? (lo >> sh) | (hi << (64 - sh)) : lo);
 }
 
+// A tile's rows in LDS, of ROW bytes, without padding: 16-byte unit u of row r
+// lies in place u ^ key(r).  LDS serves 256 bytes at a time, so that a key's
+// upper bits tell apart the rows 0 - 3 (4 - 7) whose four units, and the rows
+// 0 - 7 whose two units a transposing read takes at once, all of them 16 rows
+// of one unit (the operands' reads), and the last one neighbouring rows of
+// which the conversion writes every other unit.  Row r + 8's key is row r's ^ 1.
+// (By key = r's low bits 60 % of the cycles in LDS were conflicts: 487 us for 4096 new of 8192 tokens, 460 so.)
+template <int ROW>
+struct TreeStage {
+  static __device__ __forceinline__ constexpr int key(int r) {
+    return ROW == 128 ? (r & 2) << 1 | (r & 4) >> 1 | ((r >> 3 ^ r >> 1) & 1)
+                      : (r & 1) << 3 | (r & 2) << 1 | (r & 4) >> 1 | ((r >> 3 ^ r) & 1);
+  }
+};
+
 constexpr int kTreeWaves = 8;
 constexpr int kTreeWords = 8;  // stages of the scales and the words
 constexpr int kTreeStages = 4;
@@ -254,7 +269,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   constexpr int kLoads = (kRows + kAtOnce - 1) / kAtOnce;               // of each tensor and tile; INT8: and one of scales
   constexpr int kInFlight = 2 * kLoads + (kCoded ? 1 : 0);
   constexpr float kLift = lift_of(F);
-  typedef Stage<DP * 2> St;
+  typedef TreeStage<DP * 2> St;
   constexpr int kKeyTiles = tree_key_tiles(kCoded), kValueTiles = tree_value_tiles(kCoded);
   constexpr int kTileBytes = kTokens * DP * 2, kValuesAt = kKeyTiles * kTileBytes, kRaw = tree_raw_stage(DP);
   constexpr int kScale = tree_scale_stage(DP);
@@ -600,7 +615,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     typedef __attribute__((address_space(3))) s16x4* lds_ptr;
     constexpr int kAll = kBlocks * (kWide ? 2 : 1);
     // rows 8 (kWide) or 16 further: this far, with the units' places exchanged
-    constexpr int kFar = kWide ? 8 : 16, kOther = kWide ? (DP == 64 ? 4 : 8) : 0;
+    constexpr int kFar = kWide ? 8 : 16, kOther = kWide ? 1 : 0;
     constexpr int kAheadV = kWide ? 4 : 2;
     union Block {
       s16x4 h[2];

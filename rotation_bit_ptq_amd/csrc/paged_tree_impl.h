@@ -100,65 +100,83 @@ __device__ __forceinline__ Request request_of(const TreeArgs& a, int b) {
   return r;
 }
 
+// Over a wave's lanes, x of this lane and those before it: six steps between
+// registers (by LDS they took most of the time in which a piece is found).
+template <class V, class F>
+__device__ __forceinline__ V scan_lanes(V x, F add) {  // of values >= 0
+  auto step = [&](auto ctrl, auto rows) {
+    x = add(x, __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value,
+                                                                 decltype(rows)::value, 15, false)));
+  };
+  step(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 15>{});  // from 1, 2, 4, 8 lanes before in the row of 16
+  step(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 15>{});
+  step(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 15>{});
+  step(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 15>{});
+  step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 10>{});  // rows 1 and 3: from the last of the row before
+  step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 12>{});  // rows 2 and 3: from lane 31
+  return x;
+}
+template <class V, class F>
+__device__ __forceinline__ V over_lanes(V x, F add) {
+  return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, scan_lanes(x, add)), 63));
+}
+
 // What a workgroup takes, where contexts are cut in pieces: a row tile of a
-// request, and a piece of `per` tiles of its context; b < 0: nothing.  Every
+// request, and a piece of `per` tiles of its context; rq.b < 0: nothing.  Every
 // workgroup counts the requests' row tiles and tiles, from which the size of a
 // piece (one for all, so that together they are about a.target workgroups)
 // and whose item this is follow.  Whole pieces come first and the contexts'
 // rests last, where they fill what the others leave.
 struct Item {
-  int b, row_tile, piece, per;
+  Request rq;
+  int row_tile, piece, per;
 };
 __device__ __forceinline__ Item item_of(const TreeArgs& a, int item, int tile, int lane) {
-  auto count = [&](int x, int& row_tiles, int& tiles) {
-    row_tiles = tiles = 0;
+  int begin, n, len, row_tiles, tiles;  // of this lane's request
+  auto count = [&](int x) {
+    begin = n = len = row_tiles = tiles = 0;
     if (x >= a.batch) return;
-    const int n = a.starts ? max(start_of(a, x + 1) - start_of(a, x), 0) : 1;
+    begin = start_of(a, x);
+    n = max(start_of(a, x + 1) - begin, 0);
+    len = min(max(a.lengths[x], 0), a.cap);
     row_tiles = (n * a.group + a.rows - 1) / a.rows;
-    tiles = (min(max(a.lengths[x], 0), a.cap) + tile - 1) / tile;
+    tiles = (len + tile - 1) / tile;
     if (a.window) tiles = min(tiles, (a.window + n) / tile + a.sinks / tile + 3);  // at most, for any of its rows
   };
-  int row_tiles, tiles, most = 0, rows = 0;
+  auto add = [](auto x, auto y) { return x + y; };
+  int most = 0, rows = 0;
   float all = 0.0f;
   for (int x = 0; x < a.batch; x += 64) {
-    count(x + lane, row_tiles, tiles);
-    most = max(most, row_tiles ? tiles : 0);
-    rows += row_tiles;
-    all += (float)row_tiles * (float)tiles;
-  }
-#pragma unroll
-  for (int x = 1; x < 64; x *= 2) {
-    most = max(most, __shfl_xor(most, x));
-    rows += __shfl_xor(rows, x);
-    all += __shfl_xor(all, x);
+    count(x + lane);
+    most = max(most, over_lanes(row_tiles ? tiles : 0, [](int x, int y) { return max(x, y); }));
+    rows += over_lanes(row_tiles, add);
+    all += over_lanes((float)row_tiles * (float)tiles, add);
   }
   // as many whole pieces as leave a workgroup to each rest
   const float left = fmaxf((float)a.target - 0.5f * (float)rows * (float)a.c.kv_heads, 0.25f * (float)a.target);
   Item it;
   it.per = max(max((int)(all * (float)a.c.kv_heads / left) + 1, (most + a.pieces - 1) / a.pieces), 2);
   it.per = __builtin_amdgcn_readfirstlane(it.per);
-  it.b = -1;
-  it.row_tile = it.piece = 0;
+  it.rq.b = -1;
   for (int rest = 0; rest < 2; ++rest) {
     for (int x = 0; x < a.batch; x += 64) {
-      if (a.batch > 64) count(x + lane, row_tiles, tiles);
+      if (a.batch > 64) count(x + lane);
       const int whole = tiles / it.per;
       // a request with nothing to see has zeros to write
       const int mine = row_tiles * (!rest ? whole : tiles > whole * it.per || tiles == 0);
-      int upto = mine;
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(upto, d);
-        upto += lane >= d ? o : 0;
-      }
+      const int upto = scan_lanes(mine, add);
       const int total = __builtin_amdgcn_readlane(upto, 63);
       if (item < total) {
         const int who = __builtin_ctzll(__ballot(upto > item));
         const int local = item - (__builtin_amdgcn_readlane(upto, who) - __builtin_amdgcn_readlane(mine, who));
         const int r = __builtin_amdgcn_readlane(row_tiles, who);
-        it.b = x + who;
         it.piece = rest ? __builtin_amdgcn_readlane(whole, who) : local / r;
         it.row_tile = r - 1 - (rest ? local : local - it.piece * r);
+        it.rq.b = x + who;
+        it.rq.begin = __builtin_amdgcn_readlane(begin, who);
+        it.rq.n = __builtin_amdgcn_readlane(n, who);
+        it.rq.len = __builtin_amdgcn_readlane(len, who);
+        it.rq.base = it.rq.len - it.rq.n;
         return it;
       }
       item -= total;
@@ -207,14 +225,14 @@ constexpr int tree_rows(int dp) { return tree_tile(dp) / kTreeWaves; }  // of a 
 // more stages (a wave's codes have been read when they are converted, its
 // scales are read by all waves later), and of as many
 // for each stage a word (bits: rows whose page lies outside the cache),
-// whether a wave saw such a page, and 32 rows of zeros.
+// whether a wave saw such a page, 32 rows of zeros, and rows' maxima and sums.
 constexpr int tree_tiles_lds(int dp, bool coded) { return (tree_key_tiles(coded) + tree_value_tiles(coded)) * tree_tile(dp) * dp * 2; }
 constexpr int tree_raw_stage(int dp) { return 2 * tree_rows(dp) * dp; }    // of a wave
 constexpr int tree_scale_stage(int dp) { return 4 * tree_rows(dp); }
 constexpr int tree_lds(int dp, bool coded) {
   return tree_tiles_lds(dp, coded) +
          (coded ? kTreeWaves * (kTreeStages * tree_raw_stage(dp) + kTreeWords * tree_scale_stage(dp)) : 0) + kTreeWords * 8 +
-         kTreeWaves * 4 + (dp <= 128 ? 32 * dp * 2 : 0);
+         kTreeWaves * 4 + (dp <= 128 ? 32 * dp * 2 : 0) + kTreeWaves * 32 * 8;
 }
 alignas(16) static __device__ const uint32_t kTreeZeros[4] = {0, 0, 0, 0};  // what is read in the place of tokens that are not there
 
@@ -275,7 +293,9 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   constexpr int kScale = tree_scale_stage(DP);
   constexpr uint32_t kRawAt = tree_tiles_lds(DP, kCoded), kScaleAt = kRawAt + (kCoded ? S * kTreeWaves * kRaw : 0),
                      kGoneAt = kScaleAt + (kCoded ? kTreeWords * kTreeWaves * kScale : 0),
-                     kZerosAt = kGoneAt + kTreeWords * 8 + kTreeWaves * 4;
+                     kZerosAt = kGoneAt + kTreeWords * 8 + kTreeWaves * 4,
+                     kSumsAt = kZerosAt + (DP <= 128 ? 32 * DP * 2 : 0);
+  static_assert(tree_tiles_lds(DP, kCoded) + (kCoded ? S * kTreeWaves * kRaw : 0) >= kTreeWaves * R * DP * 4);  // sums, at the end
   extern __shared__ __align__(1024) char lds[];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -286,17 +306,16 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   Item it;
   if (a.pieces > 1) {
     it = item_of(a, item, kTokens, lane);
+    if (it.rq.b < 0) return;
   } else {
     // the last slots first: in a prompt they have the longest contexts
-    const int slot = a.slots - 1 - item;
-    it.b = request_at(a, slot, lane);
-    it.row_tile = __builtin_amdgcn_readfirstlane(slot - first_slot(a, it.b));
+    const int slot = a.slots - 1 - item, b = request_at(a, slot, lane);
+    it.rq = request_of(a, b);
+    it.row_tile = __builtin_amdgcn_readfirstlane(slot - first_slot(a, b));
     it.piece = 0;
     it.per = 1 << 30;
   }
-  const int b = it.b;
-  if (b < 0 || b >= a.batch) return;
-  const Request rq = request_of(a, b);
+  const Request rq = it.rq;
   const int row0 = it.row_tile * a.rows, all_rows = rq.n * a.group;
   if (row0 < 0 || row0 >= all_rows) return;
   const int rows_here = min(a.rows, all_rows - row0);
@@ -344,11 +363,12 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     lo = max(p - a.window + 1, 0);
   }
   // all of the wave's rows see the tokens [lo_max, hi_min)
-  int lo_max = row_in ? lo : 0, hi_min = row_in ? hi : 0x7fffffff;
+  const int i0 = (row0 + wr * R) / a.group, i1 = (row0 + min(wr * R + R, rows_here) - 1) / a.group;
+  int lo_max = a.window ? max(rq.base + i1 - a.window + 1, 0) : 0, hi_min = a.words ? rq.base : rq.base + i0 + 1;
+  if (a.window && a.words) {
+    lo_max = row_in ? lo : 0;
 #pragma unroll
-  for (int s = 1; s < R; s *= 2) {
-    lo_max = max(lo_max, __shfl_xor(lo_max, s));
-    hi_min = min(hi_min, __shfl_xor(hi_min, s));
+    for (int s = 1; s < R; s *= 2) lo_max = max(lo_max, __shfl_xor(lo_max, s));
   }
   lo_max = __builtin_amdgcn_readfirstlane(lo_max);
   hi_min = __builtin_amdgcn_readfirstlane(hi_min);
@@ -366,43 +386,6 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   auto row_max = [&](float v) { return max_rows32(kWide ? v : max_rows16(v)); };
   auto row_add = [&](float v) { return add_rows32(kWide ? v : add_rows16(v)); };
 
-  // queries as the B operand
-  V8 qf[kSteps];
-  float zscale = fmaxf(fabsf(a.scale_log2e), 1.17549435e-38f);  // not 0: a hidden score is minus infinity
-  {
-    const QT* const qrow = (const QT*)a.q + (long long)token * a.qts + qhead * a.qhs;
-    float f[kSteps][8], m = 0.0f;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int d = (s * G + g) * 8;
-      const bool in = row_in && d < dim;
-      Vec8<QT> v;
-      if (in) v = *(const Vec8<QT>*)(qrow + d);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // the scale's sign goes to the query, so that the largest product is the largest score
-        f[s][j] = in ? (a.scale_log2e < 0.0f ? -(float)v.e[j] : (float)v.e[j]) : 0.0f;
-        if (kCoded) m = fmaxf(m, fabsf(f[s][j]));
-      }
-    }
-    if (kCoded) {  // into fp16's range by a power of two per row
-      m = row_max(m);
-      const int e = m > 0.0f && m < __builtin_inff() ? __builtin_amdgcn_frexp_expf(m) : 0;
-      const float down = ldexpf(1.0f, -e / 2), down2 = ldexpf(1.0f, -e - (-e / 2));
-      zscale = ldexpf(zscale, e);
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[s][j] = f[s][j] * down * down2;
-    }
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) qf[s][j] = (T)f[s][j];
-      asm volatile("" : "+v"(qf[s]));  // or the unrounded values are kept too, for the sums below
-    }
-  }
-
   // Loading.  This wave's rows of a tile are kRows wave .. + kRows - 1, load i
   // takes those from i * kAtOnce on, a lane 16 bytes: rows on one page, all of
   // them seen by some row and without padding, at constant places from a
@@ -412,7 +395,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   const int row_bytes = dim * kElem;
   const int lrow = lane / kRowLanes, lplace = lane & (kRowLanes - 1);
   typedef const __attribute__((address_space(4))) int32_t* const_ptr;  // by scalar loads, which no vector load waits for
-  const int32_t* const table = a.table + b * a.table_stride;
+  const int32_t* const table = a.table + rq.b * a.table_stride;
   auto tile_at = [&](int k) { return (k < sink_tiles ? k : first_tile + k - sink_tiles) * kTokens; };
   const bool plain = (int)a.c.page_mask + 1 >= kRows && dim == DP;
   uint32_t lane_at[kLoads];
@@ -514,6 +497,81 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+
+  // Queries.  kWide: read by whole rows (8192 cycles of a prompt's workgroup
+  // went into reading them as operands, 32 bytes of 32 rows at a time) and
+  // brought into the operands' order in LDS, in stages that no load is on its
+  // way to yet: behind the tiles in flight, or (INT8) where codes will be
+  // converted to, from the first barrier on.
+  Vec8<QT> q8[kSteps];
+  constexpr int kUnits = DP / 8;  // 16-byte units of a row
+  {
+    const long long at = (long long)token * a.qts + qhead * a.qhs;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      int r = rl, d = (s * G + g) * 8;
+      long long from = at;
+      if constexpr (kWide) {
+        r = s * (64 / kUnits) + lane / kUnits;
+        d = lane % kUnits * 8;
+        from = __shfl(at, r);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q8[s].e[j] = (QT)0.0f;
+      if (wr * R + r < rows_here && d < dim) q8[s] = *(const Vec8<QT>*)((const QT*)a.q + from + d);
+    }
+  }
+  // the pages of the first tiles' rows, a lane each
+  uint32_t first_pages = 0xffffffffu;
+  if (lane < kTreeStages && k0 + lane < k1) {
+    const int t = tile_at(k0 + lane) + wave * kRows;
+    if (t < hi_all) first_pages = (uint32_t)table[t >> a.c.page_shift];
+  }
+  // whether any page of the piece lies outside the cache
+  bool bad = false;
+  if (k0 < k1)
+    for (int x = (tile_at(k0) >> a.c.page_shift) + tid; x <= (min(tile_at(k1 - 1) + kTokens, hi_all) - 1) >> a.c.page_shift; x += 64 * kTreeWaves)
+      bad |= (uint32_t)table[x] >= a.c.pages;
+  // as the B operand
+  V8 qf[kSteps];
+  float zscale = fmaxf(fabsf(a.scale_log2e), 1.17549435e-38f);  // not 0: a hidden score is minus infinity
+  {
+    if constexpr (kWide) {
+      char* const mine = lds + (kCoded ? wave * R * DP * 2 : wave / 4 * kValuesAt + (k0 + 2 + wave / 2 % 2) % S * kTileBytes + wave % 2 * R * DP * 2);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int r = s * (64 / kUnits) + lane / kUnits;
+        *(Vec8<QT>*)(mine + r * DP * 2 + ((lane % kUnits ^ St::key(r & 15)) << 4)) = q8[s];
+      }
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) q8[s] = *(const Vec8<QT>*)(mine + rl * DP * 2 + (((s * G + g) ^ St::key(rl & 15)) << 4));
+    }
+    float f[kSteps][8], m = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // the scale's sign goes to the query, so that the largest product is the largest score
+        f[s][j] = a.scale_log2e < 0.0f ? -(float)q8[s].e[j] : (float)q8[s].e[j];
+        if (kCoded) m = fmaxf(m, fabsf(f[s][j]));
+      }
+    if (kCoded) {  // into fp16's range by a power of two per row
+      m = row_max(m);
+      const int e = m > 0.0f && m < __builtin_inff() ? __builtin_amdgcn_frexp_expf(m) : 0;
+      const float down = ldexpf(1.0f, -e / 2), down2 = ldexpf(1.0f, -e - (-e / 2));
+      zscale = ldexpf(zscale, e);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[s][j] = f[s][j] * down * down2;
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) qf[s][j] = (T)f[s][j];
+      asm volatile("" : "+v"(qf[s]));  // or the unrounded values are kept too, for the sums below
+    }
+  }
 
   // The sums: o[c], coordinates kStride c + 4 g + i; relative to m_run.
   typedef float f32xR __attribute__((ext_vector_type(kWide ? 16 : 4)));
@@ -642,20 +700,15 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   // Tiles in flight beside a step's: codes' places are free once converted;
   // others' when the next barrier says so (kWide: the next but one).
   const int ahead = kCoded ? S : step == 2 || kWide ? 2 : S - 1;
-  look_up(k0);
 #pragma unroll 1
   for (int x = k0; x < min(k0 + ahead, k1); ++x) {
+    page = __builtin_amdgcn_readlane(first_pages, x - k0);
     issue(x);
-    look_up(x + 1);
   }
+  look_up(k0 + ahead);
   if constexpr (kWide) {
     for (int x = tid; x < 32 * DP * 2 / 16; x += 64 * kTreeWaves) *(u32x4*)(lds + kZerosAt + x * 16) = u32x4{0u, 0u, 0u, 0u};
   }
-  // whether any page of the piece lies outside the cache
-  bool bad = false;
-  if (k0 < k1)
-    for (int x = (tile_at(k0) >> a.c.page_shift) + tid; x <= (min(tile_at(k1 - 1) + kTokens, hi_all) - 1) >> a.c.page_shift; x += 64 * kTreeWaves)
-      bad |= (uint32_t)table[x] >= a.c.pages;
   if (lane == 0) ((uint32_t*)(lds + kGoneAt + kTreeWords * 8))[wave] = 0;
   if (__any(bad)) ((uint32_t*)(lds + kGoneAt + kTreeWords * 8))[wave] = 1;
   tree_wait<62>();
@@ -848,76 +901,63 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     }
   }
 
-  // The sums of the waves on the same rows meet in LDS; from here on the
-  // maximum stands for the lifted one.
-  float* const so = (float*)lds;  // [wave with wt > 0][R][DP], then its maxima and sums
-  float* const sm = so + (wt_all - 1) * wrs * R * DP;
+  // Waves on the same rows bring their sums to one maximum and the sums of all
+  // waves meet in LDS, where a row's 16-byte unit u is in place u ^ key(row);
+  // rows leave it whole, those of a wave's rows shared among the waves that
+  // hold a part of them.  From here on the maximum stands for the lifted one.
+  float2* const sm = (float2*)(lds + kSumsAt);  // [wave][R]: maxima and sums
   l_run = row_add(l_run);
   m_run -= kLift;
-  if (wt_all > 1) {
-    __syncthreads();
-    const int mine = ((wt - 1) * wrs + wr) * R + rl;
-    if (wt > 0 && wt < wt_all) {
+  if (g == 0) sm[wave * R + rl] = make_float2(m_run, l_run);
+  __syncthreads();  // and the tiles have been read
+  if (works) {
+    float m = m_run;
+    for (int w = 0; w < wt_all; ++w) m = fmaxf(m, sm[(w * wrs + wr) * R + rl].x);
+    const float e = factor(m_run - (m == -__builtin_inff() ? 0.0f : m));
+    float* const mine = (float*)lds + (wave * R + rl) * DP;
 #pragma unroll
-      for (int c = 0; c < DP / kStride; ++c) {
-        const int d = c * 4 / kOf, y = c * 4 % kOf;
-        *(f32x4*)(so + mine * DP + c * kStride + g * 4) = f32x4{o[d][y], o[d][y + 1], o[d][y + 2], o[d][y + 3]};
-      }
-      if (g == 0) {
-        sm[mine * 2] = m_run;
-        sm[mine * 2 + 1] = l_run;
-      }
-    }
-    __syncthreads();
-    if (wt == 0) {
-      float m = m_run;
-      for (int w = 1; w < wt_all; ++w) m = fmaxf(m, sm[(((w - 1) * wrs + wr) * R + rl) * 2]);
-      const float m_use = m == -__builtin_inff() ? 0.0f : m;
-      const float e0 = factor(m_run - m_use);
-      l_run *= e0;
+    for (int c = 0; c < DP / kStride; ++c) {
+      const int d = c * 4 / kOf, y = c * 4 % kOf;
+      f32x4 v;
 #pragma unroll
-      for (int d = 0; d < kBlocks; ++d) o[d] *= e0;
-      for (int w = 1; w < wt_all; ++w) {
-        const int from = ((w - 1) * wrs + wr) * R + rl;
-        const float e = factor(sm[from * 2] - m_use);
-        l_run = fmaf(e, sm[from * 2 + 1], l_run);
-#pragma unroll
-        for (int c = 0; c < DP / kStride; ++c) {
-          const f32x4 x = *(const f32x4*)(so + from * DP + c * kStride + g * 4);
-          const int d = c * 4 / kOf, y = c * 4 % kOf;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[d][y + i] = fmaf(e, x[i], o[d][y + i]);
-        }
-      }
-      m_run = m;
+      for (int i = 0; i < 4; ++i) v[i] = o[d][y + i] * e;
+      *(f32x4*)(mine + ((c * G + g) ^ St::key(rl & 15)) * 4) = v;
     }
   }
-  if (wt != 0 || !row_in) return;
-  const long long row = (long long)token * a.q_heads + qhead;
-  const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
-  const long long part = row * a.pieces + it.piece;
-#pragma unroll
-  for (int c = 0; c < DP / kStride; ++c) {
-    const int e = c * kStride + g * 4, d = c * 4 / kOf, y = c * 4 % kOf;
-    if (e >= dim) continue;
-    if (last) {
-      struct alignas(8) {
-        QT e[4];
-      } v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v.e[i] = (QT)(l_run == 0.0f ? 0.0f : o[d][y + i] * inv);
-      *(decltype(v)*)((QT*)a.out + row * dim + e) = v;
-    } else {
-      *(f32x4*)(a.part + part * dim + e) = f32x4{o[d][y], o[d][y + 1], o[d][y + 2], o[d][y + 3]};
+  __syncthreads();
+  if (!works) return;
+  constexpr int kFours = DP / 4, kTogether = 64 / kFours;  // lanes of a row, rows at a time
+  const long long row_of = (long long)token * a.q_heads + qhead;
+#pragma unroll 2
+  for (int r0 = wt * kTogether; r0 < R; r0 += wt_all * kTogether) {
+    const int r = r0 + lane / kFours, u = lane % kFours;
+    const long long row = __shfl(row_of, r);
+    if (wr * R + r < rows_here) {
+      float m = -__builtin_inff(), l = 0.0f;
+      for (int w = 0; w < wt_all; ++w) m = fmaxf(m, sm[(w * wrs + wr) * R + r].x);
+      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int w = 0; w < wt_all; ++w) {
+        const int from = (w * wrs + wr) * R + r;
+        const float2 x = sm[from];
+        l = fmaf(factor(x.x - (m == -__builtin_inff() ? 0.0f : m)), x.y, l);
+        v += *(const f32x4*)((const float*)lds + from * DP + (u ^ St::key(r & 15)) * 4);
+      }
+      if (last) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        struct alignas(8) {
+          QT e[4];
+        } y;
+  #pragma unroll
+        for (int i = 0; i < 4; ++i) y.e[i] = (QT)(l == 0.0f ? 0.0f : v[i] * inv);
+        if (u * 4 < dim) *(decltype(y)*)((QT*)a.out + row * dim + u * 4) = y;
+        if (u == 0 && a.lse) a.lse[row] = (m + __builtin_amdgcn_logf(l)) * 0.69314718056f;
+      } else {
+        const long long part = row * a.pieces + it.piece;
+        if (u * 4 < dim) *(f32x4*)(a.part + part * dim + u * 4) = v;
+        if (u == 0) *(float2*)(a.part + a.part_ml + part * 2) = make_float2(m, l);
+      }
+      if (u == 0 && a.pieces > 1 && it.piece == 0) ((int*)(a.part + a.part_n))[row] = last ? 0 : used;
     }
-  }
-  if (g == 0) {
-    if (last) {
-      if (a.lse) a.lse[row] = (m_run + __builtin_amdgcn_logf(l_run)) * 0.69314718056f;
-    } else {
-      *(float2*)(a.part + a.part_ml + part * 2) = make_float2(m_run, l_run);
-    }
-    if (a.pieces > 1 && it.piece == 0) ((int*)(a.part + a.part_n))[row] = last ? 0 : used;
   }
 }
 

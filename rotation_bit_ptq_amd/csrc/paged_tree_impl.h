@@ -232,7 +232,7 @@ constexpr int tree_scale_stage(int dp) { return 4 * tree_rows(dp); }
 constexpr int tree_lds(int dp, bool coded) {
   return tree_tiles_lds(dp, coded) +
          (coded ? kTreeWaves * (kTreeStages * tree_raw_stage(dp) + kTreeWords * tree_scale_stage(dp)) : 0) + kTreeWords * 8 +
-         kTreeWaves * 4 + (dp <= 128 ? 32 * dp * 2 : 0) + kTreeWaves * 32 * 8;
+         kTreeWaves * 4 + 511 + (dp <= 128 ? 32 * dp * 2 : 0) + kTreeWaves * 32 * 8;
 }
 alignas(16) static __device__ const uint32_t kTreeZeros[4] = {0, 0, 0, 0};  // what is read in the place of tokens that are not there
 
@@ -293,7 +293,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   constexpr int kScale = tree_scale_stage(DP);
   constexpr uint32_t kRawAt = tree_tiles_lds(DP, kCoded), kScaleAt = kRawAt + (kCoded ? S * kTreeWaves * kRaw : 0),
                      kGoneAt = kScaleAt + (kCoded ? kTreeWords * kTreeWaves * kScale : 0),
-                     kZerosAt = kGoneAt + kTreeWords * 8 + kTreeWaves * 4,
+                     kZerosAt = (kGoneAt + kTreeWords * 8 + kTreeWaves * 4 + 511) / 512 * 512,
                      kSumsAt = kZerosAt + (DP <= 128 ? 32 * DP * 2 : 0);
   static_assert(tree_tiles_lds(DP, kCoded) + (kCoded ? S * kTreeWaves * kRaw : 0) >= kTreeWaves * R * DP * 4);  // sums, at the end
   extern __shared__ __align__(1024) char lds[];
@@ -413,11 +413,11 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     page = k < k1 && t < hi_all ? (uint32_t)((const_ptr)(uintptr_t)table)[t >> a.c.page_shift] : 0xffffffffu;
   };
   auto issue = [&](int k) {
-    const int t0 = tile_at(k) + wave * kRows, stage = k % S;
+    const int t0 = tile_at(k) + wave * kRows, stage = (int)((uint32_t)k % S);
     const uint32_t to = kCoded ? kRawAt + (uint32_t)(stage * kTreeWaves + wave) * kRaw
                                : (uint32_t)stage * kTileBytes + (uint32_t)wave * kRows * DP * 2;
     constexpr uint32_t kValues = kCoded ? kRows * DP : kValuesAt;
-    const uint32_t to_scales = kScaleAt + (uint32_t)(k % kTreeWords * kTreeWaves + wave) * kScale;
+    const uint32_t to_scales = kScaleAt + ((uint32_t)k % kTreeWords * kTreeWaves + wave) * kScale;
     uint32_t gone = 0;  // of this wave's rows
     if (plain && page < a.c.pages && t0 + kRows <= hi_all) {
       const long long row = cache_row(a.c, page, head, (uint32_t)t0 & a.c.page_mask);
@@ -463,18 +463,18 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
         tree_load16(to + kValues + i * 1024, from_v[i]);
       }
     }
-    if (lane == 0) ((uint8_t*)(lds + kGoneAt))[k % kTreeWords * 8 + wave] = (uint8_t)gone;
+    if (lane == 0) ((uint8_t*)(lds + kGoneAt))[(uint32_t)k % kTreeWords * 8 + wave] = (uint8_t)gone;
   };
   // INT8: this wave's rows of tile k become fp16
   auto convert = [&](int k) {
-    const char* const raw = lds + kRawAt + (uint32_t)((k % S) * kTreeWaves + wave) * kRaw;
+    const char* const raw = lds + kRawAt + (uint32_t)(((uint32_t)k % S) * kTreeWaves + wave) * kRaw;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       if (kRows < kAtOnce && lrow >= kRows) break;
       const int r = wave * kRows + i * kAtOnce + lrow;
       const u32x4 k4 = *(const u32x4*)(raw + i * 1024 + lane * 16), v4 = *(const u32x4*)(raw + kRows * DP + i * 1024 + lane * 16);
-      char* const to = lds + k % kKeyTiles * kTileBytes + r * DP * 2;
-      char* const to_v = lds + kValuesAt + k % kValueTiles * kTileBytes + r * DP * 2;
+      char* const to = lds + (uint32_t)k % kKeyTiles * kTileBytes + r * DP * 2;
+      char* const to_v = lds + kValuesAt + (uint32_t)k % kValueTiles * kTileBytes + r * DP * 2;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int at = ((lplace * 2 + c) ^ St::key(r & 15)) << 4;
@@ -594,9 +594,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   // one tile: those values are read behind the next barrier, so the stage after
   // next is filled and not the next.
   constexpr int kScores = 4 * kQuads;  // of a lane
-  float s[kScores];
   float vt[kCoded ? kScores : 1];  // INT8: the values' scales
-  const char* pend;  // their values
+  int pend = 0;  // place of their values in LDS
   bool pend_odd = false;  // INT8: some of the values' scales are infinite or NaN
   uint32_t pend_seen = 0;
 
@@ -605,7 +604,9 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   // part of both at a time: the weights' instructions stand between the keys'
   // reads and their products.
   // CHECKED: values' scales of hidden tokens may be infinite or NaN.
-  auto advance_as = [&](float (&z)[kScores], const char* ks, auto with_scores, auto with_weights, auto checked) {
+  // Scores z of the 32 tokens whose keys lie `skip` behind the place that
+  // `keys` says, weights of s.
+  auto advance_as = [&](float (&z)[kScores], const float (&s)[kScores], int keys, auto skip, auto with_scores, auto with_weights, auto checked) {
     constexpr bool SCORES = decltype(with_scores)::value, WEIGHTS = decltype(with_weights)::value, CHECKED = decltype(checked)::value;
     constexpr int kPairs2 = kScores / 2;  // weights, two by two
     const float m_use = m_run == -__builtin_inff() ? 0.0f : m_run - kLift;
@@ -621,7 +622,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     auto read_keys = [&](int i) {
 #pragma unroll
       for (int h = 0; h < (kWide ? 1 : 2); ++h)
-        kv[i % (kAheadK + 1)][h] = __builtin_bit_cast(V8, *(const u32x4*)(ks + h * 16 * DP * 2 + (kread ^ (i * G << 4))));
+        kv[i % (kAheadK + 1)][h] = __builtin_bit_cast(V8, *(const u32x4*)(lds + ((keys ^ (i * G << 4)) + h * 16 * DP * 2 + decltype(skip)::value)));
     };
     if constexpr (SCORES) {
 #pragma unroll
@@ -663,9 +664,9 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
       for (int j = 0; j < kScores; ++j) z[j] = acc[kWide ? 0 : j / 4][kWide ? j : j % 4];
     }
   };
-  auto advance = [&](float (&z)[kScores], const char* ks, auto with_scores, auto with_weights) {
-    if (kCoded && decltype(with_weights)::value && pend_odd) advance_as(z, ks, with_scores, with_weights, std::true_type{});
-    else advance_as(z, ks, with_scores, with_weights, std::false_type{});
+  auto advance = [&](float (&z)[kScores], const float (&s)[kScores], int keys, auto skip, auto with_scores, auto with_weights) {
+    if (kCoded && decltype(with_weights)::value && pend_odd) advance_as(z, s, keys, skip, with_scores, with_weights, std::true_type{});
+    else advance_as(z, s, keys, skip, with_scores, with_weights, std::false_type{});
   };
   // The pending tokens' weights with their values, by blocks of R coordinates
   // (and 16 tokens: kWide); some products' operands are read ahead.
@@ -679,11 +680,12 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
       s16x4 h[2];
       V8 v;
     } u[kAheadV + 1];
+    const int values = vread + pend;
     auto read = [&](int n) {
       const int d = kWide ? n >> 1 : n, m = kWide ? n & 1 : 0;
-      const int at = vread ^ (d * (R / 8) << 4);
-      u[n % (kAheadV + 1)].h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(pend + m * 16 * DP * 2 + at));
-      u[n % (kAheadV + 1)].h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(pend + (m * 16 + kFar) * DP * 2 + (at ^ (kOther << 4))));
+      const int at = values ^ (d * (R / 8) << 4);
+      u[n % (kAheadV + 1)].h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + (at + m * 16 * DP * 2)));
+      u[n % (kAheadV + 1)].h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + ((at ^ (kOther << 4)) + (m * 16 + kFar) * DP * 2)));
     };
 #pragma unroll
     for (int n = 0; n < kAheadV && n < kAll; ++n) read(n);
@@ -715,8 +717,9 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   meet();
   const u32x4 bad0 = *(const u32x4*)(lds + kGoneAt + kTreeWords * 8), bad1 = *(const u32x4*)(lds + kGoneAt + kTreeWords * 8 + 16);
   const bool holes = __builtin_amdgcn_readfirstlane(bad0.x | bad0.y | bad0.z | bad0.w | bad1.x | bad1.y | bad1.z | bad1.w) != 0;
+  auto fresh = [&] { asm volatile("" : "+v"(kread), "+v"(vread)); };  // the places made of them are not kept in registers
   // A step's tiles, there and ready to be read by all waves.
-  auto begin_step = [&](int k, int here) {
+  auto begin_step = [&](int k, auto step, int here) {
     landed(min(k1, k + ahead) - k - here);
     if constexpr (kCoded) {
       // two tiles take a place that the step before had: it must have been read
@@ -731,14 +734,14 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
       issue(x);
       look_up(x + 1);
     }
-    asm volatile("" : "+v"(kread), "+v"(vread));  // the places made of them are not kept in registers
+    fresh();
   };
-  // Scores z of the 32 tokens from ts on (part `sub` of tile `at`) become s:
+  // Scores z of the 32 tokens from ts on (part `sub` of tile `at`) are
   // scaled, masked, the maximum carried on.
   auto take = [&](float (&z)[kScores], int at, int sub, int ts) {
     float lv[kCoded ? kScores : 1];
     if constexpr (kCoded) {
-      const char* const scales = lds + kScaleAt + (uint32_t)(at % kTreeWords) * kTreeWaves * kScale;  // of the first wave's rows
+      const char* const scales = lds + kScaleAt + (uint32_t)at % kTreeWords * kTreeWaves * kScale;  // of the first wave's rows
       float odd = 0.0f;
 #pragma unroll
       for (int q = 0; q < kQuads; ++q) {
@@ -760,7 +763,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     if (holes || !((ts >= lo_max || ts + 32 <= a.sinks) && ts + 32 <= hi_min)) {
       uint32_t seen = seen32(ts);
       if (holes) {  // a wave's rows are a byte, or half of one
-        uint64_t rows = *(const uint64_t*)(lds + kGoneAt + at % kTreeWords * 8);
+        uint64_t rows = *(const uint64_t*)(lds + kGoneAt + (uint32_t)at % kTreeWords * 8);
         if (kRows == 4) {
           const uint64_t gone = rows;
           rows = 0;
@@ -791,11 +794,12 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
 #pragma unroll
       for (int d = 0; d < kBlocks; ++d) o[d] *= alpha;
     }
-#pragma unroll
-    for (int j = 0; j < kScores; ++j) s[j] = z[j];
   };
-  auto keys_of = [&](int at, int sub) { return lds + at % kKeyTiles * kTileBytes + sub * 32 * DP * 2; };
-  auto values_of = [&](int at, int sub) { return lds + kValuesAt + at % kValueTiles * kTileBytes + sub * 32 * DP * 2; };
+  auto keys_of = [&](int at) { return kread + (int)((uint32_t)at % kKeyTiles) * kTileBytes; };
+  auto values_of = [&](int at, int sub) { return kValuesAt + (int)((uint32_t)at % kValueTiles) * kTileBytes + sub * 32 * DP * 2; };
+  typedef std::integral_constant<int, 0> First;
+  typedef std::integral_constant<int, 32 * DP * 2> Second;
+  float s[kScores];
   if (kWide && step == 1) {
     // nothing is pending: zeros
 #pragma unroll
@@ -803,42 +807,48 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
       s[j] = -__builtin_inff();
       if constexpr (kCoded) vt[j] = 0.0f;
     }
-    pend = lds + kZerosAt;
+    pend = kZerosAt;
+    auto next = [&](float (&z)[kScores], const float (&was)[kScores], int k, int keys, auto skip, int sub) {
+      advance(z, was, keys, skip, std::true_type{}, std::true_type{});
+      products();
+      pend = values_of(k, sub);
+      take(z, k, sub, tile_at(k) + sub * 32);
+    };
 #pragma unroll 1
     for (int k = k0; k < k1; ++k) {
-      begin_step(k, 1);
-      const int n1 = works ? kSubs : 0;
-#pragma unroll 1
-      for (int sub = wt; sub < n1; sub += wt_all) {
-        const int ts = tile_at(k) + sub * 32;
-        if (ts >= hi_all) break;
+      begin_step(k, std::integral_constant<int, 1>{}, 1);
+      // a wave has both halves of the tile or one; scores in two sets of registers
+      if (works && tile_at(k) + wt * 32 < hi_all) {
+        const int keys = keys_of(k) + wt * 32 * DP * 2;
         float z[kScores];
-        advance(z, keys_of(k, sub), std::true_type{}, std::true_type{});
-        products();
-        pend = values_of(k, sub);
-        take(z, k, sub, ts);
+        next(z, s, k, keys, First{}, wt);
+        if (wt_all == 1 && tile_at(k) + 32 < hi_all) {
+          next(s, z, k, keys, Second{}, 1);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kScores; ++j) s[j] = z[j];
+        }
       }
     }
     if (works) {
       float none[kScores];
-      advance(none, nullptr, std::false_type{}, std::true_type{});
+      advance(none, s, 0, First{}, std::false_type{}, std::true_type{});
       products();
     }
   } else {
 #pragma unroll 1
     for (int k = k0; k < k1; k += step) {
       const int here = min(step, k1 - k);  // tiles of this step
-      begin_step(k, here);
+      begin_step(k, step, here);
       const int n1 = works ? here * kSubs : 0;
 #pragma unroll 1
       for (int n = wt; n < n1; n += wt_all) {
         const int at = k + n / kSubs, sub = n % kSubs, ts = tile_at(at) + sub * 32;
         if (ts >= hi_all) break;
-        float z[kScores];
-        advance(z, keys_of(at, sub), std::true_type{}, std::false_type{});
-        take(z, at, sub, ts);
+        advance(s, s, keys_of(at) + sub * 32 * DP * 2, First{}, std::true_type{}, std::false_type{});
+        take(s, at, sub, ts);
         pend = values_of(at, sub);
-        advance(z, nullptr, std::false_type{}, std::true_type{});
+        advance(s, s, 0, First{}, std::false_type{}, std::true_type{});
         products();
       }
     }
@@ -926,37 +936,38 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   }
   __syncthreads();
   if (!works) return;
-  constexpr int kFours = DP / 4, kTogether = 64 / kFours;  // lanes of a row, rows at a time
+  float m = -__builtin_inff(), l = 0.0f;  // of this lane's row
+  for (int w = 0; w < wt_all; ++w) m = fmaxf(m, sm[(w * wrs + wr) * R + rl].x);
+  for (int w = 0; w < wt_all; ++w) {
+    const float2 x = sm[(w * wrs + wr) * R + rl];
+    l = fmaf(factor(x.x - (m == -__builtin_inff() ? 0.0f : m)), x.y, l);
+  }
   const long long row_of = (long long)token * a.q_heads + qhead;
-#pragma unroll 2
+  if (wt == 0 && g == 0 && row_in) {
+    if (!last) *(float2*)(a.part + a.part_ml + (row_of * a.pieces + it.piece) * 2) = make_float2(m, l);
+    else if (a.lse) a.lse[row_of] = (m + __builtin_amdgcn_logf(l)) * 0.69314718056f;
+    if (a.pieces > 1 && it.piece == 0) ((int*)(a.part + a.part_n))[row_of] = last ? 0 : used;
+  }
+  const float inv = !last ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+  constexpr int kFours = DP / 4, kTogether = 64 / kFours;  // lanes of a row, rows at a time
+#pragma unroll 4
   for (int r0 = wt * kTogether; r0 < R; r0 += wt_all * kTogether) {
     const int r = r0 + lane / kFours, u = lane % kFours;
     const long long row = __shfl(row_of, r);
-    if (wr * R + r < rows_here) {
-      float m = -__builtin_inff(), l = 0.0f;
-      for (int w = 0; w < wt_all; ++w) m = fmaxf(m, sm[(w * wrs + wr) * R + r].x);
-      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int w = 0; w < wt_all; ++w) {
-        const int from = (w * wrs + wr) * R + r;
-        const float2 x = sm[from];
-        l = fmaf(factor(x.x - (m == -__builtin_inff() ? 0.0f : m)), x.y, l);
-        v += *(const f32x4*)((const float*)lds + from * DP + (u ^ St::key(r & 15)) * 4);
-      }
+    const float scale = __shfl(inv, r);
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int w = 0; w < wt_all; ++w) v += *(const f32x4*)((const float*)lds + ((w * wrs + wr) * R + r) * DP + (u ^ St::key(r & 15)) * 4);
+    if (wr * R + r < rows_here && u * 4 < dim) {
       if (last) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         struct alignas(8) {
           QT e[4];
         } y;
-  #pragma unroll
-        for (int i = 0; i < 4; ++i) y.e[i] = (QT)(l == 0.0f ? 0.0f : v[i] * inv);
-        if (u * 4 < dim) *(decltype(y)*)((QT*)a.out + row * dim + u * 4) = y;
-        if (u == 0 && a.lse) a.lse[row] = (m + __builtin_amdgcn_logf(l)) * 0.69314718056f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y.e[i] = (QT)(scale == 0.0f ? 0.0f : v[i] * scale);
+        *(decltype(y)*)((QT*)a.out + row * dim + u * 4) = y;
       } else {
-        const long long part = row * a.pieces + it.piece;
-        if (u * 4 < dim) *(f32x4*)(a.part + part * dim + u * 4) = v;
-        if (u == 0) *(float2*)(a.part + a.part_ml + part * 2) = make_float2(m, l);
+        *(f32x4*)(a.part + (row * a.pieces + it.piece) * dim + u * 4) = v;
       }
-      if (u == 0 && a.pieces > 1 && it.piece == 0) ((int*)(a.part + a.part_n))[row] = last ? 0 : used;
     }
   }
 }

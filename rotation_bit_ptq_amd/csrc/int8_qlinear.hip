@@ -71,40 +71,65 @@ __device__ __forceinline__ void store8(OT* p, const float (&f)[8]) {
 }
 
 // Sums of `rows` tokens (from m0) and `cols` channels (from n0) that lie in
-// LDS as int32 [rows][pitch], finished and stored by `threads` threads of
-// which this is number t.
-template <class OT>
-__device__ __forceinline__ void finish(const ProductArgs& a, const int* sums, int pitch, int rows, int cols, long long m0,
-                                       long long n0, int t, int threads) {
-  if (a.vec) {
-    const int per = cols / 8;            // vectors of a row
-    const int at_once = threads / per;   // rows
-    const int r0 = t / per, c = (t - r0 * per) * 8;
-    const long long n = n0 + c;
-    if (r0 >= at_once || n >= a.N) return;  // vec: N is a multiple of 8
-    float sw[8], b[8];
+// LDS as int32 [rows][pitch], the tokens' scales behind them in column `cols`,
+// finished and stored by `threads` threads.  Where rows are vectors (a.vec) a
+// thread has eight channels of every so many-th row, whose scales and bias it
+// reads before the product (by 256 x 192 they took 24000 of 80000 cycles when
+// each row's were read in its turn).
+struct Finish {
+  float sw[8], b[8];
+  int r0, c, at_once;
+  bool in;
+  long long n;
+  __device__ __forceinline__ Finish(const ProductArgs& a, int cols, long long n0, int t, int threads) {
+    const int per = cols / 8;  // vectors of a row
+    at_once = threads / per;   // rows
+    r0 = t / per;
+    c = (t - r0 * per) * 8;
+    n = n0 + c;
+    in = r0 < at_once && n < a.N;  // vec: N is a multiple of 8
+    if (!a.vec || !in) return;
+    const float* const w = a.sw + n;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      sw[j] = a.sw[n + j];
-      b[j] = bias_of(a, n + j);
+      sw[j] = w[j];
+      b[j] = 0.0f;
     }
-    for (int r = r0; r < rows && m0 + r < a.M; r += at_once) {
-      const float sx = a.sx[m0 + r];
-      const i32x4 x = *(const i32x4*)(sums + r * pitch + c), y = *(const i32x4*)(sums + r * pitch + c + 4);
-      float f[8];
+    if (!a.bias) return;
+    auto read = [&](auto* bias) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = activate(fmaf((float)(j < 4 ? x[j & 3] : y[j & 3]), sx * sw[j], b[j]), a.act);
-      store8((OT*)a.out + (m0 + r) * a.N + n, f);
-    }
-  } else {
-    for (int i = t; i < rows * cols; i += threads) {
-      const int r = i / cols, c = i - r * cols;
-      if (m0 + r < a.M && n0 + c < a.N)
-        ((OT*)a.out)[(m0 + r) * a.N + n0 + c] =
-            (OT)activate(fmaf((float)sums[r * pitch + c], a.sx[m0 + r] * a.sw[n0 + c], bias_of(a, n0 + c)), a.act);
+      for (int j = 0; j < 8; ++j) b[j] = (float)bias[n + j];
+    };
+    if (a.bias_dtype == ORBIT_BF16) read((const __bf16*)a.bias);
+    else if (a.bias_dtype == ORBIT_F16) read((const _Float16*)a.bias);
+    else read((const float*)a.bias);
+  }
+  template <class OT>
+  __device__ __forceinline__ void store(const ProductArgs& a, const int* sums, int pitch, int rows, int cols, long long m0, long long n0,
+                                        int t, int threads) const {
+    auto scale = [&](int r) { return __builtin_bit_cast(float, sums[r * pitch + cols]); };
+    if (a.vec) {
+      if (!in) return;
+      const int end = (int)min((long long)rows, a.M - m0);
+#pragma unroll 2
+      for (int r = r0; r < end; r += at_once) {
+        const float sx = scale(r);
+        const i32x4 x = *(const i32x4*)(sums + r * pitch + c), y = *(const i32x4*)(sums + r * pitch + c + 4);
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = activate(fmaf((float)(j < 4 ? x[j & 3] : y[j & 3]), sx * sw[j], b[j]), a.act);
+        store8((OT*)a.out + (m0 + r) * a.N + n, f);
+      }
+    } else {
+      for (int i = t; i < rows * cols; i += threads) {
+        const int r = i / cols, q = i - r * cols;
+        if (m0 + r < a.M && n0 + q < a.N)
+          ((OT*)a.out)[(m0 + r) * a.N + n0 + q] =
+              (OT)activate(fmaf((float)sums[r * pitch + q], scale(r) * a.sw[n0 + q], bias_of(a, n0 + q)), a.act);
+      }
     }
   }
-}
+};
 
 // The loads that go from memory straight to LDS are inline assembly with
 // explicit waits: they have no register results, and the compiler would wait
@@ -164,6 +189,8 @@ __global__ __launch_bounds__(512) void thin_kernel(ProductArgs a) {
 #pragma unroll
     for (int b = 0; b < kLoads; ++b) load_lds(st + b * 1024u, from[b] + at - (c == chunks - 1 ? back(b) : 0u), b < 2 * RB ? wbase : xbase);
   };
+  const Finish finish(a, 16 * RB, n0, t, 512);
+  const float sx = t < 16 * MB && m0 + t < a.M ? a.sx[m0 + t] : 0.0f;
   i32x4 acc[RB][MB];
 #pragma unroll
   for (int i = 0; i < RB; ++i)
@@ -208,6 +235,7 @@ __global__ __launch_bounds__(512) void thin_kernel(ProductArgs a) {
   __syncthreads();
   for (int i = t; i < 16 * MB * kPitch; i += 512) sums[i] = 0;
   __syncthreads();
+  if (t < 16 * MB) sums[t * kPitch + 16 * RB] = __builtin_bit_cast(int, sx);
 #pragma unroll
   for (int i = 0; i < RB; ++i)
 #pragma unroll
@@ -215,7 +243,7 @@ __global__ __launch_bounds__(512) void thin_kernel(ProductArgs a) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) atomicAdd(&sums[(16 * j + r16) * kPitch + 16 * i + g * 4 + q], acc[i][j][q]);
   __syncthreads();
-  finish<OT>(a, sums, kPitch, 16 * MB, 16 * RB, m0, n0, t, 512);
+  finish.template store<OT>(a, sums, kPitch, 16 * MB, 16 * RB, m0, n0, t, 512);
 }
 
 template <class OT, int MB, int RB, int S>
@@ -322,6 +350,10 @@ __global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs a) {
 #pragma unroll
     for (int i = 0; i < BM; ++i) xv[set][i] = *(const i32x4*)(st + rx + i * 4096);
   };
+  const Finish finish(a, 32 * BN, n0 + wn * BN * 32, lane, 64);
+  float sx[BM];
+#pragma unroll
+  for (int i = 0; i < BM; ++i) sx[i] = a.sx[min(m0 + (wm * BM + i) * 32 + r32, a.M - 1)];
   i32x16 acc[BN][BM];
 #pragma unroll
   for (int j = 0; j < BN; ++j)
@@ -379,10 +411,11 @@ __global__ __launch_bounds__(64 * WGM * WGN) void tile_kernel(ProductArgs a) {
       for (int q = 0; q < 4; ++q)
         *(i32x4*)(mine + r32 * kPitch + 32 * j + 8 * q + 4 * half) =
             i32x4{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+    if (half == 0) mine[r32 * kPitch + 32 * BN] = __builtin_bit_cast(int, sx[i]);
     // the wave's own rows: LDS serves a wave in order
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    finish<OT>(a, mine, kPitch, 32, 32 * BN, m0 + (wm * BM + i) * 32, n0 + wn * BN * 32, lane, 64);
+    finish.template store<OT>(a, mine, kPitch, 32, 32 * BN, m0 + (wm * BM + i) * 32, n0 + wn * BN * 32, lane, 64);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
@@ -419,8 +452,8 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t stream) {
     int tm, tn;
     Launch launch;
   } kVariants[] = {
-      {16, 16, launch_thin<OT, 1, 1, 4>}, {16, 32, launch_thin<OT, 1, 2, 3>},  {32, 32, launch_thin<OT, 2, 2, 2>},
-      {64, 32, launch_thin<OT, 4, 2, 1>}, {64, 64, launch_thin<OT, 4, 4, 1>},  {128, 128, launch_tiles<OT, 2, 2, 2, 2, 2>},
+      {16, 16, launch_thin<OT, 1, 1, 4>}, {16, 32, launch_thin<OT, 1, 2, 1>},  {32, 32, launch_thin<OT, 2, 2, 1>},
+      {64, 32, launch_thin<OT, 4, 2, 1>}, {64, 64, launch_thin<OT, 4, 4, 1>},  {128, 128, launch_tiles<OT, 2, 4, 2, 1, 3>},
       {256, 192, launch_tiles<OT, 4, 2, 2, 3, 2>}, {256, 256, launch_tiles<OT, 2, 4, 4, 2, 2>}};
   Launch best = nullptr;
   double least = 0.0;

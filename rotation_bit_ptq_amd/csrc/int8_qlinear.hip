@@ -7,10 +7,10 @@
 // Two kernels.
 // * tile_kernel, for products with enough tiles to fill the chip.  Bound: the
 //   matrix cores, and what a compute unit takes in (launch_product).  16384 x
-//   4096 -> 4096 260 us (2.1 POP/s, as the library's int8 product of 8192^3;
-//   that size here 2.3), 4096 x 3072 -> 3072 43 us.
+//   4096 -> 4096 243 us (2.3 POP/s; the library's int8 product of 8192^3 2.1),
+//   4096 x 3072 -> 3072 39 us.
 // * thin_kernel, for few tokens or few tiles.  Bound: the weights' bytes, or
-//   what a compute unit takes in.  16 x 3072 -> 18432 15 us (3.8 TB/s).
+//   what a compute unit takes in.  16 x 3072 -> 18432 11 us (5.1 TB/s).
 // Everywhere the weights are the matrix instruction's A operand (rows) and
 // the tokens its B operand (columns), so that a lane's results are
 // neighbouring channels of one token.
@@ -154,8 +154,10 @@ __device__ __forceinline__ void meet() {
 // A workgroup of eight waves takes 16 RB channels and up to 16 MB tokens
 // (v_mfma_i32_16x16x64_i8); wave w the 128-byte chunks w, w + 8, ... of K,
 // through an LDS ring of its own, so that no barrier stands between two
-// chunks and 100 KB or more are in flight in a compute unit.  The waves' sums
-// are added in LDS (integers: the order does not matter).
+// chunks.  With rings of one stage two or three workgroups share a compute
+// unit, one's loads beside another's sums (16 x 3072 -> 18432 with its tokens'
+// codes made first: 16.2 us, with three stages and one workgroup 19.6).  The
+// waves' sums are added in LDS (integers: the order does not matter).
 // A chunk is blocks of 8 rows, one load instruction each (whole lines: blocks
 // of 16 rows of 64 bytes were 5 to 10 % slower); 16-byte unit u of row r lies
 // at 128 r + 16 (u ^ (r / 2) % 8), which puts the 16 rows that LDS serves at
@@ -440,11 +442,13 @@ hipError_t launch_tiles(ProductArgs a, hipStream_t stream) {
 // (TM + TN) K operand bytes at 50 KB/us (what a unit was seen to take in, from
 // one workgroup on the whole chip to several on each unit) or its 2 TM TN K
 // operations at 9 per ps (the chip's settled 2.3 POP/s, shared), whichever is
-// longer.  Measured, us (thin tile of 64 x 64, 128 x 128, 256 x 192, 256 x 256):
-// 256 x 4096 -> 4096 11.3, 20, 39, 48; 1024 x 4096 -> 4096 42, 27, 41, 50;
-// 4096 x 3072 -> 3072 (-), 50, 43, 45; 16384 x 4096 -> 4096 (-), 297, 299,
-// 260; 64 x 4096 -> 4096 with thin tiles of 16 x 32, 32 x 32, 64 x 32, 64 x 64:
-// 9.7, 7.4, 8.1, 10.4.
+// longer.  Measured, us (thin tiles of 16 x 32, 32 x 32, 64 x 32, 64 x 64; 128
+// x 128, 256 x 192, 256 x 256): 16 x 3072 -> 18432 11.1, 12.6, 17.3, 18.6;
+// 14.5, 25.9, 32.0.  64 x 4096 -> 4096 7.8, 6.2, 7.4, 16.3; 18.9, 34.9, 41.7.
+// 256 x 4096 -> 4096 21.1, 16.5, 14.3, 10.2; 18.9, 35.9, 44.1.  333 x 2064 ->
+// 8200 (-), 36.8; 13.2, 24.1, 29.7.  1024 x 4096 -> 4096 (-), 37.6; 22.7, 37.4,
+// 46.1.  4096 x 3072 -> 3072 (-), 90.9; 51.4, 39.4, 41.7.  16384 x 4096 -> 4096
+// (-), 534; 347, 277, 243.
 template <class OT>
 hipError_t launch_product(const ProductArgs& a, hipStream_t stream) {
   typedef hipError_t (*Launch)(ProductArgs, hipStream_t);

@@ -58,7 +58,7 @@ def test_rotated(gpu_lib, d, h, dtype):
     against(q, s, ref, perm, signs, h)
 
 
-# the matrix-core kernel's rows: every width, both blocks, with and without a plan, an identity, more rows than waves
+# rows of whole words: every width, both blocks, with and without a plan, an identity, more rows than waves
 @pytest.mark.parametrize("d", [1024, 2048, 3072, 4096, 8192, 12288, 16384])
 @pytest.mark.parametrize("h", [128, 256])
 @pytest.mark.parametrize("form", ["plan", "no plan", "identity"])

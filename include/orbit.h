@@ -300,7 +300,8 @@ orbit_status orbit_int4_linear(const void *Xrot, orbit_dtype xrot_dtype, int64_t
  * and, offline, the weights of orbit_int8_qlinear (rotate, then quantize, as
  * orbit_int8_pack_weights, with the whole row as the group):
  *   x' = Pi x (x itself: rot NULL), s = max|x'| / 127,
- *   q = round_half_even(x' * (127 / max|x'|)), in float32.
+ *   q = round_half_even(x' * (127 / max|x'|)), in float64; Pi x is summed in
+ *   float64 for F32 rows and in float32 for 16-bit ones.
  * A row of zeros gives s = 0 and codes 0; a row with an infinity or a NaN
  * gives s = NaN and codes 0.  Because W x = (W Pi^T)(Pi x), tokens and
  * weights coded with the same rotation multiply to the layer's product.
@@ -605,8 +606,12 @@ int64_t orbit_paged_attention_workspace(int64_t batch, int64_t q_heads, int64_t 
  * q outside starts[0] .. starts[batch] are left as they were in out and lse;
  * starts must not decrease (which rows are written is otherwise unspecified),
  * and is cut to 0 .. tokens.  Rows with nothing to see, cut lengths, table
- * entries outside the cache, head groups and roundings as in
- * orbit_paged_attention.
+ * entries outside the cache and head groups as in orbit_paged_attention.  A
+ * weight above its sum is a pair of 16-bit numbers as there where requests
+ * have at most 32 rows (new tokens times q_heads / kv_heads) on average, and
+ * one 16-bit number, rounded to nearest, where they have more: within 2^-8 of
+ * the weight (BF16), or 2^-11 (F16, and beside an int8 cache).  The sums below
+ * and lse are of float32 weights in either case.
  * q: [tokens, q_heads, head_dim] by strides, rows 16-byte aligned, BF16 or
  * F16; its type is the cache's, either one for an int8 cache.  out: [tokens,
  * q_heads, head_dim] contiguous, of q's type, 16-byte aligned.  lse: float
@@ -614,8 +619,7 @@ int64_t orbit_paged_attention_workspace(int64_t batch, int64_t q_heads, int64_t 
  * stride.  lengths: int32 [batch]; starts: int32 [batch + 1]; tree: uint64
  * [tokens, tree_words] contiguous, 1 <= tree_words <= 1024.  batch <= 65535;
  * 0 <= tokens < ORBIT_MAX_ROWS, tokens * q_heads / kv_heads < 2^30; 0 <=
- * window, sinks <= 2^30; table_width *
- * page_size <= 2^30; sm_scale finite.
+ * window, sinks <= 2^30; table_width * page_size <= 2^30; sm_scale finite.
  * workspace: device, 16-byte aligned, orbit_tree_attention_workspace bytes
  * (may be 0), overwritten.
  * Errors: ORBIT_E_ARG, ORBIT_E_SHAPE, ORBIT_E_DTYPE, ORBIT_E_HIP. */

@@ -372,13 +372,13 @@ orbit_status orbit_int8_quant_rows(const orbit_rpbh* rot, const void* X, orbit_d
   a.rows = M;
   a.stride = M > 1 ? x_stride : 0;  // the stride of one row says nothing
   a.d = (int)K;
-  a.inv_sqrt_h = 1.0f;
+  a.inv_sqrt_h = 1.0;
   a.vec = aligned16(X) && a.stride % 8 == 0;
   if (rot) {
     a.perm = rot->perm;
     a.sign_bits = rot->sign_bits;
     a.h = rot->h;
-    a.inv_sqrt_h = (float)(1.0 / std::sqrt((double)rot->h));
+    a.inv_sqrt_h = 1.0 / std::sqrt((double)rot->h);
   }
   return hip_status(orbit::launch_int8_rows(a, x_dtype, rot != nullptr, stream));
 }

@@ -14,10 +14,15 @@
 // goes through an LDS copy of the row; its offsets (with the signs) are kept
 // in registers for all rows of a workgroup.
 //
-// Codes: t = fma(x', 127 / max, 1.5 * 2^23) holds the rounded integer in its
-// low byte (one rounding of the exact product, half to even; |x'| <= max, so
-// there is nothing to clamp).  A row with an infinity or a NaN takes s = NaN
-// and codes 0, so that all that is made of it is NaN.
+// Codes: t = fma(x', 127 / max, 1.5 * 2^52) in float64 holds the rounded
+// integer in its low byte (half to even; |x'| <= max, so there is nothing to
+// clamp).  In float32 the factor's rounding moves x' up to 4e-6 of a step, and
+// a code falls to the wrong side once in some 10^5.  For the same reason
+// float32 rows are rotated in float64; 16-bit rows have 11 bits or fewer of
+// each of the terms, which float32's 24 bits hold without loss but for those
+// some 2^9 times below the block's largest.
+// A row with an infinity or a NaN takes s = NaN and codes 0, so that all that
+// is made of it is NaN.
 #include "block_common.h"
 #include "int8_rows.h"
 
@@ -27,36 +32,72 @@ using namespace orbit::block;
 namespace {
 
 template <int M>
-__device__ __forceinline__ float lane_xor(float v) {
-  const int b = __builtin_bit_cast(int, v);
-  if constexpr (M == 1) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, kXor1, 0xf, 0xf, true));
-  if constexpr (M == 2) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, kXor2, 0xf, 0xf, true));
-  return __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(b, (M << 10) | 0x1f));
+__device__ __forceinline__ int lane_xor(int b) {
+  if constexpr (M == 1) return __builtin_amdgcn_update_dpp(0, b, kXor1, 0xf, 0xf, true);
+  if constexpr (M == 2) return __builtin_amdgcn_update_dpp(0, b, kXor2, 0xf, 0xf, true);
+  return __builtin_amdgcn_ds_swizzle(b, (M << 10) | 0x1f);
 }
-
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 template <int M>
-__device__ __forceinline__ void butterfly(float (&f)[16], int lane) {
+__device__ __forceinline__ float lane_xor(float v) {
+  return __builtin_bit_cast(float, lane_xor<M>(__builtin_bit_cast(int, v)));
+}
+template <int M>
+__device__ __forceinline__ double lane_xor(double v) {
+  const i32x2 b = __builtin_bit_cast(i32x2, v);
+  return __builtin_bit_cast(double, i32x2{lane_xor<M>(b.x), lane_xor<M>(b.y)});
+}
+template <int M, class A>
+__device__ __forceinline__ void butterfly(A (&f)[16], int lane) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    const float o = lane_xor<M>(f[j]);
+    const A o = lane_xor<M>(f[j]);
     f[j] = lane & M ? o - f[j] : f[j] + o;
   }
 }
-__device__ __forceinline__ void butterfly32(float (&f)[16], int lane) {
+// of lane l % 32 and of lane 32 + l % 32
+__device__ __forceinline__ void halves(float v, float& lo, float& hi) {
+  const unsigned u = __builtin_bit_cast(unsigned, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  lo = __builtin_bit_cast(float, (unsigned)r[0]);
+  hi = __builtin_bit_cast(float, (unsigned)r[1]);
+}
+__device__ __forceinline__ void halves(double v, double& lo, double& hi) {
+  const i32x2 b = __builtin_bit_cast(i32x2, v);
+  const auto x = __builtin_amdgcn_permlane32_swap((unsigned)b.x, (unsigned)b.x, false, false);
+  const auto y = __builtin_amdgcn_permlane32_swap((unsigned)b.y, (unsigned)b.y, false, false);
+  lo = __builtin_bit_cast(double, i32x2{(int)x[0], (int)y[0]});
+  hi = __builtin_bit_cast(double, i32x2{(int)x[1], (int)y[1]});
+}
+template <class A>
+__device__ __forceinline__ void butterfly32(A (&f)[16], int lane) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    const unsigned u = __builtin_bit_cast(unsigned, f[j]);
-    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    const float lo = __builtin_bit_cast(float, (unsigned)r[0]), hi = __builtin_bit_cast(float, (unsigned)r[1]);
+    A lo, hi;
+    halves(f[j], lo, hi);
     f[j] = lane & 32 ? lo - hi : lo + hi;
   }
 }
+
+// Magnitudes as bit patterns, which order like the values, infinities and NaN last.
+__device__ __forceinline__ uint32_t size_of(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu; }
+__device__ __forceinline__ uint64_t size_of(double v) { return __builtin_bit_cast(uint64_t, v) & 0x7fffffffffffffffull; }
+__device__ __forceinline__ double value_of(uint32_t b) { return (double)__builtin_bit_cast(float, b); }
+__device__ __forceinline__ double value_of(uint64_t b) { return __builtin_bit_cast(double, b); }
+__device__ __forceinline__ uint32_t other_lane(uint32_t b, int s) { return (uint32_t)__shfl_xor((int)b, s); }
+__device__ __forceinline__ uint64_t other_lane(uint64_t b, int s) { return (uint64_t)__shfl_xor((long long)b, s); }
+
+// What rows are rotated in.
+template <class IT, bool ROT>
+using Sum = std::conditional_t<ROT && std::is_same_v<IT, float>, double, float>;
 
 // NR: rounds of 1024 coordinates per wave; W waves (blockDim / 64) of them.
 template <class IT, bool ROT, int NR>
 __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
   extern __shared__ __align__(16) char smem[];
-  unsigned* const top = (unsigned*)(smem + a.lds_row);  // the waves' maxima, behind the row's copy
+  typedef Sum<IT, ROT> A;
+  typedef decltype(size_of(A())) Size;
+  Size* const top = (Size*)(smem + a.lds_row);  // the waves' maxima, behind the row's copy
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, waves = (int)blockDim.x >> 6;
   // where each coordinate comes from, bit 15: with its sign flipped
   uint32_t from[ROT ? NR : 1][8];
@@ -77,7 +118,7 @@ __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
   const IT* const base = (const IT*)a.in;
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const IT* const x = base + row * a.stride;
-    float f[NR][16];
+    A f[NR][16];
     if constexpr (ROT) {
       IT* const copy = (IT*)smem;
       if (a.vec) {
@@ -109,10 +150,10 @@ __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
           }
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) f[r][j] = k0 < a.d ? (float)v[j >> 3].e[j & 7] : 0.0f;
+        for (int j = 0; j < 16; ++j) f[r][j] = k0 < a.d ? (A)v[j >> 3].e[j & 7] : (A)0;
       }
     }
-    unsigned m = 0;  // bit patterns of |x'| order like the values, infinities and NaN last
+    Size m = 0;
     if constexpr (ROT) {
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
@@ -122,7 +163,7 @@ __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             if (!(j & s)) {
-              const float p = f[r][j], q = f[r][j | s];
+              const A p = f[r][j], q = f[r][j | s];
               f[r][j] = p + q;
               f[r][j | s] = p - q;
             }
@@ -137,14 +178,14 @@ __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
         // rows of at most 4096: a round is a wave's, its block's others are the neighbouring waves'
 #pragma unroll 1
         for (int s = 1; s * 1024 < a.h; s *= 2) {
-          float* const all = (float*)smem;  // [wave][j][lane], over the row's copy
+          A* const all = (A*)smem;  // [wave][j][lane], over the row's copy
           __syncthreads();
 #pragma unroll
           for (int j = 0; j < 16; ++j) all[(wave * 16 + j) * 64 + lane] = f[0][j];
           __syncthreads();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float o = all[((wave ^ s) * 16 + j) * 64 + lane];
+            const A o = all[((wave ^ s) * 16 + j) * 64 + lane];
             f[0][j] = wave & s ? o - f[0][j] : f[0][j] + o;
           }
         }
@@ -155,13 +196,13 @@ __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
       const bool in = (r * waves + wave) * 1024 + lane * 16 < a.d;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const unsigned b = __builtin_bit_cast(unsigned, f[r][j]) & 0x7fffffffu;
+        const Size b = size_of(f[r][j]);
         m = in && b > m ? b : m;
       }
     }
 #pragma unroll
     for (int s = 1; s < 64; s *= 2) {
-      const unsigned o = (unsigned)__shfl_xor((int)m, s);
+      const Size o = other_lane(m, s);
       m = o > m ? o : m;
     }
     if (waves > 1) {
@@ -170,20 +211,24 @@ __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
       m = top[0];
       for (int w = 1; w < waves; ++w) m = top[w] > m ? top[w] : m;
     }
-    const Int8Scale s = int8_scale(m, a.inv_sqrt_h);
-    if (t == 0) a.s_out[row] = s.s;
-    if (s.pre != 1.0f) {
-#pragma unroll
-      for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) f[r][j] *= s.pre;
-    }
+    const double most = value_of(m);
+    const bool fine = most < __builtin_inf();
+    const float scale = fine ? (float)(most * a.inv_sqrt_h / 127.0) : __builtin_nanf("");
+    if (t == 0) a.s_out[row] = scale;
+    const double inv = scale > 0.0f ? 127.0 / most : 0.0;
+    const uint32_t keep = fine ? 0xffffffffu : 0u;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const int k0 = (r * waves + wave) * 1024 + lane * 16;
       uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = int8_codes(&f[r][4 * j], s);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma((double)f[r][4 * j + i], inv, 6755399441055744.0));
+        const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+        w[j] = (lo | hi) & keep;
+      }
       if (k0 < a.d) *(u32x4*)(a.q_out + row * a.d + k0) = u32x4{w[0], w[1], w[2], w[3]};
     }
     if (ROT || waves > 1) __syncthreads();  // the row's copy and the maxima have been read
@@ -196,10 +241,11 @@ hipError_t launch(Int8RowArgs a, hipStream_t stream) {
   int lds = 0;
   if (ROT) {
     lds = a.d * (int)sizeof(IT);
-    if (a.h > 1024 && lds < waves * 4096) lds = waves * 4096;
+    const int all = waves * 1024 * (int)sizeof(Sum<IT, ROT>);
+    if (a.h > 1024 && lds < all) lds = all;
   }
   a.lds_row = lds;
-  lds += 16;
+  lds += 32;
   // about as many workgroups as are resident, so that the offsets are read
   // once for many rows; unrotated rows have none to keep
   const long long cap = ROT ? (long long)kUnits * (nr == 1 ? 24 / waves : 4) : a.rows;

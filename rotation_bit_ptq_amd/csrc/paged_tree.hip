@@ -28,16 +28,17 @@ bool sizes_ok(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, 
 }
 
 struct Split {
-  bool few;          // one block of 16 rows per wave, and weights in pairs
+  bool few;          // 16 rows per wave, and weights in pairs
   int rows, target;  // of a workgroup; workgroups
   int64_t slots, pieces, groups;  // groups: workgroups of a key head
 };
 
-// Rows per workgroup: two blocks of 16 per wave from 33 rows of a request of
-// average size on (one at head dimensions above 128, whose sums take the
-// registers), so up to 256 or 128.  Pieces: so many that the workgroups fill the chip
-// twice over (four times where two are resident in a unit), but two tiles at
-// least (item_of).
+// Rows per workgroup: 16 to a wave where a request has at most 32 on average,
+// and at head dimensions above 128, whose sums take the registers; otherwise
+// 32 (up to 128 or 256).  Pieces: so many that the workgroups fill the units
+// twice over (four times where two are resident in a unit; 16 trees of 60
+// tokens after up to 8192 took 153, 109, 114, 126 us with one to four times as
+// many workgroups as units), but two tiles at least (item_of).
 Split split_of(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t cap, int64_t window,
                int64_t sinks, bool single) {
   Split s = {};

@@ -7,20 +7,33 @@
 //
 // Rows.  The new tokens of a request and the query heads of one key head are
 // the rows r = token * group + head of one product with its keys.  A workgroup
-// of eight waves takes 16 RB WR rows and a piece of the context: WR waves side
-// by side on the rows (16 RB each), WT on the tokens.  Tiles of 64 tokens (32
-// at head dimensions above 128) go from memory straight to an LDS ring of four
-// stages, eight (four) rows by each wave, and every wave reads what it needs:
-// a tile is read from memory once for all its rows, three are in flight while
-// one is multiplied, and one barrier stands between two.  Codes of an int8
-// cache go through a ring that is the wave's own and become fp16 on their way
-// to tiles in LDS, once for all rows.
+// of eight waves takes up to 8 R rows (R = 16 or 32 to a wave) and a piece of
+// the context: as many waves side by side on the rows as these need, the
+// others on the tokens.  Tiles of 64 tokens (32 at head dimensions above 128)
+// go from memory straight to an LDS ring of four stages, eight (four) rows by
+// each wave, and every wave reads what it needs: a tile is read from memory
+// once for all its rows, two or three are in flight while one is multiplied,
+// and one barrier stands between two.  Codes of an int8 cache go through a
+// ring that is the wave's own and become fp16 on their way to tiles in LDS,
+// once for all rows.
 //
-// Products as in the single-token kernel (paged_attention_impl.h): S^T = K Q^T
-// with the keys as A operand; O^T = V^T P^T with the probabilities in the
-// lanes that computed them, as pairs of 16-bit numbers; V^T by transposing LDS
-// reads.  A lane holds row l % 16 of its block and tokens 4 (l / 16) + i of
-// each half of 32 tokens.
+// Products.  S^T = K Q^T with the keys as A operand; O^T = V^T P^T with the
+// probabilities in the lanes that computed them; V^T by transposing LDS reads.
+// R = 16, where a request has at most 32 rows on average: 16x16x32 products,
+// probabilities as pairs of 16-bit numbers as in the single-token kernel
+// (paged_attention_impl.h).  Those are bound by memory.  R = 32: 32x32x16
+// products and single 16-bit probabilities, half the instructions around a
+// score; from 128 rows on the instructions bound them.  A probability's
+// rounding is relative (within 2^-8 of it in bfloat16), as its value's was.
+//
+// What bounds it, 4096 new of 8192 tokens, 32 + 8 heads of 128, 441 us (935
+// TFLOP/s): vector instructions share a SIMD's issue with matrix ones, four or
+// five cycles each of the 32 that a product takes.  32 x 32 scores cost a wave
+// 16 products, 24 LDS reads and about 100 vector instructions (a product and
+// an exponential each, half a conversion, a sum and half a maximum for each of
+// a lane's 16 scores), 1150 cycles in all; the products alone are 512.
+// 16 prompts of 60 drafted tokens (up to 8192 before them) 98 us (2.7 TB/s),
+// 64 single tokens behind a window of 4096 with sinks 176 us (5.4 TB/s).
 //
 // What a row sees: prefix tokens in [lo, hi) and below `sinks`, and new tokens
 // by the bits of its mask.  A wave whose rows all see all 32 tokens skips the
@@ -223,9 +236,9 @@ constexpr int tree_tile(int dp) { return dp == 256 ? 32 : 64; }
 constexpr int tree_rows(int dp) { return tree_tile(dp) / kTreeWaves; }  // of a tile, by each wave
 // LDS: the 16-bit tiles (keys, then values), the codes' ring and the scales' of
 // more stages (a wave's codes have been read when they are converted, its
-// scales are read by all waves later), and of as many
-// for each stage a word (bits: rows whose page lies outside the cache),
-// whether a wave saw such a page, 32 rows of zeros, and rows' maxima and sums.
+// scales are read by all waves later), for each of as many stages a word
+// (bits: rows whose page lies outside the cache), whether a wave saw such a
+// page, 32 rows of zeros, and rows' maxima and sums.
 constexpr int tree_tiles_lds(int dp, bool coded) { return (tree_key_tiles(coded) + tree_value_tiles(coded)) * tree_tile(dp) * dp * 2; }
 constexpr int tree_raw_stage(int dp) { return 2 * tree_rows(dp) * dp; }    // of a wave
 constexpr int tree_scale_stage(int dp) { return 4 * tree_rows(dp); }
@@ -306,7 +319,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   Item it;
   if (a.pieces > 1) {
     it = item_of(a, item, kTokens, lane);
-    if (it.rq.b < 0) return;
+    if (it.rq.b < 0 || it.piece < 0) return;  // negative: starts that decrease
   } else {
     // the last slots first: in a prompt they have the longest contexts
     const int slot = a.slots - 1 - item, b = request_at(a, slot, lane);

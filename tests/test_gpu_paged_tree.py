@@ -113,6 +113,17 @@ def test_long_contexts_in_pieces(gpu_lib, xt, fmt):
     Case(3, [(30000, 2)], xt=xt, fmt=fmt, H=4, KV=1, window=5000, sinks=300).check(gpu_lib)
 
 
+@pytest.mark.parametrize("requests", [64, 65, 100, 513])  # counted by 64 lanes; from 513 on contexts stay whole
+@pytest.mark.parametrize("xt,fmt", [("bf16", "bf16"), ("f16", "int8")])
+def test_many_requests(gpu_lib, requests, xt, fmt):
+    rng = np.random.default_rng(requests)
+    ns = [int(n) for n in rng.integers(0, 6, requests)]
+    lengths = [n + int(x) for n, x in zip(ns, rng.integers(0, 90, requests))]
+    for b in (0, requests // 2, requests - 1):
+        lengths[b] += 1500
+    Case(requests, list(zip(lengths, ns)), H=4, KV=1, D=64, xt=xt, fmt=fmt, masks=[tree_mask(rng, n) if n else np.zeros((0, 0), bool) for n in ns]).check(gpu_lib)
+
+
 def test_rows_outside_the_requests_stay(gpu_lib):
     c = Case(5, [(40, 3), (0, 0), (200, 70)], lead=4, tail=9)
     before = torch.full_like(c.q, 7.0)

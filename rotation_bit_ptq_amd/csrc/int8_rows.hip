@@ -3,8 +3,8 @@
 //   x' = Pi x (or x),  s = max|x'| / 127,  q = rint(x' * 127 / max|x'|).
 //
 // Bound: memory, one pass: a row stays in registers between the rotation,
-// its maximum and its codes.  4096 bf16 rows of 3072, blocks of 128: 13.7 us
-// (2.8 TB/s); of 16 such rows 4.4 us.
+// its maximum and its codes.  4096 bf16 rows of 3072, blocks of 128: 14.5 us
+// (2.6 TB/s), two thirds of it vector instructions; 16 such rows 4.5 us.
 //
 // A workgroup of up to four waves takes a row in rounds of 1024 coordinates:
 // lane l of a round's wave holds coordinates 16 l .. 16 l + 15, so that four
@@ -47,13 +47,18 @@ __device__ __forceinline__ double lane_xor(double v) {
   const i32x2 b = __builtin_bit_cast(i32x2, v);
   return __builtin_bit_cast(double, i32x2{lane_xor<M>(b.x), lane_xor<M>(b.y)});
 }
+// with the sign bit flipped where `sign` is 2^31
+__device__ __forceinline__ float flipped(float v, uint32_t sign) { return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) ^ sign); }
+__device__ __forceinline__ double flipped(double v, uint32_t sign) {
+  i32x2 b = __builtin_bit_cast(i32x2, v);
+  b.y ^= (int)sign;
+  return __builtin_bit_cast(double, b);
+}
 template <int M, class A>
 __device__ __forceinline__ void butterfly(A (&f)[16], int lane) {
+  const uint32_t sign = lane & M ? 0x80000000u : 0u;  // the upper one's own is subtracted
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const A o = lane_xor<M>(f[j]);
-    f[j] = lane & M ? o - f[j] : f[j] + o;
-  }
+  for (int j = 0; j < 16; ++j) f[j] = lane_xor<M>(f[j]) + flipped(f[j], sign);
 }
 // of lane l % 32 and of lane 32 + l % 32
 __device__ __forceinline__ void halves(float v, float& lo, float& hi) {
@@ -87,19 +92,26 @@ __device__ __forceinline__ double value_of(uint64_t b) { return __builtin_bit_ca
 __device__ __forceinline__ uint32_t other_lane(uint32_t b, int s) { return (uint32_t)__shfl_xor((int)b, s); }
 __device__ __forceinline__ uint64_t other_lane(uint64_t b, int s) { return (uint64_t)__shfl_xor((long long)b, s); }
 
+// A barrier for LDS alone: loads and stores of memory may be on their way.
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // What rows are rotated in.
 template <class IT, bool ROT>
 using Sum = std::conditional_t<ROT && std::is_same_v<IT, float>, double, float>;
 
 // NR: rounds of 1024 coordinates per wave; W waves (blockDim / 64) of them.
 template <class IT, bool ROT, int NR>
-__global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
+__global__ __launch_bounds__(256, NR == 1 ? 5 : 1) void rows_kernel(Int8RowArgs a) {
   extern __shared__ __align__(16) char smem[];
   typedef Sum<IT, ROT> A;
   typedef decltype(size_of(A())) Size;
   Size* const top = (Size*)(smem + a.lds_row);  // the waves' maxima, behind the row's copy
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, waves = (int)blockDim.x >> 6;
-  // where each coordinate comes from, bit 15: with its sign flipped
+  // where each coordinate comes from (times two, in 15 bits), bit 15: with its sign flipped
   uint32_t from[ROT ? NR : 1][8];
   if constexpr (ROT) {
 #pragma unroll
@@ -111,7 +123,7 @@ __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
         const uint32_t sign = a.sign_bits[k0 >> 5] >> (k0 & 31);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          from[r][j >> 1] |= ((uint32_t)a.perm[k0 + j] | ((sign >> j) & 1u) << 15) << (16 * (j & 1));
+          from[r][j >> 1] |= ((uint32_t)a.perm[k0 + j] << 1 | ((sign >> j) & 1u) << 15) << (16 * (j & 1));
       }
     }
   }
@@ -126,14 +138,18 @@ __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
       } else {
         for (int i = t; i < a.d; i += (int)blockDim.x) copy[i] = x[i];
       }
-      __syncthreads();
+      meet();
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const uint32_t w = from[r][j >> 1] >> (16 * (j & 1));
-          const float v = (float)copy[w & 0x3fffu];
-          f[r][j] = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) ^ ((w & 0x8000u) << 16));
+          if constexpr (sizeof(IT) == 2) {
+            const uint16_t v = *(const uint16_t*)(smem + (w & 0x7fffu));
+            f[r][j] = (float)__builtin_bit_cast(IT, (uint16_t)(v ^ (w & 0x8000u)));
+          } else {
+            f[r][j] = flipped(*(const float*)(smem + (w & 0x7fffu) * 2), (w & 0x8000u) << 16);
+          }
         }
     } else {
 #pragma unroll
@@ -179,10 +195,10 @@ __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
 #pragma unroll 1
         for (int s = 1; s * 1024 < a.h; s *= 2) {
           A* const all = (A*)smem;  // [wave][j][lane], over the row's copy
-          __syncthreads();
+          meet();
 #pragma unroll
           for (int j = 0; j < 16; ++j) all[(wave * 16 + j) * 64 + lane] = f[0][j];
-          __syncthreads();
+          meet();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const A o = all[((wave ^ s) * 16 + j) * 64 + lane];
@@ -193,12 +209,13 @@ __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const bool in = (r * waves + wave) * 1024 + lane * 16 < a.d;
+      Size of_round = 0;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const Size b = size_of(f[r][j]);
-        m = in && b > m ? b : m;
+        of_round = b > of_round ? b : of_round;
       }
+      if ((r * waves + wave) * 1024 + lane * 16 < a.d) m = of_round > m ? of_round : m;
     }
 #pragma unroll
     for (int s = 1; s < 64; s *= 2) {
@@ -207,7 +224,7 @@ __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
     }
     if (waves > 1) {
       if (lane == 0) top[wave] = m;
-      __syncthreads();  // and every lane has gathered: the copy may be overwritten
+      meet();  // and every lane has gathered: the copy may be overwritten
       m = top[0];
       for (int w = 1; w < waves; ++w) m = top[w] > m ? top[w] : m;
     }
@@ -231,7 +248,7 @@ __global__ __launch_bounds__(256) void rows_kernel(Int8RowArgs a) {
       }
       if (k0 < a.d) *(u32x4*)(a.q_out + row * a.d + k0) = u32x4{w[0], w[1], w[2], w[3]};
     }
-    if (ROT || waves > 1) __syncthreads();  // the row's copy and the maxima have been read
+    if (ROT || waves > 1) meet();  // the row's copy and the maxima have been read
   }
 }
 
@@ -246,9 +263,10 @@ hipError_t launch(Int8RowArgs a, hipStream_t stream) {
   }
   a.lds_row = lds;
   lds += 32;
-  // about as many workgroups as are resident, so that the offsets are read
+  // as many workgroups as are resident (five waves to a SIMD, by their registers:
+  // 51.0 us with the product, 52.8 with 24 waves to a unit), so that the offsets are read
   // once for many rows; unrotated rows have none to keep
-  const long long cap = ROT ? (long long)kUnits * (nr == 1 ? 24 / waves : 4) : a.rows;
+  const long long cap = ROT ? (long long)kUnits * (nr == 1 ? 20 / waves : 4) : a.rows;
   const dim3 grid((unsigned)(a.rows < cap ? a.rows : cap)), block(64 * waves);
   hipError_t e = hipSuccess;
   auto go = [&](auto n) {

@@ -21,7 +21,10 @@ Between those layers: norms around a branch with its gate and residual scale
 (block_norm), low-rank adapters of many requests beside a shared projection
 (adapter_add), and a paged key-value cache, 16-bit or rotate-then-quantize
 int8 (kv_append, kv_read), with the attention of one new token that reads it
-(paged_attention).
+(paged_attention), or of several: prompts, chains and trees of drafted tokens
+(paged_tree_attention).  Queries and keys may be normed for each head on the
+way (qk_norm, kv_append(norm=...)), and a layer's tokens coded in 8 bits for a
+product with weights coded alike (int8_quant_rows, int8_qlinear).
 """
 from __future__ import annotations
 

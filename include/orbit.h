@@ -497,7 +497,7 @@ orbit_status orbit_kv_append(const orbit_kv_append_args *args, hipStream_t strea
 typedef struct {
   const void *q_weight, *k_weight;
   int64_t q_weight_stride, k_weight_stride; /* elements */
-  int32_t w_dtype, norm;                    /* orbit_dtype, orbit_norm (not NONE) */
+  int32_t w_dtype, norm;                    /* orbit_dtype; RMS or LAYER */
   float eps;
 } orbit_head_norm;
 

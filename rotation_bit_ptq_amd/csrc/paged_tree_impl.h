@@ -227,24 +227,25 @@ struct TreeStage {
 };
 
 constexpr int kTreeWaves = 8;
-constexpr int kTreeWords = 8;  // stages of the scales and the words
+constexpr int kTreeWords = 8;  // stages of the words
 constexpr int kTreeStages = 4;
 constexpr int kJoinMost = 256;  // threads of a workgroup that joins
 constexpr int tree_key_tiles(bool coded) { return coded ? 2 : kTreeStages; }
 constexpr int tree_value_tiles(bool coded) { return coded ? 3 : kTreeStages; }  // values are read a step later
 constexpr int tree_tile(int dp) { return dp == 256 ? 32 : 64; }
 constexpr int tree_rows(int dp) { return tree_tile(dp) / kTreeWaves; }  // of a tile, by each wave
-// LDS: the 16-bit tiles (keys, then values), the codes' ring and the scales' of
-// more stages (a wave's codes have been read when they are converted, its
-// scales are read by all waves later), for each of as many stages a word
-// (bits: rows whose page lies outside the cache), whether a wave saw such a
-// page, 32 rows of zeros, and rows' maxima and sums.
+// LDS: the 16-bit tiles (keys, then values), an int8 cache's codes and scales
+// in the waves' own rings, what is made of the scales (float32: the keys', the
+// values' and their logarithms), for each stage a word (bits: rows whose page
+// lies outside the cache) and another (bytes: a wave's scales that are infinite
+// or NaN), whether a wave saw such a page, 32 rows of zeros, and rows' maxima
+// and sums.
 constexpr int tree_tiles_lds(int dp, bool coded) { return (tree_key_tiles(coded) + tree_value_tiles(coded)) * tree_tile(dp) * dp * 2; }
 constexpr int tree_raw_stage(int dp) { return 2 * tree_rows(dp) * dp; }    // of a wave
 constexpr int tree_scale_stage(int dp) { return 4 * tree_rows(dp); }
 constexpr int tree_lds(int dp, bool coded) {
   return tree_tiles_lds(dp, coded) +
-         (coded ? kTreeWaves * (kTreeStages * tree_raw_stage(dp) + kTreeWords * tree_scale_stage(dp)) : 0) + kTreeWords * 8 +
+         (coded ? kTreeStages * (kTreeWaves * (tree_raw_stage(dp) + tree_scale_stage(dp)) + 12 * tree_tile(dp)) : 0) + kTreeWords * 16 +
          kTreeWaves * 4 + 511 + (dp <= 128 ? 32 * dp * 2 : 0) + kTreeWaves * 32 * 8;
 }
 alignas(16) static __device__ const uint32_t kTreeZeros[4] = {0, 0, 0, 0};  // what is read in the place of tokens that are not there
@@ -305,8 +306,9 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   constexpr int kTileBytes = kTokens * DP * 2, kValuesAt = kKeyTiles * kTileBytes, kRaw = tree_raw_stage(DP);
   constexpr int kScale = tree_scale_stage(DP);
   constexpr uint32_t kRawAt = tree_tiles_lds(DP, kCoded), kScaleAt = kRawAt + (kCoded ? S * kTreeWaves * kRaw : 0),
-                     kGoneAt = kScaleAt + (kCoded ? kTreeWords * kTreeWaves * kScale : 0),
-                     kZerosAt = (kGoneAt + kTreeWords * 8 + kTreeWaves * 4 + 511) / 512 * 512,
+                     kMadeAt = kScaleAt + (kCoded ? S * kTreeWaves * kScale : 0), kGoneAt = kMadeAt + (kCoded ? S * kTokens * 12 : 0),
+                     kOddAt = kGoneAt + kTreeWords * 8, kSawAt = kOddAt + kTreeWords * 8,
+                     kZerosAt = (kSawAt + kTreeWaves * 4 + 511) / 512 * 512,
                      kSumsAt = kZerosAt + (DP <= 128 ? 32 * DP * 2 : 0);
   static_assert(tree_tiles_lds(DP, kCoded) + (kCoded ? S * kTreeWaves * kRaw : 0) >= kTreeWaves * R * DP * 4);  // sums, at the end
   extern __shared__ __align__(1024) char lds[];
@@ -430,7 +432,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     const uint32_t to = kCoded ? kRawAt + (uint32_t)(stage * kTreeWaves + wave) * kRaw
                                : (uint32_t)stage * kTileBytes + (uint32_t)wave * kRows * DP * 2;
     constexpr uint32_t kValues = kCoded ? kRows * DP : kValuesAt;
-    const uint32_t to_scales = kScaleAt + ((uint32_t)k % kTreeWords * kTreeWaves + wave) * kScale;
+    const uint32_t to_scales = kScaleAt + ((uint32_t)k % S * kTreeWaves + wave) * kScale;
     uint32_t gone = 0;  // of this wave's rows
     if (plain && page < a.c.pages && t0 + kRows <= hi_all) {
       const long long row = cache_row(a.c, page, head, (uint32_t)t0 & a.c.page_mask);
@@ -478,7 +480,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     }
     if (lane == 0) ((uint8_t*)(lds + kGoneAt))[(uint32_t)k % kTreeWords * 8 + wave] = (uint8_t)gone;
   };
-  // INT8: this wave's rows of tile k become fp16
+  // INT8: this wave's rows of tile k become fp16, and their scales float32
   auto convert = [&](int k) {
     const char* const raw = lds + kRawAt + (uint32_t)(((uint32_t)k % S) * kTreeWaves + wave) * kRaw;
 #pragma unroll
@@ -497,6 +499,18 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
         *(u32x4*)(to_v + at) = u32x4{z.x, z.y, w.x, w.y};
       }
     }
+    bool odd = false;
+    if (lane < kRows) {
+      const char* const from = lds + kScaleAt + ((uint32_t)k % S * kTreeWaves + wave) * kScale + lane * 2;
+      const float x = (float)*(const _Float16*)from, y = (float)*(const _Float16*)(from + 2 * kRows);
+      float* const made = (float*)(lds + kMadeAt) + (uint32_t)k % S * (3 * kTokens) + wave * kRows + lane;
+      made[0] = x;
+      made[kTokens] = y;
+      made[2 * kTokens] = __builtin_amdgcn_logf(fmaxf(y, 5.9604645e-8f));
+      odd = y - y != 0.0f;
+    }
+    const bool some = __any(odd);
+    if (lane == 0) ((uint8_t*)(lds + kOddAt))[(uint32_t)k % kTreeWords * 8 + wave] = some;
   };
   // this wave's loads have landed
   auto landed = [&](int later) {  // but for those of the `later` last tiles
@@ -724,11 +738,11 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   if constexpr (kWide) {
     for (int x = tid; x < 32 * DP * 2 / 16; x += 64 * kTreeWaves) *(u32x4*)(lds + kZerosAt + x * 16) = u32x4{0u, 0u, 0u, 0u};
   }
-  if (lane == 0) ((uint32_t*)(lds + kGoneAt + kTreeWords * 8))[wave] = 0;
-  if (__any(bad)) ((uint32_t*)(lds + kGoneAt + kTreeWords * 8))[wave] = 1;
+  if (lane == 0) ((uint32_t*)(lds + kSawAt))[wave] = 0;
+  if (__any(bad)) ((uint32_t*)(lds + kSawAt))[wave] = 1;
   tree_wait<62>();
   meet();
-  const u32x4 bad0 = *(const u32x4*)(lds + kGoneAt + kTreeWords * 8), bad1 = *(const u32x4*)(lds + kGoneAt + kTreeWords * 8 + 16);
+  const u32x4 bad0 = *(const u32x4*)(lds + kSawAt), bad1 = *(const u32x4*)(lds + kSawAt + 16);
   const bool holes = __builtin_amdgcn_readfirstlane(bad0.x | bad0.y | bad0.z | bad0.w | bad1.x | bad1.y | bad1.z | bad1.w) != 0;
   auto fresh = [&] { asm volatile("" : "+v"(kread), "+v"(vread)); };  // the places made of them are not kept in registers
   // A step's tiles, there and ready to be read by all waves.
@@ -754,23 +768,20 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   auto take = [&](float (&z)[kScores], int at, int sub, int ts) {
     float lv[kCoded ? kScores : 1];
     if constexpr (kCoded) {
-      const char* const scales = lds + kScaleAt + (uint32_t)at % kTreeWords * kTreeWaves * kScale;  // of the first wave's rows
-      float odd = 0.0f;
+      const float* const made = (const float*)(lds + kMadeAt) + (uint32_t)at % S * (3 * kTokens) + sub * 32 + g * 4;
 #pragma unroll
       for (int q = 0; q < kQuads; ++q) {
-        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-        const int t = sub * 32 + q * kStride + g * 4;
-        const char* const from = scales + t / kRows * kScale + t % kRows * 2;
-        const h4 x = *(const h4*)from, y = *(const h4*)(from + 2 * kRows);
+        const f32x4 x = *(const f32x4*)(made + q * kStride), y = *(const f32x4*)(made + kTokens + q * kStride),
+                    l = *(const f32x4*)(made + 2 * kTokens + q * kStride);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          vt[q * 4 + i] = (float)y[i];
-          lv[q * 4 + i] = __builtin_amdgcn_logf(fmaxf((float)y[i], 5.9604645e-8f));
-          z[q * 4 + i] *= (float)x[i];
-          odd = fmaf((float)y[i], 0.0f, odd);
+          z[q * 4 + i] *= x[i];
+          vt[q * 4 + i] = y[i];
+          lv[q * 4 + i] = l[i];
         }
       }
-      pend_odd = __any(odd != odd);
+      const uint32_t* const odd = (const uint32_t*)(lds + kOddAt + (uint32_t)at % kTreeWords * 8);
+      pend_odd = __builtin_amdgcn_readfirstlane(kRows == 4 ? odd[0] | odd[1] : odd[sub]) != 0;
       pend_seen = 0xffffffffu;
     }
     if (holes || !((ts >= lo_max || ts + 32 <= a.sinks) && ts + 32 <= hi_min)) {
@@ -963,13 +974,14 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   }
   const float inv = !last ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
   constexpr int kFours = DP / 4, kTogether = 64 / kFours;  // lanes of a row, rows at a time
-#pragma unroll 4
-  for (int r0 = wt * kTogether; r0 < R; r0 += wt_all * kTogether) {
+  auto put = [&](int r0, auto one) {
     const int r = r0 + lane / kFours, u = lane % kFours;
     const long long row = __shfl(row_of, r);
     const float scale = __shfl(inv, r);
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int w = 0; w < wt_all; ++w) v += *(const f32x4*)((const float*)lds + ((w * wrs + wr) * R + r) * DP + (u ^ St::key(r & 15)) * 4);
+    const float* const from = (const float*)lds + (wr * R + r) * DP + (u ^ St::key(r & 15)) * 4;
+    f32x4 v = *(const f32x4*)from;
+    if constexpr (!decltype(one)::value)
+      for (int w = 1; w < wt_all; ++w) v += *(const f32x4*)(from + w * wrs * R * DP);
     if (wr * R + r < rows_here && u * 4 < dim) {
       if (last) {
         struct alignas(8) {
@@ -982,6 +994,13 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
         *(f32x4*)(a.part + (row * a.pieces + it.piece) * dim + u * 4) = v;
       }
     }
+  };
+  if (wt_all == 1) {
+#pragma unroll 4
+    for (int n = 0; n < R / kTogether; ++n) put(n * kTogether, std::true_type{});
+  } else {
+#pragma unroll 1
+    for (int r0 = wt * kTogether; r0 < R; r0 += wt_all * kTogether) put(r0, std::false_type{});
   }
 }
 

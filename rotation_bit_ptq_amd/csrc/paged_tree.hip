@@ -143,10 +143,17 @@ extern "C" orbit_status orbit_tree_attention(const orbit_tree_attention_args* p,
   }
   if (e == hipSuccess && s.pieces > 1) {
     const int64_t rows = p->tokens * p->q_heads;
-    // many rows fill the chip with a wave each
-    const dim3 g((unsigned)rows), threads(rows <= 16 * kUnits ? kJoinMost : 64);
-    if (p->q_dtype == ORBIT_BF16) tree_join_kernel<__bf16><<<g, threads, 0, stream>>>(a);
-    else tree_join_kernel<_Float16><<<g, threads, 0, stream>>>(a);
+    auto join = [&](auto type) {
+      typedef decltype(type) QT;
+      if (rows <= 16 * kUnits) {
+        tree_join_kernel<QT, true><<<dim3((unsigned)rows), dim3(kJoinMost), 0, stream>>>(a);
+      } else {
+        const int groups = kJoinMost / (c.head_dim / 4);
+        tree_join_kernel<QT, false><<<dim3((unsigned)((rows + groups - 1) / groups)), dim3(kJoinMost), 0, stream>>>(a);
+      }
+    };
+    if (p->q_dtype == ORBIT_BF16) join(__bf16());
+    else join(_Float16());
     e = hipGetLastError();
   }
   return hip_status(e);

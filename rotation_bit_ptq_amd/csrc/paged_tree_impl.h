@@ -1004,21 +1004,26 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   }
 }
 
-// Joins the pieces of a row, a workgroup to each: groups of dim / 4 lanes take
-// every so many-th piece, and the first group adds their sums, in a fixed
-// order.  A group's first piece is read before it is known whether there is one.
-template <class QT>
+// Joins the pieces of a row.  A workgroup to each (SHARED): groups of dim / 4
+// lanes take every so many-th piece, and the first group adds their sums, in a
+// fixed order.  Or a group to each, where there are so many rows that groups
+// fill the chip.  A group's first piece is read before it is known whether
+// there is one.
+template <class QT, bool SHARED>
 __global__ __launch_bounds__(kJoinMost) void tree_join_kernel(TreeArgs a) {
-  __shared__ __align__(16) float so[kJoinMost * 4], sm[kJoinMost * 2];
+  __shared__ __align__(16) float so[SHARED ? kJoinMost * 4 : 4], sm[SHARED ? kJoinMost * 2 : 2];
   const int dim = a.c.head_dim, lanes = dim >> 2;
-  const int parts = (int)blockDim.x / lanes, g = (int)threadIdx.x / lanes, t = (int)threadIdx.x - g * lanes;
-  const long long row = blockIdx.x;
+  const int groups = (int)blockDim.x / lanes, at = (int)threadIdx.x / lanes, t = (int)threadIdx.x - at * lanes;
+  const int parts = SHARED ? groups : 1, g = SHARED ? at : 0;
+  const long long rows = (long long)a.tokens * a.q_heads;
+  const long long row = SHARED ? (long long)blockIdx.x : min((long long)blockIdx.x * groups + min(at, groups - 1), rows - 1);
   const float2* const ml = (const float2*)(a.part + a.part_ml) + row * a.pieces;
   const f32x4* const part = (const f32x4*)(a.part + row * a.pieces * dim) + t;
   const int n = ((const int*)(a.part + a.part_n))[row];
   const int from = min(g, a.pieces - 1);
   float2 w = ml[from];
   f32x4 v = part[(long long)from * lanes];
+  if (!SHARED && (at >= groups || (long long)blockIdx.x * groups + at >= rows)) return;
   const int tok = (int)(row / a.q_heads);
   // rows that no request has (behind the last one's) hold no count
   if (tok < start_of(a, 0) || tok >= start_of(a, a.batch)) return;
@@ -1043,26 +1048,30 @@ __global__ __launch_bounds__(kJoinMost) void tree_join_kernel(TreeArgs a) {
       v = part[(long long)c * lanes];
       add();
     }
-    *(f32x4*)(so + (g * lanes + t) * 4) = o;
-    if (t == 0) {
-      sm[2 * g] = m;
-      sm[2 * g + 1] = l;
+    if constexpr (SHARED) {
+      *(f32x4*)(so + (g * lanes + t) * 4) = o;
+      if (t == 0) {
+        sm[2 * g] = m;
+        sm[2 * g + 1] = l;
+      }
     }
   }
-  __syncthreads();
-  if (g != 0) return;
-  const int used = min(n, parts);
-  for (int c = 1; c < used; ++c) m = fmaxf(m, sm[2 * c]);
-  const float m_use = m == -__builtin_inff() ? 0.0f : m;
-  l = 0.0f;
-  o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (SHARED) {
+    __syncthreads();
+    if (g != 0) return;
+    const int used = min(n, parts);
+    for (int c = 1; c < used; ++c) m = fmaxf(m, sm[2 * c]);
+    const float m_use = m == -__builtin_inff() ? 0.0f : m;
+    l = 0.0f;
+    o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-  for (int c = 0; c < used; ++c) {
-    const float e = factor(sm[2 * c] - m_use);
-    const f32x4 x = *(const f32x4*)(so + (c * lanes + t) * 4);
-    l = fmaf(e, sm[2 * c + 1], l);
+    for (int c = 0; c < used; ++c) {
+      const float e = factor(sm[2 * c] - m_use);
+      const f32x4 x = *(const f32x4*)(so + (c * lanes + t) * 4);
+      l = fmaf(e, sm[2 * c + 1], l);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = fmaf(e, x[j], o[j]);
+      for (int j = 0; j < 4; ++j) o[j] = fmaf(e, x[j], o[j]);
+    }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   struct alignas(8) {

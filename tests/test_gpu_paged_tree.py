@@ -124,6 +124,12 @@ def test_many_requests(gpu_lib, requests, xt, fmt):
     Case(requests, list(zip(lengths, ns)), H=4, KV=1, D=64, xt=xt, fmt=fmt, masks=[tree_mask(rng, n) if n else np.zeros((0, 0), bool) for n in ns]).check(gpu_lib)
 
 
+@pytest.mark.parametrize("D", [48, 80, 128, 256])
+@pytest.mark.parametrize("xt,fmt", [("bf16", "bf16"), ("f16", "int8")])
+def test_many_rows_in_pieces(gpu_lib, D, xt, fmt):
+    Case(D, [(2500, 131), (40, 0), (1500, 7)], H=32, KV=1, D=D, xt=xt, fmt=fmt, lead=1, tail=2).check(gpu_lib)  # 4512 rows
+
+
 def test_rows_outside_the_requests_stay(gpu_lib):
     c = Case(5, [(40, 3), (0, 0), (200, 70)], lead=4, tail=9)
     before = torch.full_like(c.q, 7.0)

@@ -626,6 +626,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   bool pend_odd = false;  // INT8: some of the values' scales are infinite or NaN
   uint32_t pend_seen = 0;
 
+  // The operands' places: `lds` is at LDS's beginning, and its address would be added to each.
+  typedef const __attribute__((address_space(3))) u32x4* lds_16;
   V8 ph[kScores / 8], pl[PAIR ? kScores / 8 : 1];
   // Scores of 32 tokens (SCORES), and weights of the pending ones (WEIGHTS), a
   // part of both at a time: the weights' instructions stand between the keys'
@@ -649,7 +651,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     auto read_keys = [&](int i) {
 #pragma unroll
       for (int h = 0; h < (kWide ? 1 : 2); ++h)
-        kv[i % (kAheadK + 1)][h] = __builtin_bit_cast(V8, *(const u32x4*)(lds + ((keys ^ (i * G << 4)) + h * 16 * DP * 2 + decltype(skip)::value)));
+        kv[i % (kAheadK + 1)][h] = __builtin_bit_cast(V8, *(lds_16)(uint32_t)((keys ^ (i * G << 4)) + h * 16 * DP * 2 + decltype(skip)::value));
     };
     if constexpr (SCORES) {
 #pragma unroll
@@ -684,7 +686,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
 #pragma unroll
         for (int h = 0; h < (kWide ? 1 : 2); ++h) acc[h] = tree_mma(kv[i % (kAheadK + 1)][h], qf[i], acc[h]);
       }
-      if constexpr (SCORES && WEIGHTS) __builtin_amdgcn_sched_barrier(0);
+      if constexpr (SCORES) __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (SCORES) {
 #pragma unroll
@@ -711,8 +713,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     auto read = [&](int n) {
       const int d = kWide ? n >> 1 : n, m = kWide ? n & 1 : 0;
       const int at = values ^ (d * (R / 8) << 4);
-      u[n % (kAheadV + 1)].h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + (at + m * 16 * DP * 2)));
-      u[n % (kAheadV + 1)].h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + ((at ^ (kOther << 4)) + (m * 16 + kFar) * DP * 2)));
+      u[n % (kAheadV + 1)].h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uint32_t)(at + m * 16 * DP * 2));
+      u[n % (kAheadV + 1)].h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uint32_t)((at ^ (kOther << 4)) + (m * 16 + kFar) * DP * 2));
     };
 #pragma unroll
     for (int n = 0; n < kAheadV && n < kAll; ++n) read(n);

@@ -26,13 +26,14 @@
 // score; from 128 rows on the instructions bound them.  A probability's
 // rounding is relative (within 2^-8 of it in bfloat16), as its value's was.
 //
-// What bounds it, 4096 new of 8192 tokens, 32 + 8 heads of 128, 441 us (935
+// What bounds it, 4096 new of 8192 tokens, 32 + 8 heads of 128, 440 us (937
 // TFLOP/s): vector instructions share a SIMD's issue with matrix ones, four or
 // five cycles each of the 32 that a product takes.  32 x 32 scores cost a wave
 // 16 products, 24 LDS reads and about 100 vector instructions (a product and
 // an exponential each, half a conversion, a sum and half a maximum for each of
 // a lane's 16 scores), 1150 cycles in all; the products alone are 512.
-// 16 prompts of 60 drafted tokens (up to 8192 before them) 98 us (2.7 TB/s),
+// 16 trees of up to 60 drafted tokens after up to 8192 take 94 us (2.8 TB/s),
+// 8 of 16 after up to 65000 in an int8 cache 156 us (2.0 TB/s),
 // 64 single tokens behind a window of 4096 with sinks 176 us (5.4 TB/s).
 //
 // What a row sees: prefix tokens in [lo, hi) and below `sinks`, and new tokens
@@ -531,7 +532,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
   // way to yet: behind the tiles in flight, or (INT8) where codes will be
   // converted to, from the first barrier on.
   Vec8<QT> q8[kSteps];
-  constexpr int kUnits = DP / 8;  // 16-byte units of a row
+  constexpr int kRowUnits = DP / 8;  // 16-byte units of a row
   {
     const long long at = (long long)token * a.qts + qhead * a.qhs;
 #pragma unroll
@@ -539,8 +540,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
       int r = rl, d = (s * G + g) * 8;
       long long from = at;
       if constexpr (kWide) {
-        r = s * (64 / kUnits) + lane / kUnits;
-        d = lane % kUnits * 8;
+        r = s * (64 / kRowUnits) + lane / kRowUnits;
+        d = lane % kRowUnits * 8;
         from = __shfl(at, r);
       }
 #pragma unroll
@@ -567,8 +568,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
       char* const mine = lds + (kCoded ? wave * R * DP * 2 : wave / 4 * kValuesAt + (k0 + 2 + wave / 2 % 2) % S * kTileBytes + wave % 2 * R * DP * 2);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int r = s * (64 / kUnits) + lane / kUnits;
-        *(Vec8<QT>*)(mine + r * DP * 2 + ((lane % kUnits ^ St::key(r & 15)) << 4)) = q8[s];
+        const int r = s * (64 / kRowUnits) + lane / kRowUnits;
+        *(Vec8<QT>*)(mine + r * DP * 2 + ((lane % kRowUnits ^ St::key(r & 15)) << 4)) = q8[s];
       }
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) q8[s] = *(const Vec8<QT>*)(mine + rl * DP * 2 + (((s * G + g) ^ St::key(rl & 15)) << 4));

@@ -6,13 +6,15 @@
 // its maximum and its codes.  4096 bf16 rows of 3072, blocks of 128: 14.5 us
 // (2.6 TB/s), two thirds of it vector instructions; 16 such rows 4.5 us.
 //
-// A workgroup of up to four waves takes a row in rounds of 1024 coordinates:
-// lane l of a round's wave holds coordinates 16 l .. 16 l + 15, so that four
-// of the Hadamard's stages are in registers, six between lanes, and codes
-// leave as 16-byte words.  Blocks of 2048 and 4096 (rows of at most 4096)
-// take their last two stages between the waves, through LDS.  The gather
-// goes through an LDS copy of the row; its offsets (with the signs) are kept
-// in registers for all rows of a workgroup.
+// A workgroup takes a row at a time, a wave of it 1024 coordinates: lane l
+// holds coordinates 16 l .. 16 l + 15 of those, so that four of the Hadamard's
+// stages are in registers, six between lanes, and codes leave as 16-byte
+// words.  Blocks of 2048 and 4096 take their last two stages between the
+// waves, through LDS.  The gather goes through an LDS copy of the row; its
+// offsets (with the signs) are kept in registers for all rows of a workgroup.
+// Rows of 4352 (9164, fp16) take 53 us, and took 69 by four waves in rounds; of
+// 6336 (13404, fp16) 82 and 100, of 12288 (4096, bf16) 58 and 54, of 16384
+// (2048, float32) 58 and 86.
 //
 // Codes: t = fma(x', 127 / max, 1.5 * 2^52) in float64 holds the rounded
 // integer in its low byte (half to even; |x'| <= max, so there is nothing to
@@ -103,34 +105,31 @@ __device__ __forceinline__ void meet() {
 template <class IT, bool ROT>
 using Sum = std::conditional_t<ROT && std::is_same_v<IT, float>, double, float>;
 
-// NR: rounds of 1024 coordinates per wave; W waves (blockDim / 64) of them.
-template <class IT, bool ROT, int NR>
-__global__ __launch_bounds__(256, NR == 1 ? 5 : 1) void rows_kernel(Int8RowArgs a) {
+// A wave for each 1024 coordinates of a row, up to 16.
+template <class IT, bool ROT>
+__global__ __launch_bounds__(1024, (std::is_same_v<Sum<IT, ROT>, double> ? 4 : 5)) void rows_kernel(Int8RowArgs a) {
   extern __shared__ __align__(16) char smem[];
   typedef Sum<IT, ROT> A;
   typedef decltype(size_of(A())) Size;
   Size* const top = (Size*)(smem + a.lds_row);  // the waves' maxima, behind the row's copy
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, waves = (int)blockDim.x >> 6;
   // where each coordinate comes from (times two, in 15 bits), bit 15: with its sign flipped
-  uint32_t from[ROT ? NR : 1][8];
+  uint32_t from[8];
   if constexpr (ROT) {
+    const int k0 = wave * 1024 + lane * 16;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const int k0 = (r * waves + wave) * 1024 + lane * 16;
+    for (int j = 0; j < 8; ++j) from[j] = 0;
+    if (k0 < a.d) {
+      const uint32_t sign = a.sign_bits[k0 >> 5] >> (k0 & 31);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) from[r][j] = 0;
-      if (k0 < a.d) {
-        const uint32_t sign = a.sign_bits[k0 >> 5] >> (k0 & 31);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          from[r][j >> 1] |= ((uint32_t)a.perm[k0 + j] << 1 | ((sign >> j) & 1u) << 15) << (16 * (j & 1));
-      }
+      for (int j = 0; j < 16; ++j)
+        from[j >> 1] |= ((uint32_t)a.perm[k0 + j] << 1 | ((sign >> j) & 1u) << 15) << (16 * (j & 1));
     }
   }
   const IT* const base = (const IT*)a.in;
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const IT* const x = base + row * a.stride;
-    A f[NR][16];
+    A f[16];
     if constexpr (ROT) {
       IT* const copy = (IT*)smem;
       if (a.vec) {
@@ -140,83 +139,68 @@ __global__ __launch_bounds__(256, NR == 1 ? 5 : 1) void rows_kernel(Int8RowArgs 
       }
       meet();
 #pragma unroll
-      for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint32_t w = from[r][j >> 1] >> (16 * (j & 1));
-          if constexpr (sizeof(IT) == 2) {
-            const uint16_t v = *(const uint16_t*)(smem + (w & 0x7fffu));
-            f[r][j] = (float)__builtin_bit_cast(IT, (uint16_t)(v ^ (w & 0x8000u)));
-          } else {
-            f[r][j] = flipped(*(const float*)(smem + (w & 0x7fffu) * 2), (w & 0x8000u) << 16);
-          }
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t w = from[j >> 1] >> (16 * (j & 1));
+        if constexpr (sizeof(IT) == 2) {
+          const uint16_t v = *(const uint16_t*)(smem + (w & 0x7fffu));
+          f[j] = (float)__builtin_bit_cast(IT, (uint16_t)(v ^ (w & 0x8000u)));
+        } else {
+          f[j] = flipped(*(const float*)(smem + (w & 0x7fffu) * 2), (w & 0x8000u) << 16);
         }
-    } else {
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const int k0 = (r * waves + wave) * 1024 + lane * 16;
-        Vec8<IT> v[2];
-        if (k0 < a.d) {
-          if (a.vec) {
-            v[0] = *(const Vec8<IT>*)(x + k0);
-            v[1] = *(const Vec8<IT>*)(x + k0 + 8);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j >> 3].e[j & 7] = x[k0 + j];
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) f[r][j] = k0 < a.d ? (A)v[j >> 3].e[j & 7] : (A)0;
       }
+    } else {
+      const int k0 = wave * 1024 + lane * 16;
+      Vec8<IT> v[2];
+      if (k0 < a.d) {
+        if (a.vec) {
+          v[0] = *(const Vec8<IT>*)(x + k0);
+          v[1] = *(const Vec8<IT>*)(x + k0 + 8);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j >> 3].e[j & 7] = x[k0 + j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] = k0 < a.d ? (A)v[j >> 3].e[j & 7] : (A)0;
     }
     Size m = 0;
     if constexpr (ROT) {
+      // lanes past the row hold the first coordinate again, and whole blocks of it: cleared below
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        // lanes past the row hold the first coordinate again, and whole blocks of it: cleared below
+      for (int s = 1; s < 16; s *= 2)
 #pragma unroll
-        for (int s = 1; s < 16; s *= 2)
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (!(j & s)) {
-              const A p = f[r][j], q = f[r][j | s];
-              f[r][j] = p + q;
-              f[r][j | s] = p - q;
-            }
-        if (a.h > 16) butterfly<1>(f[r], lane);
-        if (a.h > 32) butterfly<2>(f[r], lane);
-        if (a.h > 64) butterfly<4>(f[r], lane);
-        if (a.h > 128) butterfly<8>(f[r], lane);
-        if (a.h > 256) butterfly<16>(f[r], lane);
-        if (a.h > 512) butterfly32(f[r], lane);
-      }
-      if constexpr (NR == 1) {
-        // rows of at most 4096: a round is a wave's, its block's others are the neighbouring waves'
-#pragma unroll 1
-        for (int s = 1; s * 1024 < a.h; s *= 2) {
-          A* const all = (A*)smem;  // [wave][j][lane], over the row's copy
-          meet();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) all[(wave * 16 + j) * 64 + lane] = f[0][j];
-          meet();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const A o = all[((wave ^ s) * 16 + j) * 64 + lane];
-            f[0][j] = wave & s ? o - f[0][j] : f[0][j] + o;
+        for (int j = 0; j < 16; ++j)
+          if (!(j & s)) {
+            const A p = f[j], q = f[j | s];
+            f[j] = p + q;
+            f[j | s] = p - q;
           }
+      if (a.h > 16) butterfly<1>(f, lane);
+      if (a.h > 32) butterfly<2>(f, lane);
+      if (a.h > 64) butterfly<4>(f, lane);
+      if (a.h > 128) butterfly<8>(f, lane);
+      if (a.h > 256) butterfly<16>(f, lane);
+      if (a.h > 512) butterfly32(f, lane);
+#pragma unroll 1
+      for (int s = 1; s * 1024 < a.h; s *= 2) {  // between neighbouring waves
+        A* const all = (A*)smem;                 // [wave][j][lane], over the row's copy
+        meet();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) all[(wave * 16 + j) * 64 + lane] = f[j];
+        meet();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const A o = all[((wave ^ s) * 16 + j) * 64 + lane];
+          f[j] = wave & s ? o - f[j] : f[j] + o;
         }
       }
     }
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      Size of_round = 0;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const Size b = size_of(f[r][j]);
-        of_round = b > of_round ? b : of_round;
-      }
-      if ((r * waves + wave) * 1024 + lane * 16 < a.d) m = of_round > m ? of_round : m;
+    for (int j = 0; j < 16; ++j) {
+      const Size b = size_of(f[j]);
+      m = b > m ? b : m;
     }
+    if (wave * 1024 + lane * 16 >= a.d) m = 0;
 #pragma unroll
     for (int s = 1; s < 64; s *= 2) {
       const Size o = other_lane(m, s);
@@ -234,27 +218,24 @@ __global__ __launch_bounds__(256, NR == 1 ? 5 : 1) void rows_kernel(Int8RowArgs 
     if (t == 0) a.s_out[row] = scale;
     const double inv = scale > 0.0f ? 127.0 / most : 0.0;
     const uint32_t keep = fine ? 0xffffffffu : 0u;
+    const int k0 = wave * 1024 + lane * 16;
+    uint32_t w[4];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const int k0 = (r * waves + wave) * 1024 + lane * 16;
-      uint32_t w[4];
+    for (int j = 0; j < 4; ++j) {
+      uint32_t b[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma((double)f[r][4 * j + i], inv, 6755399441055744.0));
-        const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
-        w[j] = (lo | hi) & keep;
-      }
-      if (k0 < a.d) *(u32x4*)(a.q_out + row * a.d + k0) = u32x4{w[0], w[1], w[2], w[3]};
+      for (int i = 0; i < 4; ++i) b[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma((double)f[4 * j + i], inv, 6755399441055744.0));
+      const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+      w[j] = (lo | hi) & keep;
     }
+    if (k0 < a.d) *(u32x4*)(a.q_out + row * a.d + k0) = u32x4{w[0], w[1], w[2], w[3]};
     if (ROT || waves > 1) meet();  // the row's copy and the maxima have been read
   }
 }
 
 template <class IT, bool ROT>
 hipError_t launch(Int8RowArgs a, hipStream_t stream) {
-  const int rounds = (a.d + 1023) / 1024, waves = rounds < 4 ? rounds : 4, nr = (rounds + waves - 1) / waves;
+  const int waves = (a.d + 1023) / 1024;
   int lds = 0;
   if (ROT) {
     lds = a.d * (int)sizeof(IT);
@@ -262,26 +243,18 @@ hipError_t launch(Int8RowArgs a, hipStream_t stream) {
     if (a.h > 1024 && lds < all) lds = all;
   }
   a.lds_row = lds;
-  lds += 32;
+  lds += 16 * 8;
   // as many workgroups as are resident (five waves to a SIMD, by their registers:
   // 51.0 us with the product, 52.8 with 24 waves to a unit), so that the offsets are read
   // once for many rows; unrotated rows have none to keep
-  const long long cap = ROT ? (long long)kUnits * (nr == 1 ? 20 / waves : 4) : a.rows;
+  const long long cap = ROT ? (long long)kUnits * (20 / waves) : a.rows;
   const dim3 grid((unsigned)(a.rows < cap ? a.rows : cap)), block(64 * waves);
-  hipError_t e = hipSuccess;
-  auto go = [&](auto n) {
-    auto kern = rows_kernel<IT, ROT, decltype(n)::value>;
-    static LaunchCache cache;
-    e = prepare_launch(cache, (const void*)kern, 256, lds, nullptr);
-    if (e != hipSuccess) return;
-    kern<<<grid, block, lds, stream>>>(a);
-    e = hipGetLastError();
-  };
-  if (nr == 1) go(std::integral_constant<int, 1>{});
-  else if (nr == 2) go(std::integral_constant<int, 2>{});
-  else if (nr == 3) go(std::integral_constant<int, 3>{});
-  else go(std::integral_constant<int, 4>{});
-  return e;
+  auto kern = rows_kernel<IT, ROT>;
+  static LaunchCache cache;
+  const hipError_t e = prepare_launch(cache, (const void*)kern, 64 * waves, lds, nullptr);
+  if (e != hipSuccess) return e;
+  kern<<<grid, block, lds, stream>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace

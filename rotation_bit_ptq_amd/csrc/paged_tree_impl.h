@@ -526,7 +526,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     asm volatile("" ::: "memory");
   };
 
-  // Queries.  kWide: read by whole rows (8192 cycles of a prompt's workgroup
+  // Queries.  kWide: read by whole rows (7500 cycles of a prompt's workgroup
   // went into reading them as operands, 32 bytes of 32 rows at a time) and
   // brought into the operands' order in LDS, in stages that no load is on its
   // way to yet: behind the tiles in flight, or (INT8) where codes will be

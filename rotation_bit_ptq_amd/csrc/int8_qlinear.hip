@@ -137,9 +137,10 @@ struct Finish {
 
 // The loads that go from memory straight to LDS are inline assembly with
 // explicit waits: they have no register results, and the compiler would wait
-// for every one of them before each LDS read.
+// for every one of them before each LDS read.  gfx9 asks for a wait state
+// between the write of m0 and the load, which is the block's own to keep.
 __device__ __forceinline__ void load_lds(uint32_t to, uint32_t offset, const char* base) {  // 1 KB: lane l's 16 bytes to `to` + 16 l
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {  // until at most N loads of this wave are in flight, and no LDS read

@@ -253,14 +253,16 @@ alignas(16) static __device__ const uint32_t kTreeZeros[4] = {0, 0, 0, 0};  // w
 
 // 16 (4) bytes a lane from memory to LDS at `to`, in lane order.  Inline, with
 // explicit waits: the compiler would wait for all of them before each LDS read.
+// Between the write of m0 and the load stands the wait state that gfx9 asks
+// for, which the compiler does not add inside an inline block.
 __device__ __forceinline__ void tree_load16(uint32_t to, const char* from) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
 }
 __device__ __forceinline__ void load_lds16(uint32_t to, uint32_t offset, const char* base) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
 }
 __device__ __forceinline__ void tree_load4(uint32_t to, const char* from) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void tree_wait() {  // until at most N of this wave's loads are in flight, and no LDS access

@@ -765,20 +765,21 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(GemmArgs g) {
       gs = (uint32_t)n * (uint32_t)g.groups_per_row;
     }
     // loads chunk c (clamped to the last chunk) into the stage of chunk cs
+    // (a wait state stands between m0 and the load that reads it)
     auto issue = [&](int cs, int c) {
       c = c < last ? c : last;
       const uint32_t st = (uint32_t)(cs % 3) * kStage;
 #pragma unroll
       for (int q = 0; q < kALoads; ++q)
-        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                      :: "s"(st + (q * 4 + wv) * 1024u), "v"(ga[q] + (uint32_t)c * (kCK * 2)), "s"(g.a)
                      : "memory", "m0");
 #pragma unroll
       for (int q = 0; q < kBLoads; ++q)
-        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                      :: "s"(st + kABytes + (q * 4 + wv) * 1024u), "v"(gb[q] + (uint32_t)c * kBRow), "s"(g.b)
                      : "memory", "m0");
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2"
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                    :: "s"(st + kABytes + kBBytes + wv * 256u), "v"(((gs + (uint32_t)(c >> 1)) & ~1u) * 2u),
                       "s"(g.scale_f16)
                    : "memory", "m0");

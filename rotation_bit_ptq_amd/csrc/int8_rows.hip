@@ -2,9 +2,9 @@
 // on the way:
 //   x' = Pi x (or x),  s = max|x'| / 127,  q = rint(x' * 127 / max|x'|).
 //
-// Bound: memory, one pass: a row stays in registers between the rotation,
-// its maximum and its codes.  4096 bf16 rows of 3072, blocks of 128: 14.5 us
-// (2.6 TB/s), two thirds of it vector instructions; 16 such rows 4.5 us.
+// Bound: vector instructions, in one pass over memory: a row stays in registers
+// between the rotation, its maximum and its codes.  4096 bf16 rows of 3072,
+// blocks of 128: 16.5 us (2.3 TB/s); 16 such rows 4.5 us.
 //
 // A workgroup takes a row at a time, a wave of it 1024 coordinates: lane l
 // holds coordinates 16 l .. 16 l + 15 of those, so that four of the Hadamard's
@@ -12,17 +12,17 @@
 // words.  Blocks of 2048 and 4096 take their last two stages between the
 // waves, through LDS.  The gather goes through an LDS copy of the row; its
 // offsets (with the signs) are kept in registers for all rows of a workgroup.
-// Rows of 4352 (9164, fp16) take 53 us, and took 69 by four waves in rounds; of
-// 6336 (13404, fp16) 82 and 100, of 12288 (4096, bf16) 58 and 54, of 16384
-// (2048, float32) 58 and 86.
+// Rows of 4352 (9164, fp16) take 66 us, of 6336 (13404, fp16) 122, of 12288
+// (4096, bf16) 83, of 16384 (2048, float32) 62.
+//
+// Rows of every type are rotated in float64.  In float32 the sums of 16-bit
+// values are not exact either (terms some 2^9 below a block's largest lose
+// bits), which moved some 10^-6 of the codes across a half, and finite bfloat16
+// rows left its range; it took 14 us for the 4096 rows above.
 //
 // Codes: t = fma(x', 127 / max, 1.5 * 2^52) in float64 holds the rounded
 // integer in its low byte (half to even; |x'| <= max, so there is nothing to
-// clamp).  In float32 the factor's rounding moves x' up to 4e-6 of a step, and
-// a code falls to the wrong side once in some 10^5.  For the same reason
-// float32 rows are rotated in float64; 16-bit rows have 11 bits or fewer of
-// each of the terms, which float32's 24 bits hold without loss but for those
-// some 2^9 times below the block's largest.
+// clamp).
 // A row with an infinity or a NaN takes s = NaN and codes 0, so that all that
 // is made of it is NaN.
 #include "block_common.h"
@@ -41,34 +41,21 @@ __device__ __forceinline__ int lane_xor(int b) {
 }
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 template <int M>
-__device__ __forceinline__ float lane_xor(float v) {
-  return __builtin_bit_cast(float, lane_xor<M>(__builtin_bit_cast(int, v)));
-}
-template <int M>
 __device__ __forceinline__ double lane_xor(double v) {
   const i32x2 b = __builtin_bit_cast(i32x2, v);
   return __builtin_bit_cast(double, i32x2{lane_xor<M>(b.x), lane_xor<M>(b.y)});
 }
 // with the sign bit flipped where `sign` is 2^31
 __device__ __forceinline__ float flipped(float v, uint32_t sign) { return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) ^ sign); }
-__device__ __forceinline__ double flipped(double v, uint32_t sign) {
-  i32x2 b = __builtin_bit_cast(i32x2, v);
-  b.y ^= (int)sign;
-  return __builtin_bit_cast(double, b);
-}
-template <int M, class A>
-__device__ __forceinline__ void butterfly(A (&f)[16], int lane) {
-  const uint32_t sign = lane & M ? 0x80000000u : 0u;  // the upper one's own is subtracted
+// Between lanes the upper one of a pair, whose result is the other's less its own, takes its own less the other's: one
+// product and sum in place.  A lane's coordinates are then negated where it was an upper one an odd number of times.
+template <int M>
+__device__ __forceinline__ void butterfly(double (&f)[16], int lane) {
+  const double sign = lane & M ? -1.0 : 1.0;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) f[j] = lane_xor<M>(f[j]) + flipped(f[j], sign);
+  for (int j = 0; j < 16; ++j) f[j] = __builtin_fma(lane_xor<M>(f[j]), sign, f[j]);
 }
 // of lane l % 32 and of lane 32 + l % 32
-__device__ __forceinline__ void halves(float v, float& lo, float& hi) {
-  const unsigned u = __builtin_bit_cast(unsigned, v);
-  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  lo = __builtin_bit_cast(float, (unsigned)r[0]);
-  hi = __builtin_bit_cast(float, (unsigned)r[1]);
-}
 __device__ __forceinline__ void halves(double v, double& lo, double& hi) {
   const i32x2 b = __builtin_bit_cast(i32x2, v);
   const auto x = __builtin_amdgcn_permlane32_swap((unsigned)b.x, (unsigned)b.x, false, false);
@@ -76,13 +63,12 @@ __device__ __forceinline__ void halves(double v, double& lo, double& hi) {
   lo = __builtin_bit_cast(double, i32x2{(int)x[0], (int)y[0]});
   hi = __builtin_bit_cast(double, i32x2{(int)x[1], (int)y[1]});
 }
-template <class A>
-__device__ __forceinline__ void butterfly32(A (&f)[16], int lane) {
+__device__ __forceinline__ void butterfly32(double (&f)[16], int lane) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    A lo, hi;
+    double lo, hi;
     halves(f[j], lo, hi);
-    f[j] = lane & 32 ? lo - hi : lo + hi;
+    f[j] = lane & 32 ? hi - lo : lo + hi;
   }
 }
 
@@ -101,18 +87,20 @@ __device__ __forceinline__ void meet() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// What rows are rotated in.
-template <class IT, bool ROT>
-using Sum = std::conditional_t<ROT && std::is_same_v<IT, float>, double, float>;
+// What rows are rotated in: 64 bits hold a block's sums without loss (fp16, and bfloat16 values
+// within 2^33 of each other in blocks of 4096) and without leaving their range.
+template <bool ROT>
+using Sum = std::conditional_t<ROT, double, float>;
 
 // A wave for each 1024 coordinates of a row, up to 16.
 template <class IT, bool ROT>
-__global__ __launch_bounds__(1024, (std::is_same_v<Sum<IT, ROT>, double> ? 4 : 5)) void rows_kernel(Int8RowArgs a) {
+__global__ __launch_bounds__(1024, 5) void rows_kernel(Int8RowArgs a) {
   extern __shared__ __align__(16) char smem[];
-  typedef Sum<IT, ROT> A;
+  typedef Sum<ROT> A;
   typedef decltype(size_of(A())) Size;
   Size* const top = (Size*)(smem + a.lds_row);  // the waves' maxima, behind the row's copy
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, waves = (int)blockDim.x >> 6;
+  const bool negated = ROT && __popc(lane & ((a.h >> 4) - 1)) & 1;  // see butterfly
   // where each coordinate comes from (times two, in 15 bits), bit 15: with its sign flipped
   uint32_t from[8];
   if constexpr (ROT) {
@@ -132,6 +120,8 @@ __global__ __launch_bounds__(1024, (std::is_same_v<Sum<IT, ROT>, double> ? 4 : 5
     A f[16];
     if constexpr (ROT) {
       IT* const copy = (IT*)smem;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(from[j]));  // what is made of them is not kept in registers
       if (a.vec) {
         for (int i = t * 8; i < a.d; i += (int)blockDim.x * 8) *(Vec8<IT>*)(copy + i) = *(const Vec8<IT>*)(x + i);
       } else {
@@ -195,10 +185,18 @@ __global__ __launch_bounds__(1024, (std::is_same_v<Sum<IT, ROT>, double> ? 4 : 5
         }
       }
     }
+    if constexpr (ROT) {
+      // an infinity or a NaN makes each coordinate of its block one, a lane's first among them
+      double most = 0.0;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const Size b = size_of(f[j]);
-      m = b > m ? b : m;
+      for (int j = 0; j < 16; ++j) most = __builtin_fmax(most, __builtin_fabs(f[j]));
+      m = size_of(f[0] - f[0] == 0.0 ? most : __builtin_inf());
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const Size b = size_of(f[j]);
+        m = b > m ? b : m;
+      }
     }
     if (wave * 1024 + lane * 16 >= a.d) m = 0;
 #pragma unroll
@@ -216,7 +214,7 @@ __global__ __launch_bounds__(1024, (std::is_same_v<Sum<IT, ROT>, double> ? 4 : 5
     const bool fine = most < __builtin_inf();
     const float scale = fine ? (float)(most * a.inv_sqrt_h / 127.0) : __builtin_nanf("");
     if (t == 0) a.s_out[row] = scale;
-    const double inv = scale > 0.0f ? 127.0 / most : 0.0;
+    const double inv = scale > 0.0f ? (ROT && negated ? -127.0 : 127.0) / most : 0.0;
     const uint32_t keep = fine ? 0xffffffffu : 0u;
     const int k0 = wave * 1024 + lane * 16;
     uint32_t w[4];
@@ -239,7 +237,7 @@ hipError_t launch(Int8RowArgs a, hipStream_t stream) {
   int lds = 0;
   if (ROT) {
     lds = a.d * (int)sizeof(IT);
-    const int all = waves * 1024 * (int)sizeof(Sum<IT, ROT>);
+    const int all = waves * 1024 * (int)sizeof(double);
     if (a.h > 1024 && lds < all) lds = all;
   }
   a.lds_row = lds;

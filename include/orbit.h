@@ -300,7 +300,9 @@ orbit_status orbit_int4_linear(const void *Xrot, orbit_dtype xrot_dtype, int64_t
  * and, offline, the weights of orbit_int8_qlinear (rotate, then quantize, as
  * orbit_int8_pack_weights, with the whole row as the group):
  *   x' = Pi x (x itself: rot NULL), s = max|x'| / 127,
- *   q = round_half_even(x' * (127 / max|x'|)), Pi x too in float64.
+ *   q = 127 x' / max|x'| rounded to the nearest integer, a tie (and what lies
+ *   within 2^-45 of one) to the even one.
+ * Pi x is summed in float64, and its factor 1 / sqrt(h) plays no part in q.
  * A row of zeros gives s = 0 and codes 0; a row with an infinity or a NaN
  * gives s = NaN and codes 0.  Because W x = (W Pi^T)(Pi x), tokens and
  * weights coded with the same rotation multiply to the layer's product.

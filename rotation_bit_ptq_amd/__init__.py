@@ -367,8 +367,9 @@ _binding = _load_binding()
 def int8_quant_rows(rot, X: torch.Tensor):
     """Rows in 8 bits with a scale each, rotated on the way (rot None: not):
 
-        x' = Pi x,  s = max|x'| / 127,  q = round(x' * (127 / max|x'|))
+        x' = Pi x,  s = max|x'| / 127,  q = round(127 x' / max|x'|)
 
+    (to the nearest integer, a tie to the even one; Pi x in float64).
     X: [M, K] float32, bfloat16 or float16, rows of any stride.  Returns
     (q int8 [M, K], s float32 [M]): online the tokens of int8_qlinear, offline
     its weights, a scale for each output channel (rotated alike, since W x =

@@ -4,7 +4,7 @@
 //
 // Bound: vector instructions, in one pass over memory: a row stays in registers
 // between the rotation, its maximum and its codes.  4096 bf16 rows of 3072,
-// blocks of 128: 16.5 us (2.3 TB/s); 16 such rows 4.5 us.
+// blocks of 128: 17 us (2.2 TB/s); 16 such rows 4.6 us; not rotated 9.6 us.
 //
 // A workgroup takes a row at a time, a wave of it 1024 coordinates: lane l
 // holds coordinates 16 l .. 16 l + 15 of those, so that four of the Hadamard's
@@ -12,17 +12,19 @@
 // words.  Blocks of 2048 and 4096 take their last two stages between the
 // waves, through LDS.  The gather goes through an LDS copy of the row; its
 // offsets (with the signs) are kept in registers for all rows of a workgroup.
-// Rows of 4352 (9164, fp16) take 66 us, of 6336 (13404, fp16) 122, of 12288
-// (4096, bf16) 83, of 16384 (2048, float32) 62.
+// Rows of 4352 (9164, fp16) take 67 us, of 6336 (13404, fp16) 124, of 12288
+// (4096, bf16) 83, of 16384 (2048, float32) 63.
 //
 // Rows of every type are rotated in float64.  In float32 the sums of 16-bit
 // values are not exact either (terms some 2^9 below a block's largest lose
 // bits), which moved some 10^-6 of the codes across a half, and finite bfloat16
 // rows left its range; it took 14 us for the 4096 rows above.
 //
-// Codes: t = fma(x', 127 / max, 1.5 * 2^52) in float64 holds the rounded
-// integer in its low byte (half to even; |x'| <= max, so there is nothing to
-// clamp).
+// Codes: t = fma(x', 127 / max, 1.5 * 2^8) in float64 is 127 x' / max to 44
+// bits behind the point, t + 1.5 * 2^52 - 1.5 * 2^8 holds that, rounded half to
+// even, in its low byte (|x'| <= max, so there is nothing to clamp).  16-bit rows
+// have ties (one of 10^4 codes of unrotated bf16 rows); the factor's rounding,
+// 2^-46 here, would decide them, and is gone with what lies behind 44 bits.
 // A row with an infinity or a NaN takes s = NaN and codes 0, so that all that
 // is made of it is NaN.
 #include "block_common.h"
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(1024, 5) void rows_kernel(Int8RowArgs a) {
     for (int j = 0; j < 4; ++j) {
       uint32_t b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma((double)f[4 * j + i], inv, 6755399441055744.0));
+      for (int i = 0; i < 4; ++i) b[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma((double)f[4 * j + i], inv, 384.0) + (6755399441055744.0 - 384.0));
       const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
       w[j] = (lo | hi) & keep;
     }

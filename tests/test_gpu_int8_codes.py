@@ -72,3 +72,53 @@ def test_rows_near_the_largest_value(gpu_lib, d, h, dtype):
     x[2] = 2.0 ** 127
     x[3:] *= 31 * torch.rand(3, d, generator=g, device="cuda")
     coded(gpu_lib, x.to(DTYPES[dtype]), h)
+
+
+def halves(d, dtype, seed):
+    """Rows whose largest is b, with values (k + 1/2) b / 127 in every place where the type holds them, and their neighbours."""
+    g = torch.Generator().manual_seed(seed)
+    t = DTYPES[dtype]
+    out = []
+    for b in (127.0, 254.0, 1.0, 2.0, 127.0 * 2 ** -20, 63.5, 508.0, 100.0):
+        k = torch.randint(-127, 127, (d,), generator=g).double()
+        v = ((k + 0.5) * b / 127).to(t)
+        step = torch.where(torch.rand(d, generator=g) < 0.3, 1, 0) * torch.where(torch.rand(d, generator=g) < 0.5, -1, 1)
+        v = (v.view(torch.int32 if dtype == "f32" else torch.int16) + step.to(torch.int32 if dtype == "f32" else torch.int16)).view(t)
+        v = torch.where(v.abs() > b, torch.zeros_like(v), v)
+        v[torch.randint(0, d, (1,), generator=g)] = b
+        out.append(v)
+    return torch.stack(out).cuda()
+
+
+# 127 x of a value of 24 bits or fewer is exact in float64, and its quotient by the maximum rounded once: a tie stays one, and
+# no other value becomes one (two values of 24 bits whose quotient is no tie are 2^-33 away at least)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("d", [16, 240, 1024, 1040, 4096, 16384])
+def test_ties_go_to_the_even_code(gpu_lib, d, dtype):
+    x = halves(d, dtype, d)
+    coded(gpu_lib, x, 0, near=0)
+    coded(gpu_lib, -x, 0, near=0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_every_code_of_rows_that_are_not_rotated(gpu_lib, dtype):
+    x = rows(4000, 2512, dtype, 7)
+    assert coded(gpu_lib, x, 0, near=0) > 0
+
+
+# blocks of one value (and zeros) rotate to that value times +-1 everywhere: a block of half the largest is a tie
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("d,h", [(256, 16), (256, 64), (1024, 128), (2048, 256), (2048, 1024), (4096, 2048)])
+def test_ties_of_rotated_rows(gpu_lib, d, h, dtype):
+    perm, signs = synth.rotation_params(d, seed=d + h)
+    blocks = torch.zeros(12, d // h, h)
+    size = [3.0, 3.25, 5.0, 7.0, 9.5, 11.0, 13.0, 15.0, 17.0, 19.0, 21.0, 23.0]  # 127 / size is rounded either way
+    g = torch.Generator().manual_seed(h)
+    for r in range(12):
+        for b in range(d // h):
+            blocks[r, b, torch.randint(0, h, (1,), generator=g)] = float([1.0, 0.5, -0.5, 63.5 / 127, 1.5, -2.0][(r + b) % 6]) * size[r]
+    blocks[:, 0] = 0
+    blocks[:, 0, 5] = 2 * torch.tensor(size)
+    x = torch.zeros(12, d)
+    x[:, torch.from_numpy(perm).long()] = blocks.reshape(12, d)  # the gather brings them back
+    coded(gpu_lib, x.to(DTYPES[dtype]).cuda(), h, near=0)

@@ -330,7 +330,15 @@ def _plain_product(s, c):
 
 
 def _plain_layer(s, c):
-    qx, sx = _coded(_rotated(s["x"].float(), s, c))
+    # a code next to a half is decided in 64 bits, and without the rotation's factor, so that a tie stays one: in 32 bits
+    # some 1e-6 of the codes fall to the other side, which moves a float32 output by 3e-5 of its norm
+    x, h = s["x"].double(), c["h"] or 1
+    if c["h"]:
+        ones = (_hadamard(h, torch.float64) * h ** 0.5).round()
+        x = ((x[:, s["perm"]] * s["signs"].double()).reshape(-1, h) @ ones).reshape(x.shape)
+    top = x.abs().amax(-1, keepdim=True)
+    qx = torch.where(top > 0, torch.round(127 * x / top), 0.0)
+    sx = (top[:, 0] / (127 * h ** 0.5)).float()
     return _finished((qx.float() @ s["qw"].float().t()) * sx[:, None] * s["sw"], s, c)
 
 
@@ -421,13 +429,13 @@ def exact(case, seed):
 
 
 def _fwht(x, h):
-    """Blocks of h of the last axis, a factor of two at a time."""
+    """Blocks of h of the last axis, a factor of two at a time; without the factor 1 / sqrt(h)."""
     shape, n = x.shape, 1
     while n < h:
         x = x.reshape(-1, 2, n)
         x = torch.stack([x[:, 0] + x[:, 1], x[:, 0] - x[:, 1]], 1)
         n *= 2
-    return x.reshape(shape) / math.sqrt(h)
+    return x.reshape(shape)
 
 
 def _exact_product(s, c):
@@ -445,9 +453,9 @@ def _exact_layer(s, c):
     x = s["x"].double()
     if c["h"]:
         x = _fwht(x.index_select(1, s["perm"]).mul_(s["signs"].double()), c["h"])
-    step = x.abs().max(1).values / 127
-    q = (x / step.clamp_min(1e-300).unsqueeze(1)).round_().clamp_(-127, 127)
-    return _exact_product(dict(s, qx=q, sx=step), c)
+    most = x.abs().max(1).values
+    q = (x * 127 / most.clamp_min(1e-300).unsqueeze(1)).round_()
+    return _exact_product(dict(s, qx=q, sx=most / 127 / math.sqrt(c["h"] or 1)), c)
 
 
 def _exact_heads(s, c):
@@ -473,7 +481,7 @@ def _exact_heads(s, c):
         full = [torch.zeros(s["k_cache"].shape, dtype=torch.float64, device="cuda") for _ in "kv"]
         full[0][pg, :, at], full[1][pg, :, at] = k, v
         return q, *full
-    q, k = _fwht(q, D), _fwht(k, D)
+    q, k = _fwht(q, D) / math.sqrt(D), _fwht(k, D) / math.sqrt(D)
     values, scales = [], []
     for x in (k, v):
         sc = (x.abs().max(-1).values / 127).float().half()

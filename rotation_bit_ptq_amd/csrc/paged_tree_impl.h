@@ -564,7 +564,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
       bad |= (uint32_t)table[x] >= a.c.pages;
   // as the B operand
   V8 qf[kSteps];
-  float zscale = fmaxf(fabsf(a.scale_log2e), 1.17549435e-38f);  // not 0: a hidden score is minus infinity
+  float zscale = fabsf(a.scale_log2e);
   {
     if constexpr (kWide) {
       char* const mine = lds + (kCoded ? wave * R * DP * 2 : wave / 4 * kValuesAt + (k0 + 2 + wave / 2 % 2) % S * kTileBytes + wave % 2 * R * DP * 2);
@@ -595,6 +595,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[s][j] = f[s][j] * down * down2;
     }
+    zscale = fmaxf(zscale, 1.17549435e-38f);  // not 0: a hidden score is minus infinity
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
 #pragma unroll

@@ -557,11 +557,17 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     const int t = tile_at(k0 + lane) + wave * kRows;
     if (t < hi_all) first_pages = (uint32_t)table[t >> a.c.page_shift];
   }
-  // whether any page of the piece lies outside the cache
+  // whether any page that the piece's rows see lies outside the cache.  Pages
+  // between the sinks and the window are not looked at: a server gives them up,
+  // and a part of a tile that no row sees is masked anyway.
   bool bad = false;
-  if (k0 < k1)
-    for (int x = (tile_at(k0) >> a.c.page_shift) + tid; x <= (min(tile_at(k1 - 1) + kTokens, hi_all) - 1) >> a.c.page_shift; x += 64 * kTreeWaves)
-      bad |= (uint32_t)table[x] >= a.c.pages;
+  auto look = [&](int from, int to) {  // tokens
+    if (from < to)
+      for (int x = (from >> a.c.page_shift) + tid; x <= (to - 1) >> a.c.page_shift; x += 64 * kTreeWaves)
+        bad |= (uint32_t)table[x] >= a.c.pages;
+  };
+  if (k0 < sink_tiles) look(tile_at(k0), min(min(k1, sink_tiles) * kTokens, min(a.sinks, hi_all)));
+  if (k1 > sink_tiles) look(max(tile_at(max(k0, sink_tiles)), lo_all), min(tile_at(k1 - 1) + kTokens, hi_all));
   // as the B operand
   V8 qf[kSteps];
   float zscale = fabsf(a.scale_log2e);

@@ -608,11 +608,12 @@ int64_t orbit_paged_attention_workspace(int64_t batch, int64_t q_heads, int64_t 
  * starts must not decrease (which rows are written is otherwise unspecified),
  * and is cut to 0 .. tokens.  Rows with nothing to see, cut lengths, table
  * entries outside the cache and head groups as in orbit_paged_attention.  A
- * weight above its sum is a pair of 16-bit numbers as there where requests
- * have at most 32 rows (new tokens times q_heads / kv_heads) on average, and
- * one 16-bit number, rounded to nearest, where they have more: within 2^-8 of
- * the weight (BF16), or 2^-11 (F16, and beside an int8 cache).  The sums below
- * and lse are of float32 weights in either case.
+ * weight above its sum is a pair of 16-bit numbers as there for a request of at
+ * most 32 rows (new tokens times q_heads / kv_heads), whatever it is batched
+ * with, and for all where they have at most 32 on average; for others it is one
+ * 16-bit number, rounded to nearest: within 2^-8 of the weight (BF16), or 2^-11
+ * (F16, and beside an int8 cache).  The sums below and lse are of float32
+ * weights in either case.
  * q: [tokens, q_heads, head_dim] by strides, rows 16-byte aligned, BF16 or
  * F16; its type is the cache's, either one for an int8 cache.  out: [tokens,
  * q_heads, head_dim] contiguous, of q's type, 16-byte aligned.  lse: float

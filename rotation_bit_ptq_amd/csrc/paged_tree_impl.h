@@ -22,9 +22,11 @@
 // R = 16, where a request has at most 32 rows on average: 16x16x32 products,
 // probabilities as pairs of 16-bit numbers as in the single-token kernel
 // (paged_attention_impl.h).  Those are bound by memory.  R = 32: 32x32x16
-// products and single 16-bit probabilities, half the instructions around a
-// score; from 128 rows on the instructions bound them.  A probability's
-// rounding is relative (within 2^-8 of it in bfloat16), as its value's was.
+// products, half the instructions around a score; from 128 rows on the
+// instructions bound them.  Probabilities are pairs for requests of at most 32
+// rows there too, and one 16-bit number for larger ones, as pairs double their
+// products (4096 new of 8192 tokens 627 us, trees below 125): that rounding is
+// relative (within 2^-8 of each in bfloat16), as its value's was.
 //
 // What bounds it, 4096 new of 8192 tokens, 32 + 8 heads of 128, 440 us (937
 // TFLOP/s): vector instructions share a SIMD's issue with matrix ones, four or
@@ -279,7 +281,8 @@ __device__ __forceinline__ f32x16 tree_mma(bf16x8 a, bf16x8 b, f32x16 c) { retur
 __device__ __forceinline__ f32x16 tree_mma(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 
 // Q: the queries' format; F: the cache's; DP: head_dim rounded up to 64, 128
-// or 256; R: rows of a wave, 16 or 32; PAIR: weights as two 16-bit numbers.
+// or 256; R: rows of a wave, 16 or 32; PAIR: weights of every request, and not of
+// those with at most 32 rows alone, as two 16-bit numbers.
 //
 // The lanes.  G = 64 / R lanes hold a row; lane l is number g = l / R of row l
 // % R and holds, of 32 tokens' scores, tokens 4 G q + 4 g + i (i < 4), and of a
@@ -638,14 +641,14 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
 
   // The operands' places: `lds` is at LDS's beginning, and its address would be added to each.
   typedef const __attribute__((address_space(3))) u32x4* lds_16;
-  V8 ph[kScores / 8], pl[PAIR ? kScores / 8 : 1];
+  V8 ph[kScores / 8], pl[kScores / 8];
   // Scores of 32 tokens (SCORES), and weights of the pending ones (WEIGHTS), a
   // part of both at a time: the weights' instructions stand between the keys'
   // reads and their products.
   // CHECKED: values' scales of hidden tokens may be infinite or NaN.
   // Scores z of the 32 tokens whose keys lie `skip` behind the place that
   // `keys` says, weights of s.
-  auto advance_as = [&](float (&z)[kScores], const float (&s)[kScores], int keys, auto skip, auto with_scores, auto with_weights, auto checked) {
+  auto advance_as = [&](float (&z)[kScores], const float (&s)[kScores], int keys, auto skip, auto with_scores, auto with_weights, auto in_pairs, auto checked) {
     constexpr bool SCORES = decltype(with_scores)::value, WEIGHTS = decltype(with_weights)::value, CHECKED = decltype(checked)::value;
     constexpr int kPairs2 = kScores / 2;  // weights, two by two
     const float m_use = m_run == -__builtin_inff() ? 0.0f : m_run - kLift;
@@ -684,7 +687,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
 #pragma unroll
             for (int y = 0; y < 2; ++y) p[y] = !CHECKED || (pend_seen >> bit_of(j + y)) & 1u ? p[y] * vt[j + y] : 0.0f;
           }
-          if constexpr (PAIR) {
+          if constexpr (decltype(in_pairs)::value) {
             split2(p[0], p[1], ph[j / 8], pl[j / 8], j % 8);
           } else {
             ph[j / 8][j % 8] = (T)p[0];
@@ -703,13 +706,13 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
       for (int j = 0; j < kScores; ++j) z[j] = acc[kWide ? 0 : j / 4][kWide ? j : j % 4];
     }
   };
-  auto advance = [&](float (&z)[kScores], const float (&s)[kScores], int keys, auto skip, auto with_scores, auto with_weights) {
-    if (kCoded && decltype(with_weights)::value && pend_odd) advance_as(z, s, keys, skip, with_scores, with_weights, std::true_type{});
-    else advance_as(z, s, keys, skip, with_scores, with_weights, std::false_type{});
+  auto advance = [&](float (&z)[kScores], const float (&s)[kScores], int keys, auto skip, auto with_scores, auto with_weights, auto in_pairs) {
+    if (kCoded && decltype(with_weights)::value && pend_odd) advance_as(z, s, keys, skip, with_scores, with_weights, in_pairs, std::true_type{});
+    else advance_as(z, s, keys, skip, with_scores, with_weights, in_pairs, std::false_type{});
   };
   // The pending tokens' weights with their values, by blocks of R coordinates
   // (and 16 tokens: kWide); some products' operands are read ahead.
-  auto products = [&] {
+  auto products = [&](auto in_pairs) {
     typedef __attribute__((address_space(3))) s16x4* lds_ptr;
     constexpr int kAll = kBlocks * (kWide ? 2 : 1);
     // rows 8 (kWide) or 16 further: this far, with the units' places exchanged
@@ -733,7 +736,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
       if (n + kAheadV < kAll) read(n + kAheadV);
       const int d = kWide ? n >> 1 : n, m = kWide ? n & 1 : 0;
       o[d] = tree_mma(u[n % (kAheadV + 1)].v, ph[m], o[d]);
-      if constexpr (PAIR) o[d] = tree_mma(u[n % (kAheadV + 1)].v, pl[m], o[d]);
+      if constexpr (decltype(in_pairs)::value) o[d] = tree_mma(u[n % (kAheadV + 1)].v, pl[m], o[d]);
       if (kWide || n % 2) __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -845,8 +848,8 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     }
     pend = kZerosAt;
     auto next = [&](float (&z)[kScores], const float (&was)[kScores], int k, int keys, auto skip, int sub) {
-      advance(z, was, keys, skip, std::true_type{}, std::true_type{});
-      products();
+      advance(z, was, keys, skip, std::true_type{}, std::true_type{}, std::false_type{});
+      products(std::false_type{});
       pend = values_of(k, sub);
       take(z, k, sub, tile_at(k) + sub * 32);
     };
@@ -868,26 +871,31 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
     }
     if (works) {
       float none[kScores];
-      advance(none, s, 0, First{}, std::false_type{}, std::true_type{});
-      products();
+      advance(none, s, 0, First{}, std::false_type{}, std::true_type{}, std::false_type{});
+      products(std::false_type{});
     }
   } else {
+    auto steps = [&](auto in_pairs) {
 #pragma unroll 1
-    for (int k = k0; k < k1; k += step) {
-      const int here = min(step, k1 - k);  // tiles of this step
-      begin_step(k, step, here);
-      const int n1 = works ? here * kSubs : 0;
+      for (int k = k0; k < k1; k += step) {
+        const int here = min(step, k1 - k);  // tiles of this step
+        begin_step(k, step, here);
+        const int n1 = works ? here * kSubs : 0;
 #pragma unroll 1
-      for (int n = wt; n < n1; n += wt_all) {
-        const int at = k + n / kSubs, sub = n % kSubs, ts = tile_at(at) + sub * 32;
-        if (ts >= hi_all) break;
-        advance(s, s, keys_of(at) + sub * 32 * DP * 2, First{}, std::true_type{}, std::false_type{});
-        take(s, at, sub, ts);
-        pend = values_of(at, sub);
-        advance(s, s, 0, First{}, std::false_type{}, std::true_type{});
-        products();
+        for (int n = wt; n < n1; n += wt_all) {
+          const int at = k + n / kSubs, sub = n % kSubs, ts = tile_at(at) + sub * 32;
+          if (ts >= hi_all) break;
+          advance(s, s, keys_of(at) + sub * 32 * DP * 2, First{}, std::true_type{}, std::false_type{}, in_pairs);
+          take(s, at, sub, ts);
+          pend = values_of(at, sub);
+          advance(s, s, 0, First{}, std::false_type{}, std::true_type{}, in_pairs);
+          products(in_pairs);
+        }
       }
-    }
+    };
+    // a request of few rows keeps pairs beside larger ones, too: what it is batched with does not cost it digits
+    if (PAIR || all_rows <= 32) steps(std::true_type{});
+    else steps(std::false_type{});
   }
 
   if constexpr (!kCoded) {

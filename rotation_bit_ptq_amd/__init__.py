@@ -532,7 +532,9 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, lengths, starts, *, t
     window > 0: of the tokens up to its place p (its own, in a tree that along
     its branch: base + the number of its bits - 1) those after p - window, and
     the first `sinks`; the tokens of a tree's mask are seen whatever the
-    window.  Rows outside starts[0] .. starts[batch] are left as they were.
+    window.  Table entries of pages that no token sees (between the sinks and
+    the window) may be anything.  Rows outside starts[0] .. starts[batch] are
+    left as they were.
     The rest as in paged_attention.
     """
     if starts is None:

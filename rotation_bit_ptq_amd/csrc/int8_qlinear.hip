@@ -7,8 +7,8 @@
 // Two kernels.
 // * tile_kernel, for products with enough tiles to fill the chip.  Bound: the
 //   matrix cores, and what a compute unit takes in (launch_product).  16384 x
-//   4096 -> 4096 243 us (2.3 POP/s; the library's int8 product of 8192^3 2.1),
-//   4096 x 3072 -> 3072 39 us.
+//   4096 -> 4096 243 to 262 us (2.1 to 2.3 POP/s; the library's int8 product of
+//   8192^3 2.1), 4096 x 3072 -> 3072 39 to 41 us.
 // * thin_kernel, for few tokens or few tiles.  Bound: the weights' bytes, or
 //   what a compute unit takes in.  16 x 3072 -> 18432 11 us (5.1 TB/s).
 // Everywhere the weights are the matrix instruction's A operand (rows) and

@@ -28,15 +28,16 @@
 // products (4096 new of 8192 tokens 627 us, trees below 125): that rounding is
 // relative (within 2^-8 of each in bfloat16), as its value's was.
 //
-// What bounds it, 4096 new of 8192 tokens, 32 + 8 heads of 128, 440 us (937
-// TFLOP/s): vector instructions share a SIMD's issue with matrix ones, four or
-// five cycles each of the 32 that a product takes.  32 x 32 scores cost a wave
-// 16 products, 24 LDS reads and about 100 vector instructions (a product and
+// What bounds it, 4096 new of 8192 tokens, 32 + 8 heads of 128, 420 to 443 us
+// (0.93 to 0.98 PFLOP/s): no one part.  32 x 32 scores cost a wave 16 products
+// (512 cycles), 24 LDS reads and about 100 vector instructions (a product and
 // an exponential each, half a conversion, a sum and half a maximum for each of
-// a lane's 16 scores), 1150 cycles in all; the products alone are 512.
+// a lane's 16 scores); a SIMD's matrix cores are busy 40 % of the time, its
+// vector issue 43 %, and its two waves wait 32 % of theirs: nothing sets one's
+// products against the other's weights but chance.
 // 16 trees of up to 60 drafted tokens after up to 8192 take 94 us (2.8 TB/s),
 // 8 of 16 after up to 65000 in an int8 cache 156 us (2.0 TB/s),
-// 64 single tokens behind a window of 4096 with sinks 176 us (5.4 TB/s).
+// 64 single tokens behind a window of 4096 with sinks 175 us (5.4 TB/s).
 //
 // What a row sees: prefix tokens in [lo, hi) and below `sinks`, and new tokens
 // by the bits of its mask.  A wave whose rows all see all 32 tokens skips the

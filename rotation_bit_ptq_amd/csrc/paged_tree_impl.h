@@ -570,7 +570,11 @@ __global__ __launch_bounds__(64 * kTreeWaves, R == 16 && DP == 64 ? 4 : 2) void 
       for (int x = (from >> a.c.page_shift) + tid; x <= (to - 1) >> a.c.page_shift; x += 64 * kTreeWaves)
         bad |= (uint32_t)table[x] >= a.c.pages;
   };
-  if (k0 < sink_tiles) look(tile_at(k0), min(min(k1, sink_tiles) * kTokens, min(a.sinks, hi_all)));
+  if (k0 < sink_tiles) {
+    const int from = tile_at(k0), to = min(min(k1, sink_tiles) * kTokens, hi_all);
+    look(from, min(to, a.sinks));
+    look(max(from, lo_all), to);  // a window may reach into them
+  }
   if (k1 > sink_tiles) look(max(tile_at(max(k0, sink_tiles)), lo_all), min(tile_at(k1 - 1) + kTokens, hi_all));
   // as the B operand
   V8 qf[kSteps];

@@ -53,3 +53,18 @@ def test_pages_that_are_seen_may_be_missing_beside_them(gpu_lib):
     c.table64[0, 1], c.table64[0, 3000 // 8 - 20], c.table64[1, 0], c.table64[1, 50] = -1, -7, 10 ** 6, -1
     c.table = torch.from_numpy(c.table64).cuda()
     c.check(gpu_lib)
+
+
+@pytest.mark.parametrize("xt,fmt", FORMS)
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("window,sinks", [(1000, 4), (100, 4), (60, 30), (100, 70), (333, 200)])
+def test_pages_missing_where_window_and_sinks_share_a_tile(gpu_lib, window, sinks, D, xt, fmt):
+    """Every page in its turn is missing, those that a window sees in a tile of the sinks among them."""
+    rng = np.random.default_rng(window)
+    for requests in ([(120, 2)] * 15, [(120, 70)] * 15):
+        for masks in (None, [tree_mask(rng, n) for _, n in requests]):
+            c = Case(sinks, requests, H=4, KV=2, D=D, page=8, xt=xt, fmt=fmt, window=window, sinks=sinks, masks=masks)
+            for b in range(15):
+                c.table64[b, b] = -1 - b
+            c.table = torch.from_numpy(c.table64).cuda()
+            c.check(gpu_lib)
